@@ -330,6 +330,119 @@ int a16wfp4_bmm(const void* x, int64_t sxb, int64_t sxm,
                 void* out, int64_t sob, int64_t som, int out_dtype,
                 int64_t B, int64_t M, int64_t N, int64_t K, void* stream);
 
+/*
+ * Latent attention (P3 §Motivation: the absorbed K-up and V-up products
+ * above are the two ends of attention over one shared latent vector a
+ * token).  A cached row is bf16 [576]: the normed latent (512 values, key
+ * and value of every head) and the rotated key part (64 values).  The cache
+ * is paged: page p's row i at cache[p*cache_page + i*cache_row] (ELEMENTS;
+ * multiples of 8, rows of 576 that do not overlap, 16-byte aligned), any
+ * page size >= 1.  Page numbers and lengths are int32, positions and slots
+ * int64, all on the device: they are read when the kernels run, so a
+ * captured graph follows them.
+ *
+ * mla_cache_append writes T tokens' rows.  For token t with x = kv[t]:
+ *   row[:512] = round(x[:512] / sqrt(mean(x[:512]^2) + eps) * norm_weight)
+ *   row[512:] = round(R(positions[t]) x[512:])
+ * into slot slots[t] (page slots[t] / page_size), and rotates each head's
+ * query part: q_out[t, h] = round(R(positions[t]) q_pe[t, h]).  R turns the
+ * 32 pairs (interleaved: elements 2i, 2i+1; else i, 32 + i) by the angles
+ * whose cos and sin are cos_sin[position][i] and [32 + i].  fp32 arithmetic,
+ * one rounding to bf16.
+ *
+ *   kv        bf16 [T, 576], row stride ldkv ELEMENTS (% 8, 16-byte aligned)
+ *   norm_weight  bf16 [512], 16-byte aligned;  cos_sin fp32 [max_position,
+ *             64], contiguous, 16-byte aligned
+ *   slots     a negative slot (padding), or one past the cache, writes no
+ *             row; two tokens must not share a slot
+ *   positions a position outside [0, max_position) writes nothing at all
+ *             for its token
+ *   q_pe, q_out  bf16, element (t, h, i) at t*stride + h*stride + i
+ *             (ELEMENTS, % 8, 16-byte aligned); both NULL or H = 0: keys
+ *             only.  They may be the same memory with the same strides.
+ *   T >= 0 (0 enqueues nothing).
+ */
+int mla_cache_append(const void* kv, int64_t ldkv, const void* norm_weight, float eps,
+                     const void* cos_sin, int64_t max_position, const void* positions,
+                     const void* slots, int interleaved,
+                     const void* q_pe, int64_t q_token, int64_t q_head,
+                     void* q_out, int64_t qo_token, int64_t qo_head,
+                     void* cache, int64_t pages, int64_t page_size, int64_t cache_page,
+                     int64_t cache_row, int64_t T, int64_t H, void* stream);
+
+/*
+ * Absorbed attention: S query tokens (1, or several checked together) of
+ * each of B requests over the request's cached rows, without expanding them.
+ * With n = lengths[b] rows in the cache, the S tokens' own rows the last of
+ * them, token s sees rows [0, n - S + 1 + s):
+ *   z_i = scale * (q[b,s,h] . row_i),  out[b,s,h] = round(sum_i softmax(z)_i row_i[:512]),
+ *   lse[b,s,h] = ln(sum_i exp(z_i)).
+ * A token that sees no row gives 0 and -inf.  Scores, maxima, sums and
+ * accumulators are fp32; the probabilities enter the value product rounded
+ * to bf16.  The result does not depend on timing.
+ *
+ *   q         bf16, element (b, s, h, i < 576) at b*q_batch + s*q_token +
+ *             h*q_head + i (ELEMENTS, % 8, 16-byte aligned): the absorbed
+ *             query (a16wfp4_bmm's K-up) and its rotated part
+ *   block_table  int32 [B, max_pages], row stride ldt: request b's pages in
+ *             order.  A page number outside [0, pages) hides its rows.
+ *   lengths   int32 [B], clamped to [0, max_pages * page_size]
+ *   scale     finite, > 0
+ *   out       bf16 (b, s, h, i < 512), strides as for q; rows must not overlap
+ *   lse       fp32 [B, S, H] contiguous, or NULL
+ *   workspace mla_decode_workspace_bytes bytes (max_tokens = max_pages *
+ *             page_size, prefix_len 0), 16-byte aligned; scratch of this call
+ *   B >= 0 (0 enqueues nothing), S, H >= 1, B*S*H <= 2^22,
+ *   max_pages * page_size <= 2^30.
+ *
+ * mla_decode_shared_prefix: the rows of prefix_table's pages (prefix_len of
+ * them, int32 table of prefix_pages) come before every request's own rows
+ * and are seen by all tokens; they are read once for the whole batch.  With
+ * lengths >= S the result is that of mla_decode over the joined rows.
+ * lengths counts a request's own rows only; workspace for the same prefix_len.
+ */
+size_t mla_decode_workspace_bytes(int64_t B, int64_t S, int64_t H, int64_t max_tokens,
+                                  int64_t prefix_len);
+int mla_decode(const void* q, int64_t q_batch, int64_t q_token, int64_t q_head,
+               const void* cache, int64_t pages, int64_t page_size, int64_t cache_page,
+               int64_t cache_row, const void* block_table, int64_t ldt, int64_t max_pages,
+               const void* lengths, int64_t B, int64_t S, int64_t H, float scale,
+               void* out, int64_t out_batch, int64_t out_token, int64_t out_head, void* lse,
+               void* workspace, size_t workspace_bytes, void* stream);
+int mla_decode_shared_prefix(const void* q, int64_t q_batch, int64_t q_token, int64_t q_head,
+                             const void* cache, int64_t pages, int64_t page_size,
+                             int64_t cache_page, int64_t cache_row, const void* prefix_table,
+                             int64_t prefix_pages, int64_t prefix_len, const void* block_table,
+                             int64_t ldt, int64_t max_pages, const void* lengths, int64_t B,
+                             int64_t S, int64_t H, float scale, void* out, int64_t out_batch,
+                             int64_t out_token, int64_t out_head, void* lse, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * Expanded attention of whole prompts or chunks: B sequences packed along
+ * the tokens, sequence b with queries [cu_q[b], cu_q[b+1]) and keys
+ * [cu_k[b], cu_k[b+1]).  A key of head h is k_nope[t, h] followed by k_pe[t],
+ * which all heads share.  With causal, query i of nq over nk keys sees keys
+ * [0, nk - nq + 1 + i) (the queries are the last tokens); else all nk.
+ *   out[t, h] = round(softmax(scale * q . k) v),  lse[t, h] as above.
+ * A query that sees no key gives 0 and -inf.  Arithmetic as in mla_decode.
+ *
+ *   q         bf16 [Tq, H, dn + 64], k_nope bf16 [Tk, H, dn], k_pe bf16
+ *             [Tk, 64], v bf16 [Tk, H, dv], out bf16 [Tq, H, dv]: strides of
+ *             token and head in ELEMENTS (% 8, token strides of k_nope, k_pe
+ *             and v < 2^25), 16-byte aligned; out rows must not overlap
+ *   (dn, dv)  (128, 128) or (192, 256)
+ *   cu_q, cu_k  int32 [B + 1], ascending, from 0 to Tq and Tk
+ *   lse       fp32 [Tq, H] contiguous, or NULL
+ *   Tq >= 0 and B >= 0 (0 enqueues nothing), H >= 1.
+ */
+int mla_prefill(const void* q, int64_t q_token, int64_t q_head, const void* k_nope,
+                int64_t k_token, int64_t k_head, const void* k_pe, int64_t pe_token,
+                const void* v, int64_t v_token, int64_t v_head, const void* cu_q,
+                const void* cu_k, int64_t B, int64_t H, int64_t Tq, int64_t Tk, int64_t dn,
+                int64_t dv, int causal, float scale, void* out, int64_t out_token,
+                int64_t out_head, void* lse, void* stream);
+
 #pragma GCC visibility pop
 
 #ifdef __cplusplus

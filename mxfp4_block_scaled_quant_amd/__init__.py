@@ -23,6 +23,11 @@ Entry points (same names as the C ABI):
 * :func:`mxfp4_linear_prequantized` -- the linear from row-major packed FP4 +
   scales handed over by a producer
 * :func:`a16wfp4_bmm` -- bf16 [B, M, K] x MXFP4 [B, N, K] batched GEMM
+* :func:`mla_cache_append`, :func:`mla_decode`,
+  :func:`mla_decode_shared_prefix`, :func:`mla_prefill` -- latent attention
+  between the absorbed products: cache write, attention over the paged
+  latents, with a shared prefix, and over expanded keys and values
+  (:mod:`mxfp4_block_scaled_quant_amd.mla`)
 
 Convenience: :func:`quantize_weight` (quant + preshuffle, once at load) and
 :func:`linear` (:func:`mxfp4_linear` over any leading dimensions).  The same
@@ -52,6 +57,11 @@ _c_i64 = ctypes.c_int64
 _c_vp = ctypes.c_void_p
 _c_int = ctypes.c_int
 _c_size = ctypes.c_size_t
+_c_f32 = ctypes.c_float
+
+# mla_decode's arguments from the page table on
+_MLA_REQUESTS = ([_c_vp, _c_i64, _c_i64, _c_vp] + [_c_i64] * 3 + [_c_f32, _c_vp] + [_c_i64] * 3
+                 + [_c_vp, _c_vp, _c_size, _c_vp])
 
 _SIGNATURES = {
     "mxfp4_status_str": (ctypes.c_char_p, [_c_int]),
@@ -79,6 +89,14 @@ _SIGNATURES = {
                                            _c_vp, _c_size, _c_vp]),
     "a16wfp4_bmm": (_c_int, [_c_vp, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_int,
                              _c_i64, _c_i64, _c_i64, _c_i64, _c_vp]),
+    "mla_cache_append": (_c_int, [_c_vp, _c_i64, _c_vp, _c_f32, _c_vp, _c_i64, _c_vp, _c_vp, _c_int]
+                         + [_c_vp, _c_i64, _c_i64] * 2 + [_c_vp] + [_c_i64] * 6 + [_c_vp]),
+    "mla_decode_workspace_bytes": (_c_size, [_c_i64] * 5),
+    "mla_decode": (_c_int, [_c_vp] + [_c_i64] * 3 + [_c_vp] + [_c_i64] * 4 + _MLA_REQUESTS),
+    "mla_decode_shared_prefix": (_c_int, [_c_vp] + [_c_i64] * 3 + [_c_vp] + [_c_i64] * 4
+                                 + [_c_vp, _c_i64, _c_i64] + _MLA_REQUESTS),
+    "mla_prefill": (_c_int, [_c_vp, _c_i64, _c_i64] * 2 + [_c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp]
+                    + [_c_i64] * 6 + [_c_int, _c_f32, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp]),
     "mxfp4_testing_set_gemm_path": (_c_int, [_c_int]),
 }
 
@@ -490,3 +508,7 @@ def linear(x: torch.Tensor, weight: MXFP4Weight, bias: Optional[torch.Tensor] = 
         x2 = x2.contiguous()
     y = mxfp4_linear(x2, weight.w_pre, weight.ws_pre, weight.N, bias, out_dtype)
     return y.reshape(*lead, weight.N)
+
+
+from .mla import (mla_cache_append, mla_decode, mla_decode_shared_prefix,  # noqa: E402
+                  mla_decode_workspace_bytes, mla_prefill)

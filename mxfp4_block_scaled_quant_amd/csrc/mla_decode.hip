@@ -1,0 +1,739 @@
+// Absorbed latent attention over a paged cache, for gfx950.
+//
+// A cached row is a key for every head (576 values) and, in its first 512
+// values, also the value, so a request's S tokens x H heads are S*H query
+// rows over ONE sequence of rows:
+//   z = scale q . row,  out = softmax(z) rows[:, :512],  lse = ln sum exp z.
+// Each row is read once from HBM for 2 * S*H * (576 + 512) operations: 30
+// per byte at 16 query rows (bound by HBM), 242 at 128 (near the ridge of
+// the matrix units), and a prefix that all requests share is bound by the
+// matrix units.
+//
+// Work is cut along the keys.  The list of all requests' key units (128 keys
+// for 16 and 32 query rows, 64 above) is dealt to the workgroups in equal
+// contiguous shares, computed by each workgroup from the lengths on the
+// device, so ragged batches stay balanced and a captured graph follows new
+// lengths.  A workgroup that holds a whole (request, row block) writes its
+// output; otherwise the fp32 accumulators, maxima and sums go to the
+// workspace, and a second kernel joins a row's parts in key order (results
+// do not depend on timing).
+//
+// Two forms, by the query rows of a request:
+//  * up to 32 rows (attend_split): the four waves of a workgroup take
+//    32-key tiles in turn, each with its own LDS tile, accumulators and
+//    running softmax, and meet once at the end of the share: no barrier in
+//    the loop, and four independent waves keep loads in flight.
+//  * more rows (attend_shared): the four waves share each tile (a ring of
+//    four in LDS, loaded three ahead) and take 16 or 32 query rows each.
+#include "mla_device.h"
+#include "mla_launch.h"
+
+namespace mxfp4 {
+namespace {
+
+constexpr int kTile = 32;                                  // keys per LDS tile
+constexpr uint32_t kPeOff = kTile * kLatent * 2;           // the rotated parts follow the latents
+constexpr uint32_t kTileBytes = kTile * kRowDim * 2;       // 36 KiB
+constexpr uint32_t kTabLds = 4 * kTileBytes;               // page numbers of the shared form's window
+constexpr int kTabEntries = 3584;
+constexpr uint32_t kMiscLds = kTabLds + kTabEntries * 4;   // scan and softmax exchange
+constexpr uint32_t kLdsBytes = kMiscLds + 2048;
+static_assert(kLdsBytes <= 160 * 1024, "LDS per workgroup");
+
+// What masked keys load: a key past the end or in a page the cache does not
+// have scores -inf and must add 0 * value with a finite value.
+__device__ const uint16_t zero_row[kRowDim] = {};
+
+// One list of work: `B` sequences of rows, `rows` query rows each.
+struct ListArgs {
+  DecodeArgs d;
+  const int32_t* table;
+  int64_t ldt;
+  const int32_t* lens;   // nullptr: one sequence of `fixed` rows, seen whole by the rows of every request
+  int fixed, capacity;   // lengths are clamped to the capacity of a table row
+  int B, rows, nt;       // nt row blocks per sequence
+  int grid;
+  float *part, *pml;     // parts of items that several workgroups share: [2 grid][RB][512], [..][2]
+  float *ipart, *ipml;   // parts of whole items, by query row (nullptr: write the output)
+};
+
+__device__ __forceinline__ int list_len(const ListArgs& a, int b) {
+  if (!a.lens) return a.fixed;
+  const int n = a.lens[b];
+  return n < 0 ? 0 : n > a.capacity ? a.capacity : n;
+}
+
+template <int UNIT>
+__device__ __forceinline__ int units_of(int n) { return (int)(((uint32_t)n + UNIT - 1) / UNIT); }
+
+// Sum over the workgroup's 256 threads of v before this thread's, and the
+// total, through LDS.
+__device__ __forceinline__ int scan256(int v, int& total) {
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  int x = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  lds_i32_t s = (lds_i32_t)(uintptr_t)kMiscLds;
+  if (lane == 63) s[wv] = x;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int w = s[i];
+    if (i < wv) before += w;
+    total += w;
+  }
+  __syncthreads();
+  return before + x - v;
+}
+
+// The sequence that holds unit w * total / grid of the list, the units
+// before that sequence, and this workgroup's share [lo, hi).
+template <int UNIT>
+__device__ __forceinline__ void find_share(const ListArgs& a, int w, int& b, int& base, int& lo, int& hi) {
+  const int chunk = (a.B + 255) / 256, b0 = threadIdx.x * chunk, b1 = min(a.B, b0 + chunk);
+  int sum = 0;
+  for (int i = b0; i < b1; ++i) sum += a.nt * units_of<UNIT>(list_len(a, i));
+  int total;
+  int at = scan256(sum, total);
+  const int grid = min(a.grid, total);  // workgroups with work: each has at least one unit
+  lo = hi = 0;
+  if (w < grid) {
+    lo = (int)((int64_t)w * total / grid);
+    hi = (int)((int64_t)(w + 1) * total / grid);
+  }
+  lds_i32_t s = (lds_i32_t)(uintptr_t)kMiscLds;
+  if (at <= lo && lo < at + sum) {
+    int i = b0;
+    for (;; ++i) {
+      const int u = a.nt * units_of<UNIT>(list_len(a, i));
+      if (lo < at + u) break;
+      at += u;
+    }
+    s[0] = i;
+    s[1] = at;
+  }
+  __syncthreads();
+  b = __builtin_amdgcn_readfirstlane(s[0]);
+  base = __builtin_amdgcn_readfirstlane(s[1]);
+  __syncthreads();
+}
+
+// The address of key t's row, given its page number (-1: none).
+__device__ __forceinline__ uint32_t page_of(const PagedRows& k, uint32_t t) {
+  return k.shift >= 0 ? t >> k.shift : t / (uint32_t)k.page_size;
+}
+__device__ __forceinline__ const char* row_at(const PagedRows& k, uint32_t t, int page, bool& ok) {
+  ok = (uint32_t)page < (uint32_t)k.pages;
+  const uint32_t i = t - page_of(k, t) * (uint32_t)k.page_size;
+  return ok ? k.base + page * k.page_bytes + i * k.row_bytes : (const char*)zero_row;
+}
+
+__device__ __forceinline__ const char* lane_ptr(const char* p, int lane) {
+  const uint64_t v = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), lane);
+  return (const char*)((uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ const char* shuffle_ptr(const char* p, int lane) {
+  const uint64_t v = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_ds_bpermute(lane * 4, (int)(uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_ds_bpermute(lane * 4, (int)(uint32_t)(v >> 32));
+  return (const char*)((uint64_t)hi << 32 | lo);
+}
+
+// Loads rows [r0, r0 + NR) of a tile's latents, and the rotated parts of the
+// 8 rows of each group in [g0, g0 + NG); lanes 0..31 hold the rows' addresses.
+template <int NR, int NG>
+__device__ __forceinline__ void load_rows(uint32_t tile, const char* ptr, int r0, int g0, uint32_t lane) {
+  const char* pe[NG];
+#pragma unroll
+  for (int j = 0; j < NG; ++j) pe[j] = shuffle_ptr(ptr, 8 * (g0 + j) + (int)(lane >> 3));
+#pragma unroll
+  for (int i = 0; i < NR; ++i)
+    dma16(tile + (r0 + i) * 1024, lane_ptr(ptr, r0 + i), (lane ^ bitrev4((r0 + i) & 15)) * 16);
+#pragma unroll
+  for (int j = 0; j < NG; ++j) {
+    const uint32_t row = 8 * (g0 + j) + (lane >> 3);
+    dma16_at(tile + kPeOff + (g0 + j) * 1024, pe[j] + kLatent * 2 + ((lane & 7) ^ ((row >> 1) & 7)) * 16);
+  }
+}
+
+// Accumulators and query operands of RW query rows.
+template <int RW>
+struct Rows;
+template <>
+struct Rows<16> {
+  static constexpr int kSteps = kRowDim / 32, kCols = kLatent / 16;
+  v8bf q[kSteps];
+  v4f o[kCols];
+};
+template <>
+struct Rows<32> {
+  static constexpr int kSteps = kRowDim / 16, kCols = kLatent / 32;
+  v8bf q[kSteps];
+  v16f o[kCols];
+};
+
+template <int RW>
+__device__ __forceinline__ void clear(Rows<RW>& s) {
+#pragma unroll
+  for (int i = 0; i < Rows<RW>::kCols; ++i)
+#pragma unroll
+    for (int j = 0; j < RW * RW / 64; ++j) s.o[i][j] = 0;
+}
+
+// One 32-key tile in LDS: scores, softmax step, values.  `seen` (per lane):
+// keys below it are visible to the lane's row; `bad`: bit t set if key t is
+// masked for every row; `full`: nothing is masked.
+template <int RW>
+__device__ __forceinline__ void attend_tile(uint32_t tile, Rows<RW>& st, float& m, float& l, float c, uint32_t lane,
+                                            bool full, int seen, uint32_t bad) {
+  constexpr int NX = RW / 2;
+  float x[NX];
+  if constexpr (RW == 16) {
+    const uint32_t row = lane & 15, g = lane >> 4;
+    const uint32_t ka = tile + row * 1024, kx = (g ^ bitrev4(row)) << 4;
+    const uint32_t pa = tile + kPeOff + row * 128, px = (row >> 1) & 7;
+    v4f s0 = {0, 0, 0, 0}, s1 = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 18; ++k) {
+      const uint32_t a = k < 16 ? ka + (kx ^ ((4 * (k & 3)) << 4)) + (k >> 2) * 256
+                                : pa + (((4 * (k - 16) + g) ^ px) << 4);
+      s0 = mfma_rows(lds_read16(a), st.q[k], s0);
+      s1 = mfma_rows(lds_read16(a + (k < 16 ? 16 * 1024 : 16 * 128)), st.q[k], s1);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = s0[i], x[4 + i] = s1[i];
+  } else {
+    const uint32_t row = lane & 31, h = lane >> 5;
+    const uint32_t ka = tile + row * 1024, kx = (h ^ bitrev4(row & 15)) << 4;
+    const uint32_t pa = tile + kPeOff + row * 128, px = (row >> 1) & 7;
+    v16f s = {};
+#pragma unroll
+    for (int k = 0; k < 36; ++k) {
+      const uint32_t a = k < 32 ? ka + (kx ^ ((2 * (k & 7)) << 4)) + (k >> 3) * 256
+                                : pa + (((2 * (k - 32) + h) ^ px) << 4);
+      s = mfma_rows(lds_read16(a), st.q[k], s);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = s[i];
+  }
+  if (!full) {
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+      const int t = key_of<RW>(i, lane);
+      if (t >= seen || ((bad >> t) & 1)) x[i] = kNegInf;
+    }
+  }
+  float alpha;
+  v8bf p[NX / 8];
+  if (softmax_step<RW, NX>(x, c, m, l, alpha, p)) {
+#pragma unroll
+    for (int i = 0; i < Rows<RW>::kCols; ++i)
+#pragma unroll
+      for (int j = 0; j < RW * RW / 64; ++j) st.o[i][j] *= alpha;
+  }
+  const uint32_t i16 = lane & 15;
+  if constexpr (RW == 16) {
+    const uint32_t row = 4 * (lane >> 4) + (i16 >> 2);
+    const uint32_t va = tile + row * 1024 + (i16 & 1) * 8, vx = (((i16 & 3) >> 1) ^ bitrev4(row)) << 4;
+#pragma unroll
+    for (int ct = 0; ct < 32; ++ct) {
+      const uint32_t a = va + (vx ^ (((2 * ct) & 15) << 4)) + (ct >> 3) * 256;
+      st.o[ct] = mfma_rows(join_keys(lds_read_tr(a), lds_read_tr(a + 16 * 1024)), p[0], st.o[ct]);
+    }
+  } else {
+    const uint32_t row = 4 * (lane >> 5) + (i16 >> 2);
+    const uint32_t va = tile + row * 1024 + (i16 & 1) * 8;
+    const uint32_t vx = ((2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1)) ^ bitrev4(row)) << 4;
+#pragma unroll
+    for (int ct = 0; ct < 16; ++ct) {
+      const uint32_t a = va + (vx ^ (((4 * ct) & 15) << 4)) + (ct >> 2) * 256;
+      const uint32_t e = va + 8 * 1024 + (vx ^ 16 ^ (((4 * ct) & 15) << 4)) + (ct >> 2) * 256;
+      st.o[ct] = mfma_rows(join_keys(lds_read_tr(a), lds_read_tr(e)), p[0], st.o[ct]);
+      st.o[ct] = mfma_rows(join_keys(lds_read_tr(a + 16 * 1024), lds_read_tr(e + 16 * 1024)), p[1], st.o[ct]);
+    }
+  }
+}
+
+// Query row r of sequence b: its request, token and head.
+struct RowId {
+  int b, s, h;
+};
+__device__ __forceinline__ RowId row_id(const ListArgs& a, int b, int r) {
+  if (!a.lens) {
+    const int sh = a.d.S * a.d.H;
+    b = r / sh;
+    r -= b * sh;
+  }
+  const int s = r / a.d.H;
+  return {b, s, r - s * a.d.H};
+}
+
+template <int RW>
+__device__ __forceinline__ void load_query(const ListArgs& a, const RowId& id, uint32_t lane, Rows<RW>& st) {
+  const uint16_t* q = a.d.q + id.b * a.d.sqb + id.s * a.d.sqs + id.h * a.d.sqh + 8 * (lane / RW);
+#pragma unroll
+  for (int k = 0; k < Rows<RW>::kSteps; ++k)
+    st.q[k] = __builtin_bit_cast(v8bf, *(const int4*)(q + k * (512 / RW)));
+}
+
+__device__ __forceinline__ int64_t flat_row(const DecodeArgs& d, const RowId& id) {
+  return ((int64_t)id.b * d.S + id.s) * d.H + id.h;
+}
+
+// Where a segment's rows go: the output, the part of a whole item, or part slot `slot`.
+struct Dest {
+  bool whole;
+  int slot;
+};
+
+template <int RB>
+__device__ __forceinline__ float* part_row(const ListArgs& a, const Dest& to, const RowId& id, int r_in_block) {
+  return to.whole ? a.ipart + flat_row(a.d, id) * kLatent : a.part + ((int64_t)to.slot * RB + r_in_block) * kLatent;
+}
+template <int RB>
+__device__ __forceinline__ void store_ml(const ListArgs& a, const Dest& to, const RowId& id, int r_in_block, float m,
+                                         float l) {
+  if (to.whole && !a.ipart) {
+    if (a.d.lse) a.d.lse[flat_row(a.d, id)] = l > 0 ? (m + __builtin_amdgcn_logf(l)) * kLn2 : l == 0 ? kNegInf : l;
+    return;
+  }
+  float* p = to.whole ? a.ipml + 2 * flat_row(a.d, id) : a.pml + 2 * ((int64_t)to.slot * RB + r_in_block);
+  p[0] = m;
+  p[1] = l;
+}
+
+// A share's piece of one item: tiles [t0, t1) of sequence b for row block rt.
+template <int RW>
+__device__ __forceinline__ void attend_split(const ListArgs& a, int b, int n, int rt, int t0, int t1, Dest to) {
+  const uint32_t lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t tile = wv * kTileBytes;
+  const int r0 = rt * RW;
+  const RowId id = row_id(a, b, min(r0 + (int)(lane % RW), a.rows - 1));
+  const int causal = a.lens ? n - a.d.S + 1 : n;      // keys the first token of a request sees
+  const int seen = a.lens ? causal + id.s : n;
+  const int seen_all = a.lens ? causal + r0 / a.d.H : n;
+
+  Rows<RW> st;
+  load_query<RW>(a, id, lane, st);
+  clear(st);
+  float m = kNegInf, l = 0;
+  const int32_t* table = a.table + b * a.ldt;
+  int page = -1;
+  {
+    const int t = (t0 + wv) * kTile + (int)(lane & 31);
+    if (t < n) page = table[page_of(a.d.cache, t)];
+  }
+  for (int t = t0 + wv; t < t1; t += 4) {
+    bool ok;
+    const char* ptr = row_at(a.d.cache, t * kTile + (lane & 31), page, ok);
+    const uint32_t bad = (uint32_t)__builtin_amdgcn_ballot_w64(!ok);
+    // the next tile's page numbers, ahead of this tile's rows
+    page = -1;
+    const int nx = (t + 4) * kTile + (int)(lane & 31);
+    if (t + 4 < t1 && nx < n) page = table[page_of(a.d.cache, nx)];
+    wait_lds();
+    load_rows<32, 4>(tile, ptr, 0, 0, lane);
+    wait_loads<0>();
+    attend_tile<RW>(tile, st, m, l, a.d.c, lane, bad == 0 && (t + 1) * kTile <= seen_all, seen - t * kTile, bad);
+  }
+
+  // The four waves' accumulators meet: rescaled to the rows' common maximum,
+  // through the wave's own tile, summed in wave order.
+  l = rows_sum<RW>(l);
+  lds_f32_t ml = (lds_f32_t)(uintptr_t)kMiscLds;
+  if (lane < RW) {
+    ml[(wv * RW + lane) * 2] = m;
+    ml[(wv * RW + lane) * 2 + 1] = l;
+  }
+  __syncthreads();
+  auto joined = [&](int r, float& mm, float& ll) {
+    mm = kNegInf;
+    ll = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, ml[(w * RW + r) * 2]);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float lw = ml[(w * RW + r) * 2 + 1];
+      ll += lw == 0 ? 0.0f : lw * __builtin_amdgcn_exp2f(ml[(w * RW + r) * 2] - mm);
+    }
+  };
+  float mm, ll;
+  joined(lane % RW, mm, ll);
+  const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - mm);
+  constexpr int C = RW == 16 ? 512 : 256, LD = C * 4 + 16;  // columns per pass, padded row bytes
+  constexpr int kPer = Rows<RW>::kCols * C / 512;
+#pragma unroll
+  for (int pass = 0; pass < 512 / C; ++pass) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+#pragma unroll
+      for (int j = 0; j < RW * RW / 256; ++j) {
+        const uint32_t col = i * RW + (RW == 16 ? 4 * (lane >> 4) : 8 * j + 4 * (lane >> 5));
+        v4f v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = st.o[pass * kPer + i][4 * j + e] * f;
+        *(lds_v4f_t)(uintptr_t)(tile + (lane % RW) * LD + col * 4) = v;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int it = 0; it < RW * C / 1024; ++it) {
+      const int e = it * 256 + threadIdx.x, r = e / (C / 4), col = e % (C / 4) * 4;
+      v4f v = {0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) v += *(lds_v4f_t)(uintptr_t)(w * kTileBytes + r * LD + col * 4);
+      if (r0 + r < a.rows) {
+        const RowId ri = row_id(a, b, r0 + r);
+        if (to.whole && !a.ipart) {
+          float rm, rl;
+          joined(r, rm, rl);
+          const float inv = rl == 0 ? 0.0f : 1.0f / rl;
+          const uint2 w = {pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
+          *(uint2*)(a.d.out + ri.b * a.d.sob + ri.s * a.d.sos + ri.h * a.d.soh + pass * C + col) = w;
+        } else {
+          *(v4f*)(part_row<RW>(a, to, ri, r) + pass * C + col) = v;
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x < RW && r0 + (int)threadIdx.x < a.rows)
+    store_ml<RW>(a, to, row_id(a, b, r0 + threadIdx.x), threadIdx.x, mm, ll);
+  __syncthreads();
+}
+
+template <int RW>
+__device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, int rt, int t0, int t1, Dest to) {
+  constexpr int RB = 4 * RW;
+  const uint32_t lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r0 = rt * RB + wv * RW;
+  const RowId id = row_id(a, b, min(r0 + (int)(lane % RW), a.rows - 1));
+  const int causal = a.lens ? n - a.d.S + 1 : n;
+  const int seen = a.lens ? causal + id.s : n;
+  const int seen_all = a.lens ? causal + min(r0, a.rows - 1) / a.d.H : n;
+
+  Rows<RW> st;
+  load_query<RW>(a, id, lane, st);
+  clear(st);
+  float m = kNegInf, l = 0;
+  const int32_t* table = a.table + b * a.ldt;
+  const int last_page = (int)page_of(a.d.cache, n - 1);
+  lds_i32_t tab = (lds_i32_t)(uintptr_t)kTabLds;
+  int p0 = 0, p1 = 0;  // the window of page numbers in LDS
+  auto window = [&](int t) {
+    p0 = (int)page_of(a.d.cache, t * kTile);
+    p1 = min(last_page + 1, p0 + kTabEntries);
+    for (int i = threadIdx.x; i < p1 - p0; i += 256) tab[i] = table[p0 + i];
+  };
+  auto covered = [&](int t) { return (int)page_of(a.d.cache, min(n, (t + 1) * kTile) - 1) < p1; };
+  auto issue = [&](int t, uint32_t& bad) {
+    const int key = t * kTile + (int)(lane & 31);
+    const int page = key < n ? tab[(int)page_of(a.d.cache, key) - p0] : -1;
+    bool ok;
+    const char* ptr = row_at(a.d.cache, key, page, ok);
+    bad = (uint32_t)__builtin_amdgcn_ballot_w64(!ok);
+    load_rows<8, 1>(((t - t0) & 3) * kTileBytes, ptr, wv * 8, wv, lane);
+  };
+  window(t0);
+  __syncthreads();
+  uint32_t bad0 = 0, bad1 = 0, bad2 = 0, bad3 = 0;
+  issue(t0, bad0);
+  auto ahead = [&](int t, uint32_t& bad) {  // tile t's loads, past a window's end with a new window
+    if (t >= t1) return;
+    if (!covered(t)) {
+      __syncthreads();
+      window(t);
+      __syncthreads();
+    }
+    issue(t, bad);
+  };
+  ahead(t0 + 1, bad1);
+  ahead(t0 + 2, bad2);
+  for (int t = t0; t < t1; ++t) {
+    // 9 loads a wave and tile; up to two later tiles stay in flight
+    if (t + 2 < t1) wait_loads<18>();
+    else if (t + 1 < t1) wait_loads<9>();
+    else wait_loads<0>();
+    wait_lds();
+    wave_barrier();  // tile t is whole, and tile t - 1 no longer read
+    ahead(t + 3, bad3);
+    attend_tile<RW>(((t - t0) & 3) * kTileBytes, st, m, l, a.d.c, lane, bad0 == 0 && (t + 1) * kTile <= seen_all,
+                    seen - t * kTile, bad0);
+    bad0 = bad1;
+    bad1 = bad2;
+    bad2 = bad3;
+  }
+  __syncthreads();
+
+  l = rows_sum<RW>(l);
+  const bool real = r0 + (int)(lane % RW) < a.rows;
+  if (!real) return;
+  const int r_in_block = wv * RW + lane % RW;
+  const bool direct = to.whole && !a.ipart;
+  const float inv = l == 0 ? 0.0f : 1.0f / l;
+  float* part = direct ? nullptr : part_row<RB>(a, to, id, r_in_block);
+  uint16_t* out = a.d.out + id.b * a.d.sob + id.s * a.d.sos + id.h * a.d.soh;
+#pragma unroll
+  for (int i = 0; i < Rows<RW>::kCols; ++i) {
+#pragma unroll
+    for (int j = 0; j < RW * RW / 256; ++j) {
+      const uint32_t col = i * RW + (RW == 16 ? 4 * (lane >> 4) : 8 * j + 4 * (lane >> 5));
+      v4f v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = st.o[i][4 * j + e];
+      if (direct) {
+        const uint2 w = {pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
+        *(uint2*)(out + col) = w;
+      } else {
+        *(v4f*)(part + col) = v;
+      }
+    }
+  }
+  if (lane < RW) store_ml<RB>(a, to, id, r_in_block, m, l);
+}
+
+template <int RB>
+__device__ constexpr int unit_tiles() { return RB <= 32 ? 4 : 2; }
+
+template <int RB>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void mla_attend_kernel(ListArgs a) {
+  __shared__ int4 lds_raw[kLdsBytes / 16];
+  uint32_t anchor = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int4*)lds_raw;
+  asm volatile("" : "+s"(anchor)::"memory");  // LDS is addressed by number: its array starts at 0
+
+  constexpr int kUnitTiles = unit_tiles<RB>(), kUnit = kUnitTiles * kTile;
+  const int w = blockIdx.x;
+  int b, base, lo, hi;
+  find_share<kUnit>(a, w, b, base, lo, hi);
+  for (int cur = lo; cur < hi;) {
+    const int n = __builtin_amdgcn_readfirstlane(list_len(a, b));
+    const int units = units_of<kUnit>(n);
+    if (cur - base >= units * a.nt) {  // past this sequence (or it is empty)
+      base += units * a.nt;
+      ++b;
+      continue;
+    }
+    const int rt = (cur - base) / units, u0 = (cur - base) - rt * units;
+    const int u1 = min(units, u0 + hi - cur);
+    const Dest to = {u0 == 0 && u1 == units, 2 * w + (u0 == 0)};
+    const int tiles = (int)(((uint32_t)n + kTile - 1) / kTile);
+    if constexpr (RB <= 32)
+      attend_split<RB>(a, b, n, rt, u0 * kUnitTiles, min(tiles, u1 * kUnitTiles), to);
+    else
+      attend_shared<RB / 4>(a, b, n, rt, u0 * kUnitTiles, min(tiles, u1 * kUnitTiles), to);
+    cur += u1 - u0;
+  }
+}
+
+// The parts of query row `r` of sequence b in a list: calls f(o, ml) for
+// each, in key order.  whole: one part that the list wrote by row.
+struct Parts {
+  int first, count;   // workgroups that hold pieces; count 0: none, 1: whole
+};
+template <int RB>
+__device__ __forceinline__ Parts find_parts(const ListArgs& a, int b, int r) {
+  constexpr int kUnit = unit_tiles<RB>() * kTile;
+  int before = 0, total = 0;
+  const int chunk = (a.B + 127) / 128, b0 = threadIdx.x * chunk, b1 = min(a.B, b0 + chunk);
+  for (int i = b0; i < b1; ++i) {
+    const int u = a.nt * units_of<kUnit>(list_len(a, i));
+    if (i < b) before += u;
+    total += u;
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    before += __shfl_xor(before, d);
+    total += __shfl_xor(total, d);
+  }
+  __shared__ int s[4];
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) {
+    s[(threadIdx.x >> 6) * 2] = before;
+    s[(threadIdx.x >> 6) * 2 + 1] = total;
+  }
+  __syncthreads();
+  before = s[0] + s[2];
+  total = s[1] + s[3];
+  const int units = units_of<kUnit>(list_len(a, b));
+  if (units == 0) return {0, 0};
+  const int u0 = before + r / RB * units;
+  const int grid = min(a.grid, total);
+  const int w0 = (int)((((int64_t)u0 + 1) * grid - 1) / total);
+  const int w1 = (int)((((int64_t)u0 + units) * grid - 1) / total);
+  return {w0, w1 - w0 + 1};
+}
+
+// One workgroup of 128 threads per query row joins its parts: four columns a
+// thread.  Rows that one workgroup of a call without a prefix wrote itself
+// are left alone; rows without any key become 0 and -inf.
+template <int RB, int PRB>
+__global__ __launch_bounds__(128) void mla_join_kernel(ListArgs a, ListArgs p) {
+  const int b = blockIdx.x / a.rows, r = blockIdx.x - b * a.rows;
+  const RowId id = row_id(a, b, r);
+  const int64_t flat = flat_row(a.d, id);
+  const Parts own = find_parts<RB>(a, b, r);
+  if (!PRB && own.count == 1) return;
+  Parts pre = {0, 0};
+  if constexpr (PRB != 0) pre = find_parts<PRB>(p, 0, (int)flat);
+  const int col = threadIdx.x * 4;
+  float m = kNegInf, l = 0;
+  v4f o = {0, 0, 0, 0};
+  auto part_at = [&](int i, const float*& po, const float*& pm) {
+    if (i < pre.count) {
+      if (pre.count == 1) {
+        po = p.ipart + flat * kLatent;
+        pm = p.ipml + 2 * flat;
+      } else {
+        const int64_t k = (int64_t)(2 * (pre.first + i) + (i == 0)) * PRB + (int)(flat % (PRB ? PRB : 1));
+        po = p.part + k * kLatent;
+        pm = p.pml + 2 * k;
+      }
+    } else {
+      i -= pre.count;
+      if (own.count == 1) {
+        po = a.ipart + flat * kLatent;
+        pm = a.ipml + 2 * flat;
+      } else {
+        const int64_t k = (int64_t)(2 * (own.first + i) + (i == 0)) * RB + r % RB;
+        po = a.part + k * kLatent;
+        pm = a.pml + 2 * k;
+      }
+    }
+  };
+  const int count = pre.count + own.count;
+  for (int i = 0; i < count; ++i) {
+    const float *po, *pm;
+    part_at(i, po, pm);
+    m = fmaxf(m, pm[0]);
+  }
+#pragma unroll 4
+  for (int i = 0; i < count; ++i) {
+    const float *po, *pm;
+    part_at(i, po, pm);
+    const v4f v = *(const v4f*)(po + col);
+    const float li = pm[1], f = li == 0 ? 0.0f : __builtin_amdgcn_exp2f(pm[0] - m);
+    l += li * f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += li == 0 ? 0.0f : v[e] * f;
+  }
+  const float inv = l == 0 ? 0.0f : 1.0f / l;
+  const uint2 w = {pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
+  *(uint2*)(a.d.out + id.b * a.d.sob + id.s * a.d.sos + id.h * a.d.soh + col) = w;
+  if (a.d.lse && threadIdx.x == 0)
+    a.d.lse[flat] = l > 0 ? (m + __builtin_amdgcn_logf(l)) * kLn2 : l == 0 ? kNegInf : l;
+}
+
+int rows_per_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+int unit_keys(int rb) { return rb <= 32 ? 4 * kTile : 2 * kTile; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+void launch_attend(int rb, const ListArgs& a, hipStream_t s) {
+  switch (rb) {
+    case 16: mla_attend_kernel<16><<<a.grid, 256, 0, s>>>(a); break;
+    case 32: mla_attend_kernel<32><<<a.grid, 256, 0, s>>>(a); break;
+    case 64: mla_attend_kernel<64><<<a.grid, 256, 0, s>>>(a); break;
+    default: mla_attend_kernel<128><<<a.grid, 256, 0, s>>>(a); break;
+  }
+}
+template <int PRB>
+void launch_join(int rb, const ListArgs& a, const ListArgs& p, hipStream_t s) {
+  const int grid = a.B * a.rows;
+  switch (rb) {
+    case 16: mla_join_kernel<16, PRB><<<grid, 128, 0, s>>>(a, p); break;
+    case 32: mla_join_kernel<32, PRB><<<grid, 128, 0, s>>>(a, p); break;
+    case 64: mla_join_kernel<64, PRB><<<grid, 128, 0, s>>>(a, p); break;
+    default: mla_join_kernel<128, PRB><<<grid, 128, 0, s>>>(a, p); break;
+  }
+}
+
+}  // namespace
+
+DecodePlan decode_plan(int64_t B, int64_t S, int64_t H, int64_t max_tokens, int64_t prefix_len, int cus) {
+  DecodePlan d{};
+  if (cus > kMlaMaxCus) cus = kMlaMaxCus;
+  const int64_t rows = S * H;
+  d.rows = rows_per_block(rows);
+  int64_t units = B * cdiv(rows, d.rows) * cdiv(max_tokens, unit_keys(d.rows));
+  d.grid = (int)(units < cus ? (units < 1 ? 1 : units) : cus);
+  size_t at = 0;
+  auto take = [&](int64_t n) {
+    const size_t r = at;
+    at += (size_t)((n + 63) / 64 * 64);
+    return r;
+  };
+  d.part = take(2ll * d.grid * d.rows * kLatent);
+  d.pml = take(2ll * d.grid * d.rows * 2);
+  if (prefix_len > 0) {
+    d.prows = rows_per_block(B * rows);
+    units = cdiv(B * rows, d.prows) * cdiv(prefix_len, unit_keys(d.prows));
+    d.pgrid = (int)(units < cus ? units : cus);
+    d.ppart = take(2ll * d.pgrid * d.prows * kLatent);
+    d.ppml = take(2ll * d.pgrid * d.prows * 2);
+    d.ipart = take(2 * B * rows * kLatent);
+    d.ipml = take(2 * B * rows * 2);
+  }
+  d.floats = at;
+  return d;
+}
+
+hipError_t launch_mla_decode(const DecodeArgs& d, const DecodePlan& plan, hipStream_t stream) {
+  const int rows = d.S * d.H;
+  ListArgs a{};
+  a.d = d;
+  a.table = d.table;
+  a.ldt = d.ldt;
+  a.lens = d.lens;
+  a.capacity = (int)((int64_t)d.max_pages * d.cache.page_size);
+  a.B = d.B;
+  a.rows = rows;
+  a.nt = (rows + plan.rows - 1) / plan.rows;
+  a.grid = plan.grid;
+  a.part = d.work + plan.part;
+  a.pml = d.work + plan.pml;
+  if (d.prefix_len > 0) {
+    const int64_t all = (int64_t)d.B * rows;
+    a.ipart = d.work + plan.ipart;
+    a.ipml = d.work + plan.ipml;
+    ListArgs p = a;
+    p.table = d.prefix_table;
+    p.ldt = 0;
+    p.lens = nullptr;
+    p.fixed = d.prefix_len;
+    p.B = 1;
+    p.rows = (int)all;
+    p.nt = (int)cdiv(all, plan.prows);
+    p.grid = plan.pgrid;
+    p.part = d.work + plan.ppart;
+    p.pml = d.work + plan.ppml;
+    p.ipart = a.ipart + all * kLatent;
+    p.ipml = a.ipml + 2 * all;
+    launch_attend(plan.prows, p, stream);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    launch_attend(plan.rows, a, stream);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    switch (plan.prows) {
+      case 16: launch_join<16>(plan.rows, a, p, stream); break;
+      case 32: launch_join<32>(plan.rows, a, p, stream); break;
+      case 64: launch_join<64>(plan.rows, a, p, stream); break;
+      default: launch_join<128>(plan.rows, a, p, stream); break;
+    }
+    return hipGetLastError();
+  }
+  launch_attend(plan.rows, a, stream);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  launch_join<0>(plan.rows, a, a, stream);
+  return hipGetLastError();
+}
+
+}  // namespace mxfp4

@@ -1,0 +1,163 @@
+// Device-side pieces shared by the latent-attention kernels (gfx950).
+//
+// Both attention kernels compute the transposed products
+//   S^T = K Q^T   (rows: keys, columns: query rows)
+//   O^T = V^T P^T (rows: value columns, columns: query rows)
+// so that a lane's MFMA results all belong to ONE query row (column l%16 of
+// a 16 x 16 result, l%32 of a 32 x 32 one): the softmax's maximum, sum and
+// rescaling are per-lane values, and the probabilities a lane computes are
+// already its B operand of the second product.  The contraction over keys
+// may run in any order as long as both operands agree: a lane holds the
+// keys its S^T registers hold, and V^T is read from LDS for those keys by
+// the transposing read (ds_read_b64_tr_b16: within 16 lanes, lane i supplies
+// the address of 4 consecutive 16-bit values of key i/4, columns 4 (i%4)..,
+// and receives column i of the 4 keys; lane layout measured on MI355X).
+//
+// Key and value rows reach LDS by direct loads (global_load_lds_dwordx4:
+// lane l's 16 bytes land at the wave's LDS base + 16 l), issued by inline
+// assembly so that the compiler does not wait for them before every LDS
+// read; the kernels wait by hand.  A row's 16-byte chunks are permuted when
+// they are fetched (the lane that fills LDS chunk p fetches chunk
+// p ^ swizzle(row)), so that both the 16-byte row reads of K and the
+// transposing reads of V touch every bank once.
+#pragma once
+
+#include "mxfp4_device.h"
+
+namespace mxfp4 {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) v4s* lds_v4s_t;
+typedef __attribute__((address_space(3))) v8s* lds_v8s_t;
+typedef __attribute__((address_space(3))) v4f* lds_v4f_t;
+typedef __attribute__((address_space(3))) float* lds_f32_t;
+typedef __attribute__((address_space(3))) int* lds_i32_t;
+
+// LDS by byte address (a kernel's only __shared__ array starts at 0).
+__device__ __forceinline__ v8bf lds_read16(uint32_t a) {
+  return __builtin_bit_cast(v8bf, *(lds_v8s_t)(uintptr_t)a);
+}
+__device__ __forceinline__ v4s lds_read_tr(uint32_t a) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t)(uintptr_t)a);
+}
+__device__ __forceinline__ v8bf join_keys(v4s a, v4s b) {
+  return __builtin_bit_cast(v8bf, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Reverses 4 bits: the swizzle of rows whose length is a multiple of 256
+// bytes.  16 rows' equal chunks fall on 16 different slots (K reads), and so
+// do the chunk pairs of 8 rows and the chunk quads of 4 rows (V reads).
+__host__ __device__ constexpr uint32_t bitrev4(uint32_t r) {
+  return ((r & 1) << 3) | ((r & 2) << 1) | ((r & 4) >> 1) | ((r & 8) >> 3);
+}
+
+// Direct loads of 16 bytes per lane to LDS at `lds` + 16 lane, from a
+// uniform base plus a lane's byte offset, or from a lane's own address.
+// (M0 holds the LDS base; one wait state after it is written.  A base that a
+// vector instruction wrote, as v_readlane does, needs five before the load:
+// the compiler does not count them into an assembly statement.)
+__device__ __forceinline__ void dma16(uint32_t lds, const void* base, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(lds), "v"(voff), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void dma16_at(uint32_t lds, const void* p) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :: "s"(lds), "v"(p) : "memory", "m0");
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" :: "i"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void wave_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// The larger / the sum of x over the lanes that share a query row: lanes
+// l, l ^ 32 (RW = 32), and l ^ 16 too (RW = 16).  The lane-swap
+// instructions on two copies of x give each lane both halves' values.
+template <int RW>
+__device__ __forceinline__ float rows_max(float x) {
+  if constexpr (RW == 16) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  }
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+template <int RW>
+__device__ __forceinline__ float rows_sum(float x) {
+  if constexpr (RW == 16) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  }
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// MFMA by the number of query rows (columns): K = 32 of 16 x 16, K = 16 of
+// 32 x 32.  Either way a lane's operand is 8 bf16.
+__device__ __forceinline__ v4f mfma_rows(v8bf a, v8bf b, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ v16f mfma_rows(v8bf a, v8bf b, v16f c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// The running maximum may lag the true one by this many powers of two
+// before the accumulators are rescaled: probabilities then reach 2^8, which
+// changes no relative rounding, and most tiles rescale nothing.
+constexpr float kLag = 8.0f;
+
+// Probabilities of a tile from its scores x (one query row per lane):
+// updates the row's maximum m (in units of log2, scores times c) and the
+// lane's share l of the row's sum, rounds to bf16 operands (the sum takes
+// the unrounded values: the log-sum-exp is exact to fp32).  alpha != 1 asks
+// the caller to rescale its accumulators; true if any lane's is.
+template <int RW, int NX>
+__device__ __forceinline__ bool softmax_step(float (&x)[NX], float c, float& m, float& l, float& alpha,
+                                             v8bf (&p)[NX / 8]) {
+  float mx = x[0];
+#pragma unroll
+  for (int i = 1; i < NX; ++i) mx = fmaxf(mx, x[i]);
+  mx = rows_max<RW>(mx) * c;
+  bool grew = false;
+  if (__builtin_amdgcn_ballot_w64(mx > m + kLag)) {
+    grew = true;
+    const float mn = fmaxf(m, mx);
+    alpha = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+    m = mn;
+    l *= alpha;
+  }
+  const float mu = m == kNegInf ? 0.0f : m;  // a row that has seen nothing yet
+#pragma unroll
+  for (int i = 0; i < NX; ++i) {
+    x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c, -mu));
+    l += x[i];
+  }
+#pragma unroll
+  for (int i = 0; i < NX / 8; ++i) {
+    v8bf t;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j] = (__bf16)x[8 * i + j];
+    p[i] = t;
+  }
+  return grew;
+}
+
+// Key (within a 32-key tile) of a lane's score register i.
+template <int RW>
+__device__ __forceinline__ int key_of(int i, uint32_t lane) {
+  if constexpr (RW == 16) return 16 * (i >> 2) + 4 * (int)(lane >> 4) + (i & 3);
+  else return 8 * (i >> 2) + 4 * (int)(lane >> 5) + (i & 3);
+}
+
+}  // namespace mxfp4

@@ -1,0 +1,229 @@
+// Causal attention over keys and values expanded per head (latent
+// attention's prompt form), for gfx950: sequences of unequal lengths packed
+// along the tokens, keys made of a per-head part and a rotated part that all
+// heads share (never copied per head).
+//
+// One pass over the keys with a running maximum and sum (fp32).  A workgroup
+// takes a block of query rows of one head of one sequence, 32 rows a wave,
+// and walks the keys in 32-key tiles that all its waves share in a ring of
+// LDS stages; loads run ahead of the barrier that hands a tile over.  Bound
+// by the matrix units: 2 (dn + 64 + dv) operations per (query, key) pair.
+#include "mla_device.h"
+#include "mla_launch.h"
+
+namespace mxfp4 {
+namespace {
+
+constexpr int kTile = 32;
+
+// LDS of one stage: the keys' first 128 values (256-byte rows), the next 64
+// (DN = 192; 128-byte rows), the rotated 64, then the values (DV * 2-byte rows).
+template <int DN, int DV>
+struct Stage {
+  static constexpr uint32_t kB = kTile * 256;                       // second part of the keys
+  static constexpr uint32_t kPe = kB + (DN > 128 ? kTile * 128 : 0);
+  static constexpr uint32_t kV = kPe + kTile * 128;
+  static constexpr uint32_t kBytes = kV + kTile * DV * 2;
+  static constexpr int kLoads = kBytes / 1024;                      // wave loads of a tile
+};
+
+template <int DN, int DV, int NW, int NS>
+struct Cfg {
+  using St = Stage<DN, DV>;
+  static constexpr int kPer = St::kLoads / NW;
+  static_assert(St::kLoads % NW == 0, "equal loads per wave");
+  static constexpr uint32_t kLds = NS * St::kBytes;
+  static_assert(kLds <= 160 * 1024, "LDS per workgroup");
+};
+
+// The sequence that holds query block `blk` of R rows and the block's number
+// in it (from the last: later rows see more keys, so they start first);
+// false past the end.
+template <int R>
+__device__ __forceinline__ bool find_block(const MlaPrefillArgs& a, int blk, int& b, int& i) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int s = 0; s < a.B; s += 64) {
+    const int k = s + lane;
+    int n = 0;
+    if (k < a.B) {
+      const int64_t nq = (int64_t)a.cu_q[k + 1] - a.cu_q[k];
+      n = nq > 0 ? (int)((nq + R - 1) / R) : 0;
+    }
+    int x = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int y = __shfl_up(x, d);
+      if (lane >= d) x += y;
+    }
+    const uint64_t hit = __builtin_amdgcn_ballot_w64(before + x > blk);
+    if (hit) {
+      const int f = __builtin_ctzll(hit);
+      b = s + f;
+      const int end = before + __builtin_amdgcn_readlane(x, f);
+      i = end - 1 - blk;
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(x, 63);
+  }
+  return false;
+}
+
+template <int DN, int DV, int NW, int NS>
+__global__ __launch_bounds__(64 * NW) void mla_prefill_kernel(MlaPrefillArgs a) {
+  using St = Stage<DN, DV>;
+  using C = Cfg<DN, DV, NW, NS>;
+  constexpr int R = 32 * NW, kSteps = (DN + kRope) / 16, kCols = DV / 32;
+  __shared__ int4 lds_raw[C::kLds / 16];
+  uint32_t anchor = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int4*)lds_raw;
+  asm volatile("" : "+s"(anchor)::"memory");  // LDS is addressed by number: its array starts at 0
+
+  const uint32_t lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = blockIdx.x % a.H;
+  int b, blk;
+  if (!find_block<R>(a, blockIdx.x / a.H, b, blk)) return;
+  b = __builtin_amdgcn_readfirstlane(b);
+  blk = __builtin_amdgcn_readfirstlane(blk);
+  // Offsets are clamped to the packed tensors: bad ones cannot leave them.
+  const int64_t q0 = max((int64_t)0, min(a.Tq, (int64_t)a.cu_q[b])), q1 = max(q0, min(a.Tq, (int64_t)a.cu_q[b + 1]));
+  const int64_t k0 = max((int64_t)0, min(a.Tk, (int64_t)a.cu_k[b])), k1 = max(k0, min(a.Tk, (int64_t)a.cu_k[b + 1]));
+  const int nq = (int)(q1 - q0), nk = (int)(k1 - k0);
+  const int r0 = blk * R;                      // first query row of the block
+  if (r0 >= nq) return;
+  const int wr0 = r0 + wv * 32;                // of the wave
+  const int row = wr0 + (int)(lane & 31);
+  const int past = a.causal ? nk - nq + 1 : nk;  // keys the first query sees
+  auto sees = [&](int r) { return a.causal ? min(nk, past + r) : nk; };
+  const int seen = sees(row), seen_first = sees(wr0), seen_wave = sees(min(wr0 + 31, nq - 1));
+  const int nt = (max(0, sees(min(r0 + R, nq) - 1)) + kTile - 1) / kTile;
+  const int wave_tiles = wr0 < nq ? (max(0, seen_wave) + kTile - 1) / kTile : 0;
+
+  v8bf q[kSteps];
+  {
+    const uint16_t* p = a.q + (q0 + min(row, nq - 1)) * a.sqt + h * a.sqh + 8 * (lane >> 5);
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) q[k] = __builtin_bit_cast(v8bf, *(const int4*)(p + k * 16));
+  }
+  v16f o[kCols];
+#pragma unroll
+  for (int i = 0; i < kCols; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[i][j] = 0;
+  float m = kNegInf, l = 0;
+
+  const char* kb = (const char*)(a.k + k0 * a.skt + h * a.skh);
+  const char* pb = (const char*)(a.k_pe + k0 * a.spt);
+  const char* vb = (const char*)(a.v + k0 * a.svt + h * a.svh);
+  // Load j of a tile: 1 KiB of one of the stage's regions.
+  auto issue = [&](int t) {
+    const uint32_t lds = (t % NS) * St::kBytes;
+    const int left = nk - t * kTile;  // rows of the tile that exist (the last is loaded again past them)
+#pragma unroll
+    for (int i = 0; i < C::kPer; ++i) {
+      const uint32_t at = (wv * C::kPer + i) * 1024;
+      const char* base;
+      uint32_t off;
+      if (at < St::kB) {                                   // 4 rows of 256 bytes
+        const uint32_t r = at / 256 + (lane >> 4);
+        base = kb + (int64_t)t * kTile * a.skt * 2;
+        off = min((int)r, left - 1) * (uint32_t)a.skt * 2 + (((lane & 15) ^ bitrev4(r & 15)) << 4);
+      } else if (at < St::kV) {                            // 8 rows of 128 bytes
+        const bool second = DN > 128 && at < St::kPe;
+        const uint32_t r = (at - (second ? St::kB : St::kPe)) / 128 + (lane >> 3);
+        const uint32_t ch = ((lane & 7) ^ ((r >> 1) & 7)) << 4;
+        base = second ? kb + (int64_t)t * kTile * a.skt * 2 + 256 : pb + (int64_t)t * kTile * a.spt * 2;
+        off = min((int)r, left - 1) * (uint32_t)(second ? a.skt : a.spt) * 2 + ch;
+      } else {                                             // rows of DV values
+        constexpr uint32_t kChunks = DV / 8, kRows = 64 / kChunks;
+        const uint32_t r = (at - St::kV) / (DV * 2) + lane / kChunks;
+        (void)kRows;
+        base = vb + (int64_t)t * kTile * a.svt * 2;
+        off = min((int)r, left - 1) * (uint32_t)a.svt * 2 + (((lane % kChunks) ^ bitrev4(r & 15)) << 4);
+      }
+      dma16(lds + at, base, off);
+    }
+  };
+
+#pragma unroll
+  for (int t = 0; t < NS - 1; ++t)
+    if (t < nt) issue(t);
+  for (int t = 0; t < nt; ++t) {
+    const int later = min(nt, t + NS - 1) - t - 1;  // tiles in flight behind this one
+    if (later >= 2) wait_loads<2 * C::kPer>();
+    else if (later == 1) wait_loads<C::kPer>();
+    else wait_loads<0>();
+    wait_lds();
+    wave_barrier();
+    if (t + NS - 1 < nt) issue(t + NS - 1);
+    if (t >= wave_tiles) continue;
+
+    const uint32_t tile = (t % NS) * St::kBytes;
+    const uint32_t kr = lane & 31, hh = lane >> 5, px = (kr >> 1) & 7;
+    v16f s = {};
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      uint32_t at;
+      if (k < 8) at = tile + kr * 256 + (((2 * k) ^ hh ^ bitrev4(kr & 15)) << 4);
+      else if (k < DN / 16) at = tile + St::kB + kr * 128 + (((2 * (k - 8) + hh) ^ px) << 4);
+      else at = tile + St::kPe + kr * 128 + (((2 * (k - DN / 16) + hh) ^ px) << 4);
+      s = mfma_rows(lds_read16(at), q[k], s);
+    }
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = s[i];
+    if ((t + 1) * kTile > seen_first) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (t * kTile + key_of<32>(i, lane) >= seen) x[i] = kNegInf;
+    }
+    float alpha;
+    v8bf p[2];
+    if (softmax_step<32, 16>(x, a.c, m, l, alpha, p)) {
+#pragma unroll
+      for (int i = 0; i < kCols; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] *= alpha;
+    }
+    const uint32_t i16 = lane & 15, vr = 4 * hh + (i16 >> 2);
+    const uint32_t va = tile + St::kV + vr * (DV * 2) + (i16 & 1) * 8;
+    const uint32_t vx = ((2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1)) ^ bitrev4(vr)) << 4;
+#pragma unroll
+    for (int ct = 0; ct < kCols; ++ct) {
+      const uint32_t c0 = (((4 * ct) & 15) << 4), c1 = (ct >> 2) * 256;
+      const uint32_t at = va + (vx ^ c0) + c1, ae = va + 8 * DV * 2 + (vx ^ 16 ^ c0) + c1;
+      o[ct] = mfma_rows(join_keys(lds_read_tr(at), lds_read_tr(ae)), p[0], o[ct]);
+      o[ct] = mfma_rows(join_keys(lds_read_tr(at + 16 * DV * 2), lds_read_tr(ae + 16 * DV * 2)), p[1], o[ct]);
+    }
+  }
+
+  l = rows_sum<32>(l);
+  if (row >= nq) return;
+  const float inv = l == 0 ? 0.0f : 1.0f / l;  // a row that sees no key: 0 and -inf
+  uint16_t* out = a.out + (q0 + row) * a.sot + h * a.soh;
+#pragma unroll
+  for (int i = 0; i < kCols; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint2 w = {pack_bf16x2(o[i][4 * j] * inv, o[i][4 * j + 1] * inv),
+                       pack_bf16x2(o[i][4 * j + 2] * inv, o[i][4 * j + 3] * inv)};
+      *(uint2*)(out + 32 * i + 8 * j + 4 * (lane >> 5)) = w;
+    }
+  if (a.lse && lane < 32)
+    a.lse[(q0 + row) * a.H + h] = l > 0 ? (m + __builtin_amdgcn_logf(l)) * kLn2 : l == 0 ? kNegInf : l;
+}
+
+}  // namespace
+
+hipError_t launch_mla_prefill(const MlaPrefillArgs& p, int dn, int dv, int cus, hipStream_t stream) {
+  (void)cus;
+  constexpr int NW = 4;
+  // at most one part-filled block per sequence
+  const int64_t blocks = p.Tq / (32 * NW) + (p.Tq < p.B ? p.Tq : p.B);
+  const dim3 grid((unsigned)(blocks * p.H));
+  if (dn == 192) mla_prefill_kernel<192, 256, NW, 4><<<grid, 64 * NW, 0, stream>>>(p);
+  else mla_prefill_kernel<128, 128, NW, 4><<<grid, 64 * NW, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace mxfp4
