@@ -195,34 +195,52 @@ __device__ __forceinline__ void attend_tile(uint32_t tile, Rows<RW>& st, float& 
                                             bool full, int seen, uint32_t bad) {
   constexpr int NX = RW / 2;
   float x[NX];
+  const uint32_t i16 = lane & 15;
+  // Step i of the scores: for 16 rows, keys 0-15 and 16-31 in turn.
+  const uint32_t row = lane % RW, part = lane / RW;  // the lane's key row and its 8-value piece of a step
+  const uint32_t ka = tile + row * 1024, kx = (part ^ bitrev4(row & 15)) << 4;
+  const uint32_t pa = tile + kPeOff + row * 128, px = (row >> 1) & 7;
+  auto key_frag = [&](int i) {
+    if constexpr (RW == 16) {
+      const int k = i >> 1;
+      const uint32_t a = k < 16 ? ka + (kx ^ ((4 * (k & 3)) << 4)) + (k >> 2) * 256 + (i & 1) * 16 * 1024
+                                : pa + (((4 * (k - 16) + part) ^ px) << 4) + (i & 1) * 16 * 128;
+      return lds_read16(a);
+    } else {
+      const uint32_t a = i < 32 ? ka + (kx ^ ((2 * (i & 7)) << 4)) + (i >> 3) * 256
+                                : pa + (((2 * (i - 32) + part) ^ px) << 4);
+      return lds_read16(a);
+    }
+  };
+  v8bf first[4];
+  read_group(first, key_frag);
   if constexpr (RW == 16) {
-    const uint32_t row = lane & 15, g = lane >> 4;
-    const uint32_t ka = tile + row * 1024, kx = (g ^ bitrev4(row)) << 4;
-    const uint32_t pa = tile + kPeOff + row * 128, px = (row >> 1) & 7;
-    v4f s0 = {0, 0, 0, 0}, s1 = {0, 0, 0, 0};
+    v4f s[2] = {};
+    pipeline<36, 4>(first, key_frag, [&](int i, v8bf f) { s[i & 1] = mfma_rows(f, st.q[i >> 1], s[i & 1]); });
 #pragma unroll
-    for (int k = 0; k < 18; ++k) {
-      const uint32_t a = k < 16 ? ka + (kx ^ ((4 * (k & 3)) << 4)) + (k >> 2) * 256
-                                : pa + (((4 * (k - 16) + g) ^ px) << 4);
-      s0 = mfma_rows(lds_read16(a), st.q[k], s0);
-      s1 = mfma_rows(lds_read16(a + (k < 16 ? 16 * 1024 : 16 * 128)), st.q[k], s1);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = s0[i], x[4 + i] = s1[i];
+    for (int i = 0; i < 8; ++i) x[i] = s[i >> 2][i & 3];
   } else {
-    const uint32_t row = lane & 31, h = lane >> 5;
-    const uint32_t ka = tile + row * 1024, kx = (h ^ bitrev4(row & 15)) << 4;
-    const uint32_t pa = tile + kPeOff + row * 128, px = (row >> 1) & 7;
     v16f s = {};
-#pragma unroll
-    for (int k = 0; k < 36; ++k) {
-      const uint32_t a = k < 32 ? ka + (kx ^ ((2 * (k & 7)) << 4)) + (k >> 3) * 256
-                                : pa + (((2 * (k - 32) + h) ^ px) << 4);
-      s = mfma_rows(lds_read16(a), st.q[k], s);
-    }
+    pipeline<36, 4>(first, key_frag, [&](int i, v8bf f) { s = mfma_rows(f, st.q[i], s); });
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = s[i];
   }
+  // Step i of the values: for 16 rows column tile i over all keys, for 32
+  // rows column tile i / 2 over keys 0-15 or 16-31.
+  const uint32_t vrow = 4 * (lane >> (RW == 16 ? 4 : 5)) + (i16 >> 2);
+  const uint32_t vchunk = (RW == 16 ? 0 : 2 * ((lane >> 4) & 1)) + ((i16 & 3) >> 1);
+  const uint32_t va = tile + vrow * 1024 + (i16 & 1) * 8, vx = (vchunk ^ bitrev4(vrow)) << 4;
+  auto value_frag = [&](int i) {
+    if constexpr (RW == 16) {
+      const uint32_t a = va + (vx ^ (((2 * i) & 15) << 4)) + (i >> 3) * 256;
+      return join_keys(lds_read_tr(a), lds_read_tr(a + 16 * 1024));
+    } else {
+      const int ct = i >> 1;
+      const uint32_t c0 = ((4 * ct) & 15) << 4, c1 = (ct >> 2) * 256 + (i & 1) * 16 * 1024;
+      return join_keys(lds_read_tr(va + (vx ^ c0) + c1), lds_read_tr(va + 8 * 1024 + (vx ^ 16 ^ c0) + c1));
+    }
+  };
+  read_group(first, value_frag);
   if (!full) {
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
@@ -232,33 +250,11 @@ __device__ __forceinline__ void attend_tile(uint32_t tile, Rows<RW>& st, float& 
   }
   float alpha;
   v8bf p[NX / 8];
-  if (softmax_step<RW, NX>(x, c, m, l, alpha, p)) {
-#pragma unroll
-    for (int i = 0; i < Rows<RW>::kCols; ++i)
-#pragma unroll
-      for (int j = 0; j < RW * RW / 64; ++j) st.o[i][j] *= alpha;
-  }
-  const uint32_t i16 = lane & 15;
-  if constexpr (RW == 16) {
-    const uint32_t row = 4 * (lane >> 4) + (i16 >> 2);
-    const uint32_t va = tile + row * 1024 + (i16 & 1) * 8, vx = (((i16 & 3) >> 1) ^ bitrev4(row)) << 4;
-#pragma unroll
-    for (int ct = 0; ct < 32; ++ct) {
-      const uint32_t a = va + (vx ^ (((2 * ct) & 15) << 4)) + (ct >> 3) * 256;
-      st.o[ct] = mfma_rows(join_keys(lds_read_tr(a), lds_read_tr(a + 16 * 1024)), p[0], st.o[ct]);
-    }
-  } else {
-    const uint32_t row = 4 * (lane >> 5) + (i16 >> 2);
-    const uint32_t va = tile + row * 1024 + (i16 & 1) * 8;
-    const uint32_t vx = ((2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1)) ^ bitrev4(row)) << 4;
-#pragma unroll
-    for (int ct = 0; ct < 16; ++ct) {
-      const uint32_t a = va + (vx ^ (((4 * ct) & 15) << 4)) + (ct >> 2) * 256;
-      const uint32_t e = va + 8 * 1024 + (vx ^ 16 ^ (((4 * ct) & 15) << 4)) + (ct >> 2) * 256;
-      st.o[ct] = mfma_rows(join_keys(lds_read_tr(a), lds_read_tr(e)), p[0], st.o[ct]);
-      st.o[ct] = mfma_rows(join_keys(lds_read_tr(a + 16 * 1024), lds_read_tr(e + 16 * 1024)), p[1], st.o[ct]);
-    }
-  }
+  if (softmax_step<RW, NX>(x, c, m, l, alpha, p)) rescale(st.o, alpha);
+  pipeline<32, 4>(first, value_frag, [&](int i, v8bf f) {
+    if constexpr (RW == 16) st.o[i] = mfma_rows(f, p[0], st.o[i]);
+    else st.o[i >> 1] = mfma_rows(f, p[i & 1], st.o[i >> 1]);
+  });
 }
 
 // Query row r of sequence b: its request, token and head.

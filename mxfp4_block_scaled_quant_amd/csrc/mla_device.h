@@ -153,6 +153,58 @@ __device__ __forceinline__ bool softmax_step(float (&x)[NX], float c, float& m, 
   return grew;
 }
 
+// o *= alpha for accumulators that stay in accumulation registers: vector
+// instructions cannot take those, and written as plain C++ the compiler moves
+// every accumulator through vector registers on each tile, not only where
+// the maximum grew.  The leading wait covers matrix results still in flight
+// (the compiler does not count them for assembly statements).
+template <typename V, int N>
+__device__ __forceinline__ void rescale(V (&o)[N], float alpha) {
+  asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+#pragma unroll
+    for (int j = 0; j < (int)(sizeof(V) / 4); ++j) {
+      float t = o[i][j], r;
+      asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(t) : "a"(t));
+      t *= alpha;
+      asm volatile("v_accvgpr_write_b32 %0, %1" : "=a"(r) : "v"(t));
+      o[i][j] = r;
+    }
+  }
+  asm volatile("s_nop 3" ::: "memory");
+}
+
+// A run of N matrix steps whose operands come from LDS in groups of G: the
+// next group's reads are issued before this group's products, and nothing
+// moves between groups, so that a wave alone on its SIMD hides the LDS
+// latency behind G products and no more than two groups are in registers.
+// read(i) gives step i's operand, mul(i, operand) uses it; `first` holds
+// group 0, read ahead by the caller.
+template <int N, int G, typename T, typename Read, typename Mul>
+__device__ __forceinline__ void pipeline(T (&first)[G], Read read, Mul mul) {
+  static_assert(N % G == 0, "whole groups");
+  T f[2][G];
+#pragma unroll
+  for (int i = 0; i < G; ++i) f[0][i] = first[i];
+#pragma unroll
+  for (int g = 0; g < N / G; ++g) {
+    if (g + 1 < N / G) {
+#pragma unroll
+      for (int i = 0; i < G; ++i) f[(g + 1) & 1][i] = read((g + 1) * G + i);
+    }
+#pragma unroll
+    for (int i = 0; i < G; ++i) mul(g * G + i, f[g & 1][i]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+template <int G, typename T, typename Read>
+__device__ __forceinline__ void read_group(T (&first)[G], Read read) {
+#pragma unroll
+  for (int i = 0; i < G; ++i) first[i] = read(i);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // Key (within a 32-key tile) of a lane's score register i.
 template <int RW>
 __device__ __forceinline__ int key_of(int i, uint32_t lane) {

@@ -179,12 +179,7 @@ __global__ __launch_bounds__(64 * NW) void mla_prefill_kernel(MlaPrefillArgs a) 
     }
     float alpha;
     v8bf p[2];
-    if (softmax_step<32, 16>(x, a.c, m, l, alpha, p)) {
-#pragma unroll
-      for (int i = 0; i < kCols; ++i)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) o[i][j] *= alpha;
-    }
+    if (softmax_step<32, 16>(x, a.c, m, l, alpha, p)) rescale(o, alpha);
     const uint32_t i16 = lane & 15, vr = 4 * hh + (i16 >> 2);
     const uint32_t va = tile + St::kV + vr * (DV * 2) + (i16 & 1) * 8;
     const uint32_t vx = ((2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1)) ^ bitrev4(vr)) << 4;
