@@ -33,10 +33,17 @@ FLAGS = [
     "-fvisibility=hidden",
 ]
 
+FILE_FLAGS = {
+    # Two waves per SIMD: every accumulator in one of a wave's 256 vector
+    # registers (the compiler's own choice splits them 128 + 128 with the
+    # accumulation registers, and spills).
+    "mla_prefill.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+}
+
 
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD, os.path.basename(src).replace(".hip", ".o"))
-    cmd = [HIPCC, *FLAGS, "-c", src, "-o", obj]
+    cmd = [HIPCC, *FLAGS, *FILE_FLAGS.get(os.path.basename(src), []), "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)

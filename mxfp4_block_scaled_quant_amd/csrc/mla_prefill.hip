@@ -70,10 +70,11 @@ __device__ __forceinline__ bool find_block(const MlaPrefillArgs& a, int blk, int
 }
 
 template <int DN, int DV, int NW, int NS>
-__global__ __launch_bounds__(64 * NW) void mla_prefill_kernel(MlaPrefillArgs a) {
+__global__ __launch_bounds__(64 * NW, 2) void mla_prefill_kernel(MlaPrefillArgs a) {
   using St = Stage<DN, DV>;
   using C = Cfg<DN, DV, NW, NS>;
   constexpr int R = 32 * NW, kSteps = (DN + kRope) / 16, kCols = DV / 32;
+  constexpr int G = DV == 256 ? 2 : 4;  // LDS operands read ahead: what the registers leave
   __shared__ int4 lds_raw[C::kLds / 16];
   uint32_t anchor = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int4*)lds_raw;
   asm volatile("" : "+s"(anchor)::"memory");  // LDS is addressed by number: its array starts at 0
@@ -112,63 +113,83 @@ __global__ __launch_bounds__(64 * NW) void mla_prefill_kernel(MlaPrefillArgs a) 
     for (int j = 0; j < 16; ++j) o[i][j] = 0;
   float m = kNegInf, l = 0;
 
-  const char* kb = (const char*)(a.k + k0 * a.skt + h * a.skh);
-  const char* pb = (const char*)(a.k_pe + k0 * a.spt);
-  const char* vb = (const char*)(a.v + k0 * a.svt + h * a.svh);
-  // Load j of a tile: 1 KiB of one of the stage's regions.
-  auto issue = [&](int t) {
-    const uint32_t lds = (t % NS) * St::kBytes;
-    const int left = nk - t * kTile;  // rows of the tile that exist (the last is loaded again past them)
+  // This wave's loads of a tile, 1 KiB each: a running base (the tile's
+  // first row), its step per tile, and the lane's offset, which names a row
+  // and the row's permuted chunk.  All of it is fixed before the loop.
+  const char* base[C::kPer];
+  int64_t step[C::kPer];
+  uint32_t off[C::kPer], pitch[C::kPer];
+  int first_row[C::kPer], shift[C::kPer];
+#pragma unroll
+  for (int i = 0; i < C::kPer; ++i) {
+    const uint32_t at = (wv * C::kPer + i) * 1024;
+    const bool second = DN > 128 && at >= St::kB && at < St::kPe;
+    if (at < St::kPe) base[i] = (const char*)(a.k + k0 * a.skt + h * a.skh + (second ? 128 : 0));
+    else if (at < St::kV) base[i] = (const char*)(a.k_pe + k0 * a.spt);
+    else base[i] = (const char*)(a.v + k0 * a.svt + h * a.svh);
+    pitch[i] = (uint32_t)(at < St::kPe ? a.skt : at < St::kV ? a.spt : a.svt) * 2;
+    step[i] = (int64_t)kTile * pitch[i];
+    shift[i] = at < St::kB ? 4 : at < St::kV ? 3 : DV == 256 ? 5 : 4;      // log2 of a row's chunks
+    first_row[i] = (int)((at - (at < St::kB ? 0 : second ? St::kB : at < St::kV ? St::kPe : St::kV)) >> (shift[i] + 4));
+    const uint32_t r = first_row[i] + (lane >> shift[i]), ch = lane & ((1u << shift[i]) - 1);
+    off[i] = r * pitch[i] + ((ch ^ (shift[i] == 3 ? (r >> 1) & 7 : bitrev4(r & 15))) << 4);
+  }
+  auto issue = [&](int t, uint32_t lds) {
+    const int left = nk - t * kTile;  // rows of the tile that exist
 #pragma unroll
     for (int i = 0; i < C::kPer; ++i) {
-      const uint32_t at = (wv * C::kPer + i) * 1024;
-      const char* base;
-      uint32_t off;
-      if (at < St::kB) {                                   // 4 rows of 256 bytes
-        const uint32_t r = at / 256 + (lane >> 4);
-        base = kb + (int64_t)t * kTile * a.skt * 2;
-        off = min((int)r, left - 1) * (uint32_t)a.skt * 2 + (((lane & 15) ^ bitrev4(r & 15)) << 4);
-      } else if (at < St::kV) {                            // 8 rows of 128 bytes
-        const bool second = DN > 128 && at < St::kPe;
-        const uint32_t r = (at - (second ? St::kB : St::kPe)) / 128 + (lane >> 3);
-        const uint32_t ch = ((lane & 7) ^ ((r >> 1) & 7)) << 4;
-        base = second ? kb + (int64_t)t * kTile * a.skt * 2 + 256 : pb + (int64_t)t * kTile * a.spt * 2;
-        off = min((int)r, left - 1) * (uint32_t)(second ? a.skt : a.spt) * 2 + ch;
-      } else {                                             // rows of DV values
-        constexpr uint32_t kChunks = DV / 8, kRows = 64 / kChunks;
-        const uint32_t r = (at - St::kV) / (DV * 2) + lane / kChunks;
-        (void)kRows;
-        base = vb + (int64_t)t * kTile * a.svt * 2;
-        off = min((int)r, left - 1) * (uint32_t)a.svt * 2 + (((lane % kChunks) ^ bitrev4(r & 15)) << 4);
+      uint32_t o = off[i];
+      if (left < kTile) {             // past them the last row is loaded again
+        const int over = first_row[i] + (int)(lane >> shift[i]) - (left - 1);
+        o -= (over > 0 ? over : 0) * pitch[i];
       }
-      dma16(lds + at, base, off);
+      dma16(lds + (wv * C::kPer + i) * 1024, base[i], o);
+      base[i] += step[i];
     }
   };
 
 #pragma unroll
   for (int t = 0; t < NS - 1; ++t)
-    if (t < nt) issue(t);
+    if (t < nt) issue(t, t * St::kBytes);
+  // Lane addresses within a stage.  Rows start at multiples of their length,
+  // so a step's chunk is one XOR away and its row group an immediate offset.
+  const uint32_t kr = lane & 31, hh = lane >> 5, i16 = lane & 15, vr = 4 * hh + (i16 >> 2);
+  uint32_t ka = kr * 256 + ((hh ^ bitrev4(kr & 15)) << 4);
+  uint32_t kb = St::kB + kr * 128 + ((hh ^ ((kr >> 1) & 7)) << 4);
+  uint32_t va = St::kV + vr * (DV * 2) + (i16 & 1) * 8 +
+                (((2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1)) ^ bitrev4(vr)) << 4);
+  uint32_t tile = 0, fill = (NS - 1) * St::kBytes;  // this tile's stage, and the next to load
   for (int t = 0; t < nt; ++t) {
-    const int later = min(nt, t + NS - 1) - t - 1;  // tiles in flight behind this one
-    if (later >= 2) wait_loads<2 * C::kPer>();
-    else if (later == 1) wait_loads<C::kPer>();
+    if (t + 2 < nt) wait_loads<2 * C::kPer>();
+    else if (t + 1 < nt) wait_loads<C::kPer>();
     else wait_loads<0>();
     wait_lds();
     wave_barrier();
-    if (t + NS - 1 < nt) issue(t + NS - 1);
+    if (t + NS - 1 < nt) issue(t + NS - 1, fill);
+    const uint32_t at = tile;
+    fill = tile;
+    tile = tile + St::kBytes == NS * St::kBytes ? 0 : tile + St::kBytes;
     if (t >= wave_tiles) continue;
 
-    const uint32_t tile = (t % NS) * St::kBytes;
-    const uint32_t kr = lane & 31, hh = lane >> 5, px = (kr >> 1) & 7;
+    // (opaque, so that the steps' addresses are computed here and not kept)
+    uint32_t ta = ka + at, tb = kb + at, tv = va + at;
+    asm volatile("" : "+v"(ta), "+v"(tb), "+v"(tv));
+    auto key_frag = [&](int k) {
+      if (k < 8) return lds_read16(ta ^ ((2 * k) << 4));
+      const int i = k < DN / 16 ? k - 8 : k - DN / 16;
+      return lds_read16((tb ^ ((2 * i) << 4)) + (k < DN / 16 ? 0 : St::kPe - St::kB));
+    };
+    v8bf first[G];
+    read_group(first, key_frag);
     v16f s = {};
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      uint32_t at;
-      if (k < 8) at = tile + kr * 256 + (((2 * k) ^ hh ^ bitrev4(kr & 15)) << 4);
-      else if (k < DN / 16) at = tile + St::kB + kr * 128 + (((2 * (k - 8) + hh) ^ px) << 4);
-      else at = tile + St::kPe + kr * 128 + (((2 * (k - DN / 16) + hh) ^ px) << 4);
-      s = mfma_rows(lds_read16(at), q[k], s);
-    }
+    pipeline<kSteps, G>(first, key_frag, [&](int k, v8bf f) { s = mfma_rows(f, q[k], s); });
+    // Step i of the values: column tile i / 2 over keys 0-15 or 16-31.
+    auto value_frag = [&](int i) {
+      const int ct = i >> 1;
+      const uint32_t c0 = ((4 * ct) & 15) << 4, c1 = (ct >> 2) * 256 + (i & 1) * 16 * DV * 2;
+      return join_keys(lds_read_tr((tv ^ c0) + c1), lds_read_tr((tv ^ (c0 | 16)) + c1 + 8 * DV * 2));
+    };
+    read_group(first, value_frag);
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = s[i];
@@ -179,17 +200,13 @@ __global__ __launch_bounds__(64 * NW) void mla_prefill_kernel(MlaPrefillArgs a) 
     }
     float alpha;
     v8bf p[2];
-    if (softmax_step<32, 16>(x, a.c, m, l, alpha, p)) rescale(o, alpha);
-    const uint32_t i16 = lane & 15, vr = 4 * hh + (i16 >> 2);
-    const uint32_t va = tile + St::kV + vr * (DV * 2) + (i16 & 1) * 8;
-    const uint32_t vx = ((2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1)) ^ bitrev4(vr)) << 4;
+    if (softmax_step<32, 16>(x, a.c, m, l, alpha, p)) {
 #pragma unroll
-    for (int ct = 0; ct < kCols; ++ct) {
-      const uint32_t c0 = (((4 * ct) & 15) << 4), c1 = (ct >> 2) * 256;
-      const uint32_t at = va + (vx ^ c0) + c1, ae = va + 8 * DV * 2 + (vx ^ 16 ^ c0) + c1;
-      o[ct] = mfma_rows(join_keys(lds_read_tr(at), lds_read_tr(ae)), p[0], o[ct]);
-      o[ct] = mfma_rows(join_keys(lds_read_tr(at + 16 * DV * 2), lds_read_tr(ae + 16 * DV * 2)), p[1], o[ct]);
+      for (int i = 0; i < kCols; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] *= alpha;
     }
+    pipeline<2 * kCols, G>(first, value_frag, [&](int i, v8bf f) { o[i >> 1] = mfma_rows(f, p[i & 1], o[i >> 1]); });
   }
 
   l = rows_sum<32>(l);
@@ -212,12 +229,10 @@ __global__ __launch_bounds__(64 * NW) void mla_prefill_kernel(MlaPrefillArgs a) 
 
 hipError_t launch_mla_prefill(const MlaPrefillArgs& p, int dn, int dv, int cus, hipStream_t stream) {
   (void)cus;
-  constexpr int NW = 4;
   // at most one part-filled block per sequence
-  const int64_t blocks = p.Tq / (32 * NW) + (p.Tq < p.B ? p.Tq : p.B);
-  const dim3 grid((unsigned)(blocks * p.H));
-  if (dn == 192) mla_prefill_kernel<192, 256, NW, 4><<<grid, 64 * NW, 0, stream>>>(p);
-  else mla_prefill_kernel<128, 128, NW, 4><<<grid, 64 * NW, 0, stream>>>(p);
+  auto grid = [&](int rows) { return dim3((unsigned)((p.Tq / rows + (p.Tq < p.B ? p.Tq : p.B)) * p.H)); };
+  if (dn == 192) mla_prefill_kernel<192, 256, 8, 4><<<grid(256), 512, 0, stream>>>(p);
+  else mla_prefill_kernel<128, 128, 4, 4><<<grid(128), 256, 0, stream>>>(p);
   return hipGetLastError();
 }
 
