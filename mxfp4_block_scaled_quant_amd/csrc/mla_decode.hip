@@ -195,21 +195,25 @@ __device__ __forceinline__ void attend_tile(uint32_t tile, Rows<RW>& st, float& 
                                             bool full, int seen, uint32_t bad) {
   constexpr int NX = RW / 2;
   float x[NX];
-  const uint32_t i16 = lane & 15;
-  // Step i of the scores: for 16 rows, keys 0-15 and 16-31 in turn.
+  // Lane addresses: rows start at multiples of their length, so a step's
+  // chunk is one XOR away and its row group an immediate offset.  (Opaque, so
+  // that the steps' addresses are computed here and not kept in registers.)
   const uint32_t row = lane % RW, part = lane / RW;  // the lane's key row and its 8-value piece of a step
-  const uint32_t ka = tile + row * 1024, kx = (part ^ bitrev4(row & 15)) << 4;
-  const uint32_t pa = tile + kPeOff + row * 128, px = (row >> 1) & 7;
+  const uint32_t i16 = lane & 15, vrow = 4 * (lane >> (RW == 16 ? 4 : 5)) + (i16 >> 2);
+  const uint32_t vchunk = (RW == 16 ? 0 : 2 * ((lane >> 4) & 1)) + ((i16 & 3) >> 1);
+  uint32_t ka = tile + row * 1024 + ((part ^ bitrev4(row & 15)) << 4);
+  uint32_t pa = tile + kPeOff + row * 128 + ((part ^ ((row >> 1) & 7)) << 4);
+  uint32_t va = tile + vrow * 1024 + (i16 & 1) * 8 + ((vchunk ^ bitrev4(vrow)) << 4);
+  asm volatile("" : "+v"(ka), "+v"(pa), "+v"(va));
+  // Step i of the scores: for 16 rows, keys 0-15 and 16-31 in turn.
   auto key_frag = [&](int i) {
     if constexpr (RW == 16) {
       const int k = i >> 1;
-      const uint32_t a = k < 16 ? ka + (kx ^ ((4 * (k & 3)) << 4)) + (k >> 2) * 256 + (i & 1) * 16 * 1024
-                                : pa + (((4 * (k - 16) + part) ^ px) << 4) + (i & 1) * 16 * 128;
-      return lds_read16(a);
+      if (k < 16) return lds_read16((ka ^ ((4 * (k & 3)) << 4)) + (k >> 2) * 256 + (i & 1) * 16 * 1024);
+      return lds_read16((pa ^ ((4 * (k - 16)) << 4)) + (i & 1) * 16 * 128);
     } else {
-      const uint32_t a = i < 32 ? ka + (kx ^ ((2 * (i & 7)) << 4)) + (i >> 3) * 256
-                                : pa + (((2 * (i - 32) + part) ^ px) << 4);
-      return lds_read16(a);
+      if (i < 32) return lds_read16((ka ^ ((2 * (i & 7)) << 4)) + (i >> 3) * 256);
+      return lds_read16(pa ^ ((2 * (i - 32)) << 4));
     }
   };
   v8bf first[4];
@@ -221,23 +225,21 @@ __device__ __forceinline__ void attend_tile(uint32_t tile, Rows<RW>& st, float& 
     for (int i = 0; i < 8; ++i) x[i] = s[i >> 2][i & 3];
   } else {
     v16f s = {};
-    pipeline<36, 4>(first, key_frag, [&](int i, v8bf f) { s = mfma_rows(f, st.q[i], s); });
+    pipeline<36, 4>(first, key_frag, [&](int i, v8bf f) { mfma_vgpr(s, f, st.q[i]); });
+    mfma_settle(s);
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = s[i];
   }
   // Step i of the values: for 16 rows column tile i over all keys, for 32
   // rows column tile i / 2 over keys 0-15 or 16-31.
-  const uint32_t vrow = 4 * (lane >> (RW == 16 ? 4 : 5)) + (i16 >> 2);
-  const uint32_t vchunk = (RW == 16 ? 0 : 2 * ((lane >> 4) & 1)) + ((i16 & 3) >> 1);
-  const uint32_t va = tile + vrow * 1024 + (i16 & 1) * 8, vx = (vchunk ^ bitrev4(vrow)) << 4;
   auto value_frag = [&](int i) {
     if constexpr (RW == 16) {
-      const uint32_t a = va + (vx ^ (((2 * i) & 15) << 4)) + (i >> 3) * 256;
+      const uint32_t a = (va ^ (((2 * i) & 15) << 4)) + (i >> 3) * 256;
       return join_keys(lds_read_tr(a), lds_read_tr(a + 16 * 1024));
     } else {
       const int ct = i >> 1;
       const uint32_t c0 = ((4 * ct) & 15) << 4, c1 = (ct >> 2) * 256 + (i & 1) * 16 * 1024;
-      return join_keys(lds_read_tr(va + (vx ^ c0) + c1), lds_read_tr(va + 8 * 1024 + (vx ^ 16 ^ c0) + c1));
+      return join_keys(lds_read_tr((va ^ c0) + c1), lds_read_tr((va ^ (c0 | 16)) + c1 + 8 * 1024));
     }
   };
   read_group(first, value_frag);

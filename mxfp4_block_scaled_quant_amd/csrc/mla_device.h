@@ -108,6 +108,15 @@ __device__ __forceinline__ v16f mfma_rows(v8bf a, v8bf b, v16f c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
+// The 32 x 32 product with its result in vector registers, for kernels whose
+// other accumulators fill all accumulation registers.  The compiler counts no
+// wait states after an assembly statement: mfma_settle() stands between the
+// last product and the first use of the sum.
+__device__ __forceinline__ void mfma_vgpr(v16f& c, v8bf a, v8bf b) {
+  asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void mfma_settle(v16f& c) { asm volatile("s_nop 15\n\ts_nop 7" : "+v"(c)); }
+
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
