@@ -532,17 +532,16 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   }
 }
 
-// The parts of query row `r` of sequence b in a list: calls f(o, ml) for
-// each, in key order.  whole: one part that the list wrote by row.
+// The workgroups that hold pieces of query row r of sequence b in a list:
+// count 0 if the sequence is empty, 1 if one workgroup held the whole item.
 struct Parts {
-  int first, count;   // workgroups that hold pieces; count 0: none, 1: whole
+  int first, count;
 };
 template <int RB>
 __device__ __forceinline__ Parts find_parts(const ListArgs& a, int b, int r) {
   constexpr int kUnit = unit_tiles<RB>() * kTile;
-  int before = 0, total = 0;
-  const int chunk = (a.B + 127) / 128, b0 = threadIdx.x * chunk, b1 = min(a.B, b0 + chunk);
-  for (int i = b0; i < b1; ++i) {
+  int before = 0, total = 0;  // units of the sequences before b, and of all (each wave by itself)
+  for (int i = threadIdx.x & 63; i < a.B; i += 64) {
     const int u = a.nt * units_of<kUnit>(list_len(a, i));
     if (i < b) before += u;
     total += u;
@@ -552,15 +551,6 @@ __device__ __forceinline__ Parts find_parts(const ListArgs& a, int b, int r) {
     before += __shfl_xor(before, d);
     total += __shfl_xor(total, d);
   }
-  __shared__ int s[4];
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) {
-    s[(threadIdx.x >> 6) * 2] = before;
-    s[(threadIdx.x >> 6) * 2 + 1] = total;
-  }
-  __syncthreads();
-  before = s[0] + s[2];
-  total = s[1] + s[3];
   const int units = units_of<kUnit>(list_len(a, b));
   if (units == 0) return {0, 0};
   const int u0 = before + r / RB * units;
@@ -570,11 +560,16 @@ __device__ __forceinline__ Parts find_parts(const ListArgs& a, int b, int r) {
   return {w0, w1 - w0 + 1};
 }
 
-// One workgroup of 128 threads per query row joins its parts: four columns a
-// thread.  Rows that one workgroup of a call without a prefix wrote itself
-// are left alone; rows without any key become 0 and -inf.
+// One workgroup of four waves per query row joins its parts.  Wave w takes
+// parts w, w + 4, ..: its lanes fetch 64 parts' maxima and sums at once, then
+// the wave runs over the parts' 512 values, 8 a lane; the four waves' sums
+// meet in LDS in wave order.  Rows that one workgroup of a call without a
+// prefix wrote itself are left alone; rows without any key become 0 and -inf.
 template <int RB, int PRB>
-__global__ __launch_bounds__(128) void mla_join_kernel(ListArgs a, ListArgs p) {
+__global__ __launch_bounds__(256) void mla_join_kernel(ListArgs a, ListArgs p) {
+  __shared__ v4f so[4][kLatent / 4];
+  __shared__ float sml[4][2];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int b = blockIdx.x / a.rows, r = blockIdx.x - b * a.rows;
   const RowId id = row_id(a, b, r);
   const int64_t flat = flat_row(a.d, id);
@@ -582,50 +577,76 @@ __global__ __launch_bounds__(128) void mla_join_kernel(ListArgs a, ListArgs p) {
   if (!PRB && own.count == 1) return;
   Parts pre = {0, 0};
   if constexpr (PRB != 0) pre = find_parts<PRB>(p, 0, (int)flat);
-  const int col = threadIdx.x * 4;
-  float m = kNegInf, l = 0;
-  v4f o = {0, 0, 0, 0};
+  // Part i's row: (list, slot row); whole items lie by query row.
   auto part_at = [&](int i, const float*& po, const float*& pm) {
-    if (i < pre.count) {
-      if (pre.count == 1) {
-        po = p.ipart + flat * kLatent;
-        pm = p.ipml + 2 * flat;
-      } else {
-        const int64_t k = (int64_t)(2 * (pre.first + i) + (i == 0)) * PRB + (int)(flat % (PRB ? PRB : 1));
-        po = p.part + k * kLatent;
-        pm = p.pml + 2 * k;
-      }
-    } else {
-      i -= pre.count;
-      if (own.count == 1) {
-        po = a.ipart + flat * kLatent;
-        pm = a.ipml + 2 * flat;
-      } else {
-        const int64_t k = (int64_t)(2 * (own.first + i) + (i == 0)) * RB + r % RB;
-        po = a.part + k * kLatent;
-        pm = a.pml + 2 * k;
-      }
-    }
+    const bool in_prefix = PRB != 0 && i < pre.count;
+    const ListArgs& g = in_prefix ? p : a;
+    const Parts& q = in_prefix ? pre : own;
+    i -= in_prefix ? 0 : pre.count;
+    const bool whole = q.count == 1;
+    const int64_t k = whole ? flat
+                      : in_prefix ? (int64_t)(2 * (q.first + i) + (i == 0)) * PRB + (int)(flat % (PRB ? PRB : 1))
+                                  : (int64_t)(2 * (q.first + i) + (i == 0)) * RB + r % RB;
+    po = (whole ? g.ipart : g.part) + k * kLatent;
+    pm = (whole ? g.ipml : g.pml) + 2 * k;
   };
   const int count = pre.count + own.count;
-  for (int i = 0; i < count; ++i) {
+  float m = kNegInf, l = 0;
+  v4f o[2] = {};
+  for (int i0 = wv; i0 < count; i0 += 256) {  // 64 parts of this wave
+    const int mine = i0 + 4 * lane, n = min(64, (count - i0 + 3) / 4);
     const float *po, *pm;
-    part_at(i, po, pm);
-    m = fmaxf(m, pm[0]);
-  }
-#pragma unroll 4
-  for (int i = 0; i < count; ++i) {
-    const float *po, *pm;
-    part_at(i, po, pm);
-    const v4f v = *(const v4f*)(po + col);
-    const float li = pm[1], f = li == 0 ? 0.0f : __builtin_amdgcn_exp2f(pm[0] - m);
-    l += li * f;
+    float pmx = kNegInf, pl = 0;
+    if (lane < n) {
+      part_at(mine, po, pm);
+      pmx = pm[0];
+      pl = pm[1];
+    }
+    float mn = pmx;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] += li == 0 ? 0.0f : v[e] * f;
+    for (int d = 1; d < 64; d <<= 1) mn = fmaxf(mn, __shfl_xor(mn, d));
+    mn = fmaxf(mn, m);
+    const float keep = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
+    const float f = pl == 0 ? 0.0f : __builtin_amdgcn_exp2f(pmx - mn);  // a part without keys counts nothing
+    float ls = pl * f;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) ls += __shfl_xor(ls, d);
+    l = l * keep + ls;
+    m = mn;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e >> 2][e & 3] *= keep;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float fi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
+      part_at(i0 + 4 * i, po, pm);
+      const v4f v0 = *(const v4f*)(po + 4 * lane), v1 = *(const v4f*)(po + 256 + 4 * lane);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        o[0][e] += fi == 0 ? 0.0f : v0[e] * fi;
+        o[1][e] += fi == 0 ? 0.0f : v1[e] * fi;
+      }
+    }
+  }
+  so[wv][lane] = o[0];
+  so[wv][64 + lane] = o[1];
+  if (lane == 0) {
+    sml[wv][0] = m;
+    sml[wv][1] = l;
+  }
+  __syncthreads();
+  if (threadIdx.x >= 128) return;
+  m = fmaxf(fmaxf(sml[0][0], sml[1][0]), fmaxf(sml[2][0], sml[3][0]));
+  l = 0;
+  v4f t = {0, 0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float lw = sml[w][1], f = lw == 0 ? 0.0f : __builtin_amdgcn_exp2f(sml[w][0] - m);
+    l += lw * f;
+    t += so[w][threadIdx.x] * f;
   }
   const float inv = l == 0 ? 0.0f : 1.0f / l;
-  const uint2 w = {pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
-  *(uint2*)(a.d.out + id.b * a.d.sob + id.s * a.d.sos + id.h * a.d.soh + col) = w;
+  const uint2 w = {pack_bf16x2(t[0] * inv, t[1] * inv), pack_bf16x2(t[2] * inv, t[3] * inv)};
+  *(uint2*)(a.d.out + id.b * a.d.sob + id.s * a.d.sos + id.h * a.d.soh + 4 * threadIdx.x) = w;
   if (a.d.lse && threadIdx.x == 0)
     a.d.lse[flat] = l > 0 ? (m + __builtin_amdgcn_logf(l)) * kLn2 : l == 0 ? kNegInf : l;
 }
@@ -646,10 +667,10 @@ template <int PRB>
 void launch_join(int rb, const ListArgs& a, const ListArgs& p, hipStream_t s) {
   const int grid = a.B * a.rows;
   switch (rb) {
-    case 16: mla_join_kernel<16, PRB><<<grid, 128, 0, s>>>(a, p); break;
-    case 32: mla_join_kernel<32, PRB><<<grid, 128, 0, s>>>(a, p); break;
-    case 64: mla_join_kernel<64, PRB><<<grid, 128, 0, s>>>(a, p); break;
-    default: mla_join_kernel<128, PRB><<<grid, 128, 0, s>>>(a, p); break;
+    case 16: mla_join_kernel<16, PRB><<<grid, 256, 0, s>>>(a, p); break;
+    case 32: mla_join_kernel<32, PRB><<<grid, 256, 0, s>>>(a, p); break;
+    case 64: mla_join_kernel<64, PRB><<<grid, 256, 0, s>>>(a, p); break;
+    default: mla_join_kernel<128, PRB><<<grid, 256, 0, s>>>(a, p); break;
   }
 }
 
