@@ -58,9 +58,15 @@ PagedRows paged(const void* cache, int64_t pages, int64_t page_size, int64_t cac
   r.row_bytes = cache_row * 2;
   r.pages = (int)pages;
   r.page_size = (int)page_size;
-  r.shift = -1;
-  for (int i = 0; i < 31; ++i)
-    if (page_size == (1ll << i)) r.shift = i;
+  // magic = floor(2^(32 + shift) / d) + 1 exceeds 2^(32 + shift) / d by at
+  // most 1, so the quotient is exact while t * d <= 2^(32 + shift): with
+  // 2^(shift + 2) > d that holds for every t < 2^30.
+  if (page_size == 1) {
+    r.whole = ~0u;
+  } else {
+    while ((2ll << (r.shift + 1)) <= page_size) ++r.shift;
+    r.magic = (uint32_t)((1ull << (32 + r.shift)) / (uint64_t)page_size + 1);
+  }
   return r;
 }
 

@@ -125,7 +125,7 @@ __device__ __forceinline__ void find_share(const ListArgs& a, int w, int& b, int
 
 // The address of key t's row, given its page number (-1: none).
 __device__ __forceinline__ uint32_t page_of(const PagedRows& k, uint32_t t) {
-  return k.shift >= 0 ? t >> k.shift : t / (uint32_t)k.page_size;
+  return (__umulhi(t, k.magic) >> k.shift) + (t & k.whole);
 }
 __device__ __forceinline__ const char* row_at(const PagedRows& k, uint32_t t, int page, bool& ok) {
   ok = (uint32_t)page < (uint32_t)k.pages;
@@ -187,76 +187,110 @@ __device__ __forceinline__ void clear(Rows<RW>& s) {
     for (int j = 0; j < RW * RW / 64; ++j) s.o[i][j] = 0;
 }
 
-// One 32-key tile in LDS: scores, softmax step, values.  `seen` (per lane):
-// keys below it are visible to the lane's row; `bad`: bit t set if key t is
-// masked for every row; `full`: nothing is masked.
+// Where a lane reads a tile's operands: rows start at multiples of their
+// length, so a step's chunk is one XOR away and its row group an immediate
+// offset.
 template <int RW>
-__device__ __forceinline__ void attend_tile(uint32_t tile, Rows<RW>& st, float& m, float& l, float c, uint32_t lane,
-                                            bool full, int seen, uint32_t bad) {
-  constexpr int NX = RW / 2;
-  float x[NX];
-  // Lane addresses: rows start at multiples of their length, so a step's
-  // chunk is one XOR away and its row group an immediate offset.  (Opaque, so
-  // that the steps' addresses are computed here and not kept in registers.)
-  const uint32_t row = lane % RW, part = lane / RW;  // the lane's key row and its 8-value piece of a step
-  const uint32_t i16 = lane & 15, vrow = 4 * (lane >> (RW == 16 ? 4 : 5)) + (i16 >> 2);
-  const uint32_t vchunk = (RW == 16 ? 0 : 2 * ((lane >> 4) & 1)) + ((i16 & 3) >> 1);
-  uint32_t ka = tile + row * 1024 + ((part ^ bitrev4(row & 15)) << 4);
-  uint32_t pa = tile + kPeOff + row * 128 + ((part ^ ((row >> 1) & 7)) << 4);
-  uint32_t va = tile + vrow * 1024 + (i16 & 1) * 8 + ((vchunk ^ bitrev4(vrow)) << 4);
-  asm volatile("" : "+v"(ka), "+v"(pa), "+v"(va));
+struct LaneAddr {
+  uint32_t k, pe, v;
+  __device__ __forceinline__ explicit LaneAddr(uint32_t lane) {
+    const uint32_t row = lane % RW, part = lane / RW;  // the lane's key row and its 8-value piece of a step
+    const uint32_t i16 = lane & 15, vrow = 4 * (lane >> (RW == 16 ? 4 : 5)) + (i16 >> 2);
+    const uint32_t vchunk = (RW == 16 ? 0 : 2 * ((lane >> 4) & 1)) + ((i16 & 3) >> 1);
+    k = row * 1024 + ((part ^ bitrev4(row & 15)) << 4);
+    pe = kPeOff + row * 128 + ((part ^ ((row >> 1) & 7)) << 4);
+    v = vrow * 1024 + (i16 & 1) * 8 + ((vchunk ^ bitrev4(vrow)) << 4);
+  }
+};
+// The same within one tile, opaque, so that the steps' addresses are computed
+// where they are used and not kept in registers.
+template <int RW>
+struct TileAddr {
+  uint32_t k, pe, v;
+  __device__ __forceinline__ TileAddr(const LaneAddr<RW>& l, uint32_t tile) : k(l.k + tile), pe(l.pe + tile), v(l.v + tile) {
+    asm volatile("" : "+v"(k), "+v"(pe), "+v"(v));
+  }
   // Step i of the scores: for 16 rows, keys 0-15 and 16-31 in turn.
-  auto key_frag = [&](int i) {
+  __device__ __forceinline__ v8bf key(int i) const {
     if constexpr (RW == 16) {
-      const int k = i >> 1;
-      if (k < 16) return lds_read16((ka ^ ((4 * (k & 3)) << 4)) + (k >> 2) * 256 + (i & 1) * 16 * 1024);
-      return lds_read16((pa ^ ((4 * (k - 16)) << 4)) + (i & 1) * 16 * 128);
+      const int s = i >> 1;
+      if (s < 16) return lds_read16((k ^ ((4 * (s & 3)) << 4)) + (s >> 2) * 256 + (i & 1) * 16 * 1024);
+      return lds_read16((pe ^ ((4 * (s - 16)) << 4)) + (i & 1) * 16 * 128);
     } else {
-      if (i < 32) return lds_read16((ka ^ ((2 * (i & 7)) << 4)) + (i >> 3) * 256);
-      return lds_read16(pa ^ ((2 * (i - 32)) << 4));
+      if (i < 32) return lds_read16((k ^ ((2 * (i & 7)) << 4)) + (i >> 3) * 256);
+      return lds_read16(pe ^ ((2 * (i - 32)) << 4));
     }
-  };
-  v8bf first[4];
-  read_group(first, key_frag);
-  if constexpr (RW == 16) {
-    v4f s[2] = {};
-    pipeline<36, 4>(first, key_frag, [&](int i, v8bf f) { s[i & 1] = mfma_rows(f, st.q[i >> 1], s[i & 1]); });
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = s[i >> 2][i & 3];
-  } else {
-    v16f s = {};
-    pipeline<36, 4>(first, key_frag, [&](int i, v8bf f) { mfma_vgpr(s, f, st.q[i]); });
-    mfma_settle(s);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = s[i];
   }
   // Step i of the values: for 16 rows column tile i over all keys, for 32
   // rows column tile i / 2 over keys 0-15 or 16-31.
-  auto value_frag = [&](int i) {
+  __device__ __forceinline__ v8bf value(int i) const {
     if constexpr (RW == 16) {
-      const uint32_t a = (va ^ (((2 * i) & 15) << 4)) + (i >> 3) * 256;
+      const uint32_t a = (v ^ (((2 * i) & 15) << 4)) + (i >> 3) * 256;
       return join_keys(lds_read_tr(a), lds_read_tr(a + 16 * 1024));
     } else {
       const int ct = i >> 1;
       const uint32_t c0 = ((4 * ct) & 15) << 4, c1 = (ct >> 2) * 256 + (i & 1) * 16 * 1024;
-      return join_keys(lds_read_tr((va ^ c0) + c1), lds_read_tr((va ^ (c0 | 16)) + c1 + 8 * 1024));
-    }
-  };
-  read_group(first, value_frag);
-  if (!full) {
-#pragma unroll
-    for (int i = 0; i < NX; ++i) {
-      const int t = key_of<RW>(i, lane);
-      if (t >= seen || ((bad >> t) & 1)) x[i] = kNegInf;
+      return join_keys(lds_read_tr((v ^ c0) + c1), lds_read_tr((v ^ (c0 | 16)) + c1 + 8 * 1024));
     }
   }
-  float alpha;
-  v8bf p[NX / 8];
-  if (softmax_step<RW, NX>(x, c, m, l, alpha, p)) rescale(st.o, alpha);
-  pipeline<32, 4>(first, value_frag, [&](int i, v8bf f) {
+};
+
+// Hides masked keys' scores: `seen` (per lane): keys below it are visible to
+// the lane's row; `bad`: bit t set if key t is masked for every row.
+template <int RW, int NX>
+__device__ __forceinline__ void mask_scores(float (&x)[NX], uint32_t lane, int seen, uint32_t bad) {
+  asm volatile("" : "+v"(lane));  // (keeps the keys' numbers out of registers elsewhere)
+#pragma unroll
+  for (int i = 0; i < NX; ++i) {
+    const int t = key_of<RW>(i, lane);
+    if (t >= seen || ((bad >> t) & 1)) x[i] = kNegInf;
+  }
+}
+
+// Product i of the 36 of a 32-row score tile.
+__device__ __forceinline__ void score_product(v16f& s, int i, v8bf f, v8bf q) {
+  if (i == 0) mfma_vgpr<true, false>(s, f, q);
+  else if (i == 35) mfma_vgpr<false, true>(s, f, q);
+  else mfma_vgpr<false, false>(s, f, q);
+}
+
+template <int RW>
+__device__ __forceinline__ void tile_values(const TileAddr<RW>& at, v8bf (&first)[4], Rows<RW>& st,
+                                            const v8bf (&p)[RW / 16]) {
+  pipeline<32, 4>(first, [&](int i) { return at.value(i); }, [&](int i, v8bf f) {
     if constexpr (RW == 16) st.o[i] = mfma_rows(f, p[0], st.o[i]);
     else st.o[i >> 1] = mfma_rows(f, p[i & 1], st.o[i >> 1]);
   });
+}
+
+// One 32-key tile in LDS: scores, softmax step, values; `full`: nothing is masked.
+template <int RW>
+__device__ __forceinline__ void attend_tile(uint32_t tile, const LaneAddr<RW>& la, Rows<RW>& st, float& m, float& l,
+                                            float c, uint32_t lane, bool full, int seen, uint32_t bad) {
+  constexpr int NX = RW / 2;
+  float x[NX];
+  const TileAddr<RW> at(la, tile);
+  auto key = [&](int i) { return at.key(i); };
+  auto value = [&](int i) { return at.value(i); };
+  v8bf first[4];
+  read_group(first, key);
+  if constexpr (RW == 16) {
+    v4f s[2] = {};
+    pipeline<36, 4>(first, key, [&](int i, v8bf f) { s[i & 1] = mfma_rows(f, st.q[i >> 1], s[i & 1]); });
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = s[i >> 2][i & 3];
+  } else {
+    v16f s;
+    pipeline<36, 4>(first, key, [&](int i, v8bf f) { score_product(s, i, f, st.q[i]); });
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = s[i];
+  }
+  read_group(first, value);
+  if (!full) mask_scores<RW, NX>(x, lane, seen, bad);
+  float alpha;
+  v8bf p[NX / 8];
+  if (softmax_step<RW, NX>(x, c, m, l, alpha, p)) rescale(st.o, alpha);
+  tile_values<RW>(at, first, st, p);
 }
 
 // Query row r of sequence b: its request, token and head.
@@ -323,6 +357,7 @@ __device__ __forceinline__ void attend_split(const ListArgs& a, int b, int n, in
   load_query<RW>(a, id, lane, st);
   clear(st);
   float m = kNegInf, l = 0;
+  const LaneAddr<RW> la(lane);
   const int32_t* table = a.table + b * a.ldt;
   int page = -1;
   {
@@ -340,7 +375,7 @@ __device__ __forceinline__ void attend_split(const ListArgs& a, int b, int n, in
     wait_lds();
     load_rows<32, 4>(tile, ptr, 0, 0, lane);
     wait_loads<0>();
-    attend_tile<RW>(tile, st, m, l, a.d.c, lane, bad == 0 && (t + 1) * kTile <= seen_all, seen - t * kTile, bad);
+    attend_tile<RW>(tile, la, st, m, l, a.d.c, lane, bad == 0 && (t + 1) * kTile <= seen_all, seen - t * kTile, bad);
   }
 
   // The four waves' accumulators meet: rescaled to the rows' common maximum,
@@ -433,43 +468,158 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
     for (int i = threadIdx.x; i < p1 - p0; i += 256) tab[i] = table[p0 + i];
   };
   auto covered = [&](int t) { return (int)page_of(a.d.cache, min(n, (t + 1) * kTile) - 1) < p1; };
-  auto issue = [&](int t, uint32_t& bad) {
+  // A tile's loads in two steps: the rows' addresses (lanes 0..31, and of
+  // the rotated parts this wave loads, lane by lane), then 9 loads a wave.
+  const char* ptr = nullptr;
+  const char* pe_ptr = nullptr;
+  // (Tiles past the end have no rows: their loads fetch zeros from the cache.)
+  const int end = min(n, t1 * kTile);
+  auto lookup = [&](int t) {
     const int key = t * kTile + (int)(lane & 31);
-    const int page = key < n ? tab[(int)page_of(a.d.cache, key) - p0] : -1;
-    bool ok;
-    const char* ptr = row_at(a.d.cache, key, page, ok);
-    bad = (uint32_t)__builtin_amdgcn_ballot_w64(!ok);
-    load_rows<8, 1>(((t - t0) & 3) * kTileBytes, ptr, wv * 8, wv, lane);
+    const int page = tab[min((int)page_of(a.d.cache, key), p1 - 1) - p0];
+    return key < end ? page : -1;
   };
-  window(t0);
-  __syncthreads();
-  uint32_t bad0 = 0, bad1 = 0, bad2 = 0, bad3 = 0;
-  issue(t0, bad0);
-  auto ahead = [&](int t, uint32_t& bad) {  // tile t's loads, past a window's end with a new window
-    if (t >= t1) return;
-    if (!covered(t)) {
+  auto locate = [&](int t, int page) {
+    bool ok;
+    ptr = row_at(a.d.cache, t * kTile + (lane & 31), page, ok);
+    const uint32_t r = 8 * wv + (lane >> 3);
+    pe_ptr = shuffle_ptr(ptr, r) + kLatent * 2 + ((lane & 7) ^ ((r >> 1) & 7)) * 16;
+    return (uint32_t)__builtin_amdgcn_ballot_w64(!ok);
+  };
+  auto load = [&](uint32_t stage, int i) {  // load i of 9
+    const int r = 8 * wv + i;
+    uint32_t at = lane * 16;
+    asm volatile("" : "+v"(at));  // (one register, not one per load)
+    if (i < 8) dma16(stage + r * 1024, lane_ptr(ptr, r), at ^ (bitrev4(r & 15) << 4));
+    else dma16_at(stage + kPeOff + wv * 1024, pe_ptr);
+  };
+  auto stage_of = [&](int t) { return ((t - t0) & 3) * kTileBytes; };
+  auto refill = [&](int t) {  // a new window if tile t's pages lie past this one
+    if (t < t1 && !covered(t)) {
       __syncthreads();
       window(t);
       __syncthreads();
     }
-    issue(t, bad);
   };
-  ahead(t0 + 1, bad1);
-  ahead(t0 + 2, bad2);
-  for (int t = t0; t < t1; ++t) {
-    // 9 loads a wave and tile; up to two later tiles stay in flight
-    if (t + 2 < t1) wait_loads<18>();
-    else if (t + 1 < t1) wait_loads<9>();
-    else wait_loads<0>();
-    wait_lds();
-    wave_barrier();  // tile t is whole, and tile t - 1 no longer read
-    ahead(t + 3, bad3);
-    attend_tile<RW>(((t - t0) & 3) * kTileBytes, st, m, l, a.d.c, lane, bad0 == 0 && (t + 1) * kTile <= seen_all,
-                    seen - t * kTile, bad0);
-    bad0 = bad1;
-    bad1 = bad2;
-    bad2 = bad3;
+  const LaneAddr<RW> la(lane);
+  window(t0);
+  __syncthreads();
+  // bad[i]: the masked keys of tile t + i
+  uint32_t bad[5] = {};
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    refill(t0 + i);
+    bad[i] = locate(t0 + i, lookup(t0 + i));
+#pragma unroll
+    for (int j = 0; j < 9; ++j) load(stage_of(t0 + i), j);
   }
+  if constexpr (RW == 16) {
+    for (int t = t0; t < t1; ++t) {
+      wait_loads<18>();  // two later tiles stay in flight
+      wait_lds();
+      wave_barrier();    // tile t is whole, and tile t - 1 no longer read
+      refill(t + 3);
+      bad[3] = locate(t + 3, lookup(t + 3));
+#pragma unroll
+      for (int j = 0; j < 9; ++j) load(stage_of(t + 3), j);
+      attend_tile<RW>(stage_of(t), la, st, m, l, a.d.c, lane, bad[0] == 0 && (t + 1) * kTile <= seen_all,
+                      seen - t * kTile, bad[0]);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) bad[i] = bad[i + 1];
+    }
+  } else {
+    // One wave a SIMD: nothing else fills the matrix unit while this wave
+    // does anything but issue products.  So tile t's softmax runs between the
+    // value products of tile t - 1, and the loads of tile t + 2 and the
+    // addresses of tile t + 3 between the score products of tile t.
+    auto full = [&](int t) { return bad[0] == 0 && (t + 1) * kTile <= seen_all; };
+    v8bf p[2];            // the probabilities of the tile before,
+    bool grew = false;    // whether its maxima rose, and by what the
+    float alpha = 1;      // accumulators are to be scaled then
+    wait_loads<18>();
+    wave_barrier();
+    {
+      const TileAddr<RW> at(la, stage_of(t0));
+      auto key = [&](int i) { return at.key(i); };
+      v8bf first[4];
+      read_group(first, key);
+      v16f s;
+      pipeline<36, 4>(first, key, [&](int i, v8bf f) { score_product(s, i, f, st.q[i]); });
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = s[i];
+      if (!full(t0)) mask_scores<RW, 16>(x, lane, seen - t0 * kTile, bad[0]);
+      softmax_step<RW, 16>(x, a.d.c, m, l, alpha, p);  // (nothing to rescale yet)
+    }
+    refill(t0 + 3);
+    bad[3] = locate(t0 + 3, lookup(t0 + 3));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad[i] = bad[i + 1];
+    for (int t = t0 + 1; t < t1; ++t) {
+      wait_loads<9>();  // tile t is there, t + 1 may be in flight
+      wait_lds();
+      wave_barrier();   // tile t is whole, and tile t - 2 no longer read
+      refill(t + 3);
+      const uint32_t fill = stage_of(t + 2);
+      v16f s;
+      {
+        const TileAddr<RW> at(la, stage_of(t));
+        auto key = [&](int i) { return at.key(i); };
+        v8bf first[4];
+        read_group(first, key);
+        int page = -1;
+        pipeline<36, 4>(first, key, [&](int i, v8bf f) {
+          score_product(s, i, f, st.q[i]);
+          if (i < 9) load(fill, i);
+          if (i == 15) page = lookup(t + 3);
+          if (i == 27) bad[3] = locate(t + 3, page);
+        });
+      }
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = s[i];
+      if (!full(t)) mask_scores<RW, 16>(x, lane, seen - t * kTile, bad[0]);
+      float mx = x[0], mu = 0;
+      if (grew) rescale(st.o, alpha);
+      const TileAddr<RW> at(la, stage_of(t - 1));
+      auto value = [&](int i) { return at.value(i); };
+      v8bf first[4];
+      read_group(first, value);
+      pipeline<32, 4>(first, value, [&](int i, v8bf f) {
+        st.o[i >> 1] = mfma_rows(f, p[i & 1], st.o[i >> 1]);
+        if (i == 0) {
+#pragma unroll
+          for (int j = 1; j < 16; ++j) mx = fmaxf(mx, x[j]);
+        } else if (i == 1) {
+          mx = rows_max<RW>(mx) * a.d.c;
+          const float mn = mx > m + kLag ? mx : m;
+          grew = __builtin_amdgcn_ballot_w64(mn != m) != 0;
+          alpha = mn == m ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+          m = mn;
+          mu = m == kNegInf ? 0.0f : m;
+          l *= alpha;
+        } else if (i >= 4 && i < 20) {
+          const int e = i - 4;
+          x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], a.d.c, -mu));
+          l += x[e];
+          asm volatile("" : "+v"(x[e]));  // here, not where the values are used
+        }
+      });
+#pragma unroll
+      for (int i = 0; i < 16; ++i) p[i >> 3][i & 7] = (__bf16)x[i];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) bad[i] = bad[i + 1];
+    }
+    if (grew) rescale(st.o, alpha);
+    {
+      const TileAddr<RW> at(la, stage_of(t1 - 1));
+      auto value = [&](int i) { return at.value(i); };
+      v8bf first[4];
+      read_group(first, value);
+      tile_values<RW>(at, first, st, p);
+    }
+  }
+  wait_loads<0>();
   __syncthreads();
 
   l = rows_sum<RW>(l);

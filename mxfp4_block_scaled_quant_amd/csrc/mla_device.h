@@ -108,14 +108,18 @@ __device__ __forceinline__ v16f mfma_rows(v8bf a, v8bf b, v16f c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// The 32 x 32 product with its result in vector registers, for kernels whose
-// other accumulators fill all accumulation registers.  The compiler counts no
-// wait states after an assembly statement: mfma_settle() stands between the
-// last product and the first use of the sum.
+// A chain of 32 x 32 products with its sum in vector registers, for kernels
+// whose other accumulators fill all accumulation registers.  The compiler
+// counts no wait states after an assembly statement, so the last product
+// carries the wait that its sum's first reader (or copy) needs.
+template <bool FIRST, bool LAST>
 __device__ __forceinline__ void mfma_vgpr(v16f& c, v8bf a, v8bf b) {
-  asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+  static_assert(!(FIRST && LAST), "a chain has two products at least");
+  if constexpr (FIRST) asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(c) : "v"(a), "v"(b));
+  else if constexpr (LAST)
+    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0\n\ts_nop 15\n\ts_nop 3" : "+v"(c) : "v"(a), "v"(b));
+  else asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
 }
-__device__ __forceinline__ void mfma_settle(v16f& c) { asm volatile("s_nop 15\n\ts_nop 7" : "+v"(c)); }
 
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f;
@@ -190,22 +194,20 @@ __device__ __forceinline__ void rescale(V (&o)[N], float alpha) {
 // latency behind G products and no more than two groups are in registers.
 // read(i) gives step i's operand, mul(i, operand) uses it; `first` holds
 // group 0, read ahead by the caller.
-template <int N, int G, typename T, typename Read, typename Mul>
-__device__ __forceinline__ void pipeline(T (&first)[G], Read read, Mul mul) {
+// (Recursion, not a loop: the operand registers need constant indices, and
+// the compiler does not unroll every such loop.)
+template <int N, int G, int AT = 0, typename T, typename Read, typename Mul>
+__device__ __forceinline__ void pipeline(T (&now)[G], Read read, Mul mul) {
   static_assert(N % G == 0, "whole groups");
-  T f[2][G];
+  T next[G];
+  if constexpr (AT + G < N) {
 #pragma unroll
-  for (int i = 0; i < G; ++i) f[0][i] = first[i];
-#pragma unroll
-  for (int g = 0; g < N / G; ++g) {
-    if (g + 1 < N / G) {
-#pragma unroll
-      for (int i = 0; i < G; ++i) f[(g + 1) & 1][i] = read((g + 1) * G + i);
-    }
-#pragma unroll
-    for (int i = 0; i < G; ++i) mul(g * G + i, f[g & 1][i]);
-    __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < G; ++i) next[i] = read(AT + G + i);
   }
+#pragma unroll
+  for (int i = 0; i < G; ++i) mul(AT + i, now[i]);
+  __builtin_amdgcn_sched_barrier(0);
+  if constexpr (AT + G < N) pipeline<N, G, AT + G>(next, read, mul);
 }
 template <int G, typename T, typename Read>
 __device__ __forceinline__ void read_group(T (&first)[G], Read read) {

@@ -16,7 +16,9 @@ struct PagedRows {
   const char* base;
   int64_t page_bytes, row_bytes;
   int pages, page_size;
-  int shift;                      // log2(page_size), or -1
+  // t / page_size for t < 2^30 as (mulhi(t, magic) >> shift) + (t & whole)
+  // (magic 0 and whole ~0 for pages of one row).
+  uint32_t magic, shift, whole;
 };
 
 struct AppendArgs {
