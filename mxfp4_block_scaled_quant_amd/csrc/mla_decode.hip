@@ -32,7 +32,11 @@ namespace mxfp4 {
 namespace {
 
 constexpr int kTile = 32;                                  // keys per LDS tile
-constexpr uint32_t kPeOff = kTile * kLatent * 2;           // the rotated parts follow the latents
+// A tile in LDS: nine blocks of 64 values (128 bytes) of all 32 rows, so that
+// a load covers 8 rows' whole cache lines and a lane that loads keeps one row
+// address for all nine.
+constexpr uint32_t kBlock = kTile * 128;
+constexpr int kBlocks = kRowDim / 64;
 constexpr uint32_t kTileBytes = kTile * kRowDim * 2;       // 36 KiB
 constexpr uint32_t kTabLds = 4 * kTileBytes;               // page numbers of the shared form's window
 constexpr int kTabEntries = 3584;
@@ -133,34 +137,18 @@ __device__ __forceinline__ const char* row_at(const PagedRows& k, uint32_t t, in
   return ok ? k.base + page * k.page_bytes + i * k.row_bytes : (const char*)zero_row;
 }
 
-__device__ __forceinline__ const char* lane_ptr(const char* p, int lane) {
-  const uint64_t v = (uint64_t)p;
-  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane);
-  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), lane);
-  return (const char*)((uint64_t)hi << 32 | lo);
+// Lane l loads, of each group of 8 rows, row l / 8's chunk l % 8 of every
+// block (permuted): its bytes past the row's address.
+__device__ __forceinline__ uint32_t load_chunk(uint32_t lane) {
+  return ((lane & 7) ^ swizzle128(lane >> 3)) * 16;
 }
-__device__ __forceinline__ const char* shuffle_ptr(const char* p, int lane) {
-  const uint64_t v = (uint64_t)p;
-  const uint32_t lo = __builtin_amdgcn_ds_bpermute(lane * 4, (int)(uint32_t)v);
-  const uint32_t hi = __builtin_amdgcn_ds_bpermute(lane * 4, (int)(uint32_t)(v >> 32));
-  return (const char*)((uint64_t)hi << 32 | lo);
+// Groups g and g ^ 1 differ in bit 3 of the row, which the swizzle maps to bit 0.
+__device__ __forceinline__ uint32_t load_chunk(uint32_t lane, uint32_t group) {
+  return load_chunk(lane) ^ ((group & 1) << 4);
 }
-
-// Loads rows [r0, r0 + NR) of a tile's latents, and the rotated parts of the
-// 8 rows of each group in [g0, g0 + NG); lanes 0..31 hold the rows' addresses.
-template <int NR, int NG>
-__device__ __forceinline__ void load_rows(uint32_t tile, const char* ptr, int r0, int g0, uint32_t lane) {
-  const char* pe[NG];
-#pragma unroll
-  for (int j = 0; j < NG; ++j) pe[j] = shuffle_ptr(ptr, 8 * (g0 + j) + (int)(lane >> 3));
-#pragma unroll
-  for (int i = 0; i < NR; ++i)
-    dma16(tile + (r0 + i) * 1024, lane_ptr(ptr, r0 + i), (lane ^ bitrev4((r0 + i) & 15)) * 16);
-#pragma unroll
-  for (int j = 0; j < NG; ++j) {
-    const uint32_t row = 8 * (g0 + j) + (lane >> 3);
-    dma16_at(tile + kPeOff + (g0 + j) * 1024, pe[j] + kLatent * 2 + ((lane & 7) ^ ((row >> 1) & 7)) * 16);
-  }
+template <int... J>
+__device__ __forceinline__ void load_group(uint32_t at, const char* p, std::integer_sequence<int, J...>) {
+  (dma16_at<J * 128>(at + J * kBlock, p), ...);
 }
 
 // Accumulators and query operands of RW query rows.
@@ -192,45 +180,42 @@ __device__ __forceinline__ void clear(Rows<RW>& s) {
 // offset.
 template <int RW>
 struct LaneAddr {
-  uint32_t k, pe, v;
+  uint32_t k, v;
   __device__ __forceinline__ explicit LaneAddr(uint32_t lane) {
     const uint32_t row = lane % RW, part = lane / RW;  // the lane's key row and its 8-value piece of a step
     const uint32_t i16 = lane & 15, vrow = 4 * (lane >> (RW == 16 ? 4 : 5)) + (i16 >> 2);
     const uint32_t vchunk = (RW == 16 ? 0 : 2 * ((lane >> 4) & 1)) + ((i16 & 3) >> 1);
-    k = row * 1024 + ((part ^ bitrev4(row & 15)) << 4);
-    pe = kPeOff + row * 128 + ((part ^ ((row >> 1) & 7)) << 4);
-    v = vrow * 1024 + (i16 & 1) * 8 + ((vchunk ^ bitrev4(vrow)) << 4);
+    k = row * 128 + ((part ^ swizzle128(row)) << 4);
+    v = vrow * 128 + (i16 & 1) * 8 + ((vchunk ^ swizzle128(vrow)) << 4);
   }
 };
 // The same within one tile, opaque, so that the steps' addresses are computed
 // where they are used and not kept in registers.
 template <int RW>
 struct TileAddr {
-  uint32_t k, pe, v;
-  __device__ __forceinline__ TileAddr(const LaneAddr<RW>& l, uint32_t tile) : k(l.k + tile), pe(l.pe + tile), v(l.v + tile) {
-    asm volatile("" : "+v"(k), "+v"(pe), "+v"(v));
+  uint32_t k, v;
+  __device__ __forceinline__ TileAddr(const LaneAddr<RW>& l, uint32_t tile) : k(l.k + tile), v(l.v + tile) {
+    asm volatile("" : "+v"(k), "+v"(v));
   }
   // Step i of the scores: for 16 rows, keys 0-15 and 16-31 in turn.
   __device__ __forceinline__ v8bf key(int i) const {
     if constexpr (RW == 16) {
       const int s = i >> 1;
-      if (s < 16) return lds_read16((k ^ ((4 * (s & 3)) << 4)) + (s >> 2) * 256 + (i & 1) * 16 * 1024);
-      return lds_read16((pe ^ ((4 * (s - 16)) << 4)) + (i & 1) * 16 * 128);
+      return lds_read16((k ^ ((s & 1) << 6)) + (s >> 1) * kBlock + (i & 1) * 16 * 128);
     } else {
-      if (i < 32) return lds_read16((k ^ ((2 * (i & 7)) << 4)) + (i >> 3) * 256);
-      return lds_read16(pe ^ ((2 * (i - 32)) << 4));
+      return lds_read16((k ^ ((i & 3) << 5)) + (i >> 2) * kBlock);
     }
   }
   // Step i of the values: for 16 rows column tile i over all keys, for 32
   // rows column tile i / 2 over keys 0-15 or 16-31.
   __device__ __forceinline__ v8bf value(int i) const {
     if constexpr (RW == 16) {
-      const uint32_t a = (v ^ (((2 * i) & 15) << 4)) + (i >> 3) * 256;
-      return join_keys(lds_read_tr(a), lds_read_tr(a + 16 * 1024));
+      const uint32_t a = (v ^ ((i & 3) << 5)) + (i >> 2) * kBlock;
+      return join_keys(lds_read_tr(a), lds_read_tr(a + 16 * 128));
     } else {
       const int ct = i >> 1;
-      const uint32_t c0 = ((4 * ct) & 15) << 4, c1 = (ct >> 2) * 256 + (i & 1) * 16 * 1024;
-      return join_keys(lds_read_tr((v ^ c0) + c1), lds_read_tr((v ^ (c0 | 16)) + c1 + 8 * 1024));
+      const uint32_t c0 = (ct & 1) << 6, c1 = (ct >> 1) * kBlock + (i & 1) * 16 * 128;
+      return join_keys(lds_read_tr((v ^ c0) + c1), lds_read_tr((v ^ (c0 | 16)) + c1 + 8 * 128));
     }
   }
 };
@@ -359,21 +344,35 @@ __device__ __forceinline__ void attend_split(const ListArgs& a, int b, int n, in
   float m = kNegInf, l = 0;
   const LaneAddr<RW> la(lane);
   const int32_t* table = a.table + b * a.ldt;
-  int page = -1;
-  {
-    const int t = (t0 + wv) * kTile + (int)(lane & 31);
-    if (t < n) page = table[page_of(a.d.cache, t)];
-  }
+  // Rows 8g + lane / 8 of a tile: page numbers one tile ahead.
+  int page[4];
+  auto lookup = [&](int t) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int key = t * kTile + 8 * g + (int)(lane >> 3);
+      page[g] = t < t1 && key < n ? table[page_of(a.d.cache, key)] : -1;
+    }
+  };
+  lookup(t0 + wv);
   for (int t = t0 + wv; t < t1; t += 4) {
-    bool ok;
-    const char* ptr = row_at(a.d.cache, t * kTile + (lane & 31), page, ok);
-    const uint32_t bad = (uint32_t)__builtin_amdgcn_ballot_w64(!ok);
-    // the next tile's page numbers, ahead of this tile's rows
-    page = -1;
-    const int nx = (t + 4) * kTile + (int)(lane & 31);
-    if (t + 4 < t1 && nx < n) page = table[page_of(a.d.cache, nx)];
+    const char* ptr[4];
+    uint64_t hidden[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      bool ok;
+      ptr[g] = row_at(a.d.cache, t * kTile + 8 * g + (lane >> 3), page[g], ok) + load_chunk(lane, g);
+      hidden[g] = __builtin_amdgcn_ballot_w64(!ok);
+    }
+    lookup(t + 4);
     wait_lds();
-    load_rows<32, 4>(tile, ptr, 0, 0, lane);
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      load_group(tile + g * 1024, ptr[g], std::make_integer_sequence<int, kBlocks>{});
+    uint32_t bad = 0;  // (seldom more than the keys past the end)
+    if ((hidden[0] | hidden[1] | hidden[2] | hidden[3]) != 0) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) bad |= (uint32_t)((hidden[i >> 3] >> (8 * (i & 7))) & 1) << i;
+    }
     wait_loads<0>();
     attend_tile<RW>(tile, la, st, m, l, a.d.c, lane, bad == 0 && (t + 1) * kTile <= seen_all, seen - t * kTile, bad);
   }
@@ -468,30 +467,28 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
     for (int i = threadIdx.x; i < p1 - p0; i += 256) tab[i] = table[p0 + i];
   };
   auto covered = [&](int t) { return (int)page_of(a.d.cache, min(n, (t + 1) * kTile) - 1) < p1; };
-  // A tile's loads in two steps: the rows' addresses (lanes 0..31, and of
-  // the rotated parts this wave loads, lane by lane), then 9 loads a wave.
+  // A tile's loads in three steps: page numbers (of the row this lane loads,
+  // and of key lane % 32), the row's address and the hidden keys, then the
+  // nine loads of this wave's 8 rows.  (Tiles past the end have no rows:
+  // their loads fetch zeros.)
   const char* ptr = nullptr;
-  const char* pe_ptr = nullptr;
-  // (Tiles past the end have no rows: their loads fetch zeros from the cache.)
+  const uint32_t chunk = load_chunk(lane, wv);
   const int end = min(n, t1 * kTile);
-  auto lookup = [&](int t) {
-    const int key = t * kTile + (int)(lane & 31);
+  auto page_at = [&](int key) {
     const int page = tab[min((int)page_of(a.d.cache, key), p1 - 1) - p0];
     return key < end ? page : -1;
   };
-  auto locate = [&](int t, int page) {
-    bool ok;
-    ptr = row_at(a.d.cache, t * kTile + (lane & 31), page, ok);
-    const uint32_t r = 8 * wv + (lane >> 3);
-    pe_ptr = shuffle_ptr(ptr, r) + kLatent * 2 + ((lane & 7) ^ ((r >> 1) & 7)) * 16;
-    return (uint32_t)__builtin_amdgcn_ballot_w64(!ok);
+  auto lookup = [&](int t, int& mine, int& all) {
+    mine = page_at(t * kTile + 8 * wv + (int)(lane >> 3));
+    all = page_at(t * kTile + (int)(lane & 31));
   };
-  auto load = [&](uint32_t stage, int i) {  // load i of 9
-    const int r = 8 * wv + i;
-    uint32_t at = lane * 16;
-    asm volatile("" : "+v"(at));  // (one register, not one per load)
-    if (i < 8) dma16(stage + r * 1024, lane_ptr(ptr, r), at ^ (bitrev4(r & 15) << 4));
-    else dma16_at(stage + kPeOff + wv * 1024, pe_ptr);
+  auto locate = [&](int t, int mine, int all) {
+    bool ok;
+    ptr = row_at(a.d.cache, t * kTile + 8 * wv + (lane >> 3), mine, ok) + chunk;
+    return (uint32_t)__builtin_amdgcn_ballot_w64((uint32_t)all >= (uint32_t)a.d.cache.pages);
+  };
+  auto load = [&](uint32_t stage) {
+    load_group(stage + wv * 1024, ptr, std::make_integer_sequence<int, kBlocks>{});
   };
   auto stage_of = [&](int t) { return ((t - t0) & 3) * kTileBytes; };
   auto refill = [&](int t) {  // a new window if tile t's pages lie past this one
@@ -509,9 +506,10 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
     refill(t0 + i);
-    bad[i] = locate(t0 + i, lookup(t0 + i));
-#pragma unroll
-    for (int j = 0; j < 9; ++j) load(stage_of(t0 + i), j);
+    int mine, all;
+    lookup(t0 + i, mine, all);
+    bad[i] = locate(t0 + i, mine, all);
+    load(stage_of(t0 + i));
   }
   if constexpr (RW == 16) {
     for (int t = t0; t < t1; ++t) {
@@ -519,9 +517,10 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
       wait_lds();
       wave_barrier();    // tile t is whole, and tile t - 1 no longer read
       refill(t + 3);
-      bad[3] = locate(t + 3, lookup(t + 3));
-#pragma unroll
-      for (int j = 0; j < 9; ++j) load(stage_of(t + 3), j);
+      int mine, all;
+      lookup(t + 3, mine, all);
+      bad[3] = locate(t + 3, mine, all);
+      load(stage_of(t + 3));
       attend_tile<RW>(stage_of(t), la, st, m, l, a.d.c, lane, bad[0] == 0 && (t + 1) * kTile <= seen_all,
                       seen - t * kTile, bad[0]);
 #pragma unroll
@@ -552,7 +551,9 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
       softmax_step<RW, 16>(x, a.d.c, m, l, alpha, p);  // (nothing to rescale yet)
     }
     refill(t0 + 3);
-    bad[3] = locate(t0 + 3, lookup(t0 + 3));
+    int mine, all;
+    lookup(t0 + 3, mine, all);
+    bad[3] = locate(t0 + 3, mine, all);
 #pragma unroll
     for (int i = 0; i < 4; ++i) bad[i] = bad[i + 1];
     for (int t = t0 + 1; t < t1; ++t) {
@@ -567,12 +568,12 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
         auto key = [&](int i) { return at.key(i); };
         v8bf first[4];
         read_group(first, key);
-        int page = -1;
-        pipeline<36, 4>(first, key, [&](int i, v8bf f) {
+        pipeline<36, 4>(first, key, [&](auto ic, v8bf f) {
+          constexpr int i = ic;
           score_product(s, i, f, st.q[i]);
-          if (i < 9) load(fill, i);
-          if (i == 15) page = lookup(t + 3);
-          if (i == 27) bad[3] = locate(t + 3, page);
+          if constexpr (i < 9) dma16_at<i * 128>(fill + wv * 1024 + i * kBlock, ptr);
+          else if constexpr (i == 15) lookup(t + 3, mine, all);
+          else if constexpr (i == 27) bad[3] = locate(t + 3, mine, all);
         });
       }
       float x[16];

@@ -22,6 +22,9 @@
 // transposing reads of V touch every bank once.
 #pragma once
 
+#include <type_traits>
+#include <utility>
+
 #include "mxfp4_device.h"
 
 namespace mxfp4 {
@@ -46,6 +49,13 @@ __device__ __forceinline__ v8bf join_keys(v4s a, v4s b) {
   return __builtin_bit_cast(v8bf, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// Reverses 3 bits of the row's pair number: the swizzle of 128-byte rows, of
+// which a 256-byte bank line holds two.  16 rows' equal chunks fall on 16
+// different slots (K reads), and so do the chunk pairs of 8 rows and the
+// chunk quads of 4 rows (V reads).
+__host__ __device__ constexpr uint32_t swizzle128(uint32_t row) {
+  return ((row & 2) << 1) | ((row & 4) >> 1) | ((row & 8) >> 3);
+}
 // Reverses 4 bits: the swizzle of rows whose length is a multiple of 256
 // bytes.  16 rows' equal chunks fall on 16 different slots (K reads), and so
 // do the chunk pairs of 8 rows and the chunk quads of 4 rows (V reads).
@@ -54,17 +64,20 @@ __host__ __device__ constexpr uint32_t bitrev4(uint32_t r) {
 }
 
 // Direct loads of 16 bytes per lane to LDS at `lds` + 16 lane, from a
-// uniform base plus a lane's byte offset, or from a lane's own address.
-// (M0 holds the LDS base; one wait state after it is written.  A base that a
-// vector instruction wrote, as v_readlane does, needs five before the load:
-// the compiler does not count them into an assembly statement.)
+// uniform base plus a lane's byte offset, or OFF bytes past a lane's own
+// address.  (M0 holds the LDS base; one wait state after it is written.  A
+// base that a vector instruction wrote would need five: the compiler does
+// not count them into an assembly statement, so there are four here.)
 __device__ __forceinline__ void dma16(uint32_t lds, const void* base, uint32_t voff) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2"
                :: "s"(lds), "v"(voff), "s"(base) : "memory", "m0");
 }
+// (The instruction adds its immediate offset to the LDS address too.)
+template <int OFF>
 __device__ __forceinline__ void dma16_at(uint32_t lds, const void* p) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-               :: "s"(lds), "v"(p) : "memory", "m0");
+  lds -= OFF;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2"
+               :: "s"(lds), "v"(p), "i"(OFF) : "memory", "m0");
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -192,27 +205,30 @@ __device__ __forceinline__ void rescale(V (&o)[N], float alpha) {
 // next group's reads are issued before this group's products, and nothing
 // moves between groups, so that a wave alone on its SIMD hides the LDS
 // latency behind G products and no more than two groups are in registers.
-// read(i) gives step i's operand, mul(i, operand) uses it; `first` holds
-// group 0, read ahead by the caller.
-// (Recursion, not a loop: the operand registers need constant indices, and
-// the compiler does not unroll every such loop.)
+// read(i) gives step i's operand, mul(i, operand) uses it, i a compile-time
+// constant; `now` holds group 0, read ahead by the caller.  (Recursion, not
+// a loop: the operand registers need constant indices, and the compiler does
+// not unroll every such loop.)
+template <int AT, typename T, int G, typename Mul, int... I>
+__device__ __forceinline__ void multiply_group(T (&now)[G], Mul& mul, std::integer_sequence<int, I...>) {
+  (mul(std::integral_constant<int, AT + I>{}, now[I]), ...);
+}
+template <int AT, typename T, int G, typename Read, int... I>
+__device__ __forceinline__ void read_group_at(T (&next)[G], Read& read, std::integer_sequence<int, I...>) {
+  ((next[I] = read(AT + I)), ...);
+}
 template <int N, int G, int AT = 0, typename T, typename Read, typename Mul>
 __device__ __forceinline__ void pipeline(T (&now)[G], Read read, Mul mul) {
   static_assert(N % G == 0, "whole groups");
   T next[G];
-  if constexpr (AT + G < N) {
-#pragma unroll
-    for (int i = 0; i < G; ++i) next[i] = read(AT + G + i);
-  }
-#pragma unroll
-  for (int i = 0; i < G; ++i) mul(AT + i, now[i]);
+  if constexpr (AT + G < N) read_group_at<AT + G>(next, read, std::make_integer_sequence<int, G>{});
+  multiply_group<AT>(now, mul, std::make_integer_sequence<int, G>{});
   __builtin_amdgcn_sched_barrier(0);
   if constexpr (AT + G < N) pipeline<N, G, AT + G>(next, read, mul);
 }
 template <int G, typename T, typename Read>
 __device__ __forceinline__ void read_group(T (&first)[G], Read read) {
-#pragma unroll
-  for (int i = 0; i < G; ++i) first[i] = read(i);
+  read_group_at<0>(first, read, std::make_integer_sequence<int, G>{});
   __builtin_amdgcn_sched_barrier(0);
 }
 
