@@ -624,30 +624,59 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
   __syncthreads();
 
   l = rows_sum<RW>(l);
-  const bool real = r0 + (int)(lane % RW) < a.rows;
-  if (!real) return;
   const int r_in_block = wv * RW + lane % RW;
-  const bool direct = to.whole && !a.ipart;
-  const float inv = l == 0 ? 0.0f : 1.0f / l;
-  float* part = direct ? nullptr : part_row<RB>(a, to, id, r_in_block);
-  uint16_t* out = a.d.out + id.b * a.d.sob + id.s * a.d.sos + id.h * a.d.soh;
+  auto column = [&](int i, int j) {  // of a lane's values 4j..4j+3 of column tile i
+    return i * RW + (RW == 16 ? 4 * (int)(lane >> 4) : 8 * j + 4 * (int)(lane >> 5));
+  };
+  if (!to.whole) {
+    // A part goes out through the wave's share of LDS, so that whole lines
+    // are stored (in registers a lane holds 4 columns of its row); rows past
+    // the last are stored too, into their place in the part.
+    constexpr int C = 256, LD = C * 4 + 16;  // columns per pass, padded row bytes
+    constexpr int kPer = Rows<RW>::kCols * C / 512;
+    const uint32_t mine = wv * kTileBytes;
+    float* part = a.part + ((int64_t)to.slot * RB + wv * RW) * kLatent + 4 * lane;
 #pragma unroll
-  for (int i = 0; i < Rows<RW>::kCols; ++i) {
+    for (int pass = 0; pass < 512 / C; ++pass) {
 #pragma unroll
-    for (int j = 0; j < RW * RW / 256; ++j) {
-      const uint32_t col = i * RW + (RW == 16 ? 4 * (lane >> 4) : 8 * j + 4 * (lane >> 5));
-      v4f v;
+      for (int i = 0; i < kPer; ++i) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = st.o[i][4 * j + e];
-      if (direct) {
-        const uint2 w = {pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
-        *(uint2*)(out + col) = w;
-      } else {
-        *(v4f*)(part + col) = v;
+        for (int j = 0; j < RW * RW / 256; ++j) {
+          v4f v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = st.o[pass * kPer + i][4 * j + e];
+          *(lds_v4f_t)(uintptr_t)(mine + (lane % RW) * LD + column(i, j) * 4) = v;
+        }
+      }
+      wait_lds();
+#pragma unroll 8
+      for (int r = 0; r < RW; ++r)
+        *(v4f*)(part + r * kLatent + pass * C) = *(lds_v4f_t)(uintptr_t)(mine + r * LD + lane * 16);
+      wait_lds();
+    }
+  } else if (r0 + (int)(lane % RW) < a.rows) {
+    const bool direct = !a.ipart;
+    const float inv = l == 0 ? 0.0f : 1.0f / l;
+    float* part = direct ? nullptr : a.ipart + flat_row(a.d, id) * kLatent;
+    uint16_t* out = a.d.out + id.b * a.d.sob + id.s * a.d.sos + id.h * a.d.soh;
+#pragma unroll
+    for (int i = 0; i < Rows<RW>::kCols; ++i) {
+#pragma unroll
+      for (int j = 0; j < RW * RW / 256; ++j) {
+        v4f v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = st.o[i][4 * j + e];
+        if (direct) {
+          const uint2 w = {pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
+          *(uint2*)(out + column(i, j)) = w;
+        } else {
+          *(v4f*)(part + column(i, j)) = v;
+        }
       }
     }
   }
-  if (lane < RW) store_ml<RB>(a, to, id, r_in_block, m, l);
+  if (lane < RW && r0 + (int)lane < a.rows) store_ml<RB>(a, to, id, r_in_block, m, l);
+  __syncthreads();
 }
 
 template <int RB>
