@@ -682,12 +682,9 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
 template <int RB>
 __device__ constexpr int unit_tiles() { return RB <= 32 ? 4 : 2; }
 
+// This workgroup's share of one list.
 template <int RB>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void mla_attend_kernel(ListArgs a) {
-  __shared__ int4 lds_raw[kLdsBytes / 16];
-  uint32_t anchor = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int4*)lds_raw;
-  asm volatile("" : "+s"(anchor)::"memory");  // LDS is addressed by number: its array starts at 0
-
+__device__ __forceinline__ void attend_list(const ListArgs& a) {
   constexpr int kUnitTiles = unit_tiles<RB>(), kUnit = kUnitTiles * kTile;
   const int w = blockIdx.x;
   int b, base, lo, hi;
@@ -710,6 +707,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       attend_shared<RB / 4>(a, b, n, rt, u0 * kUnitTiles, min(tiles, u1 * kUnitTiles), to);
     cur += u1 - u0;
   }
+}
+
+// One list (PRB = 0), or a prefix's list and then the requests' own: a
+// workgroup that has stored its prefix part starts on its requests at once.
+template <int RB, int PRB>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void mla_attend_kernel(ListArgs a,
+                                                                                                   ListArgs p) {
+  __shared__ int4 lds_raw[kLdsBytes / 16];
+  uint32_t anchor = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int4*)lds_raw;
+  asm volatile("" : "+s"(anchor)::"memory");  // LDS is addressed by number: its array starts at 0
+  if constexpr (PRB != 0) attend_list<PRB>(p);
+  attend_list<RB>(a);
 }
 
 // The workgroups that hold pieces of query row r of sequence b in a list:
@@ -835,12 +844,14 @@ int rows_per_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : ro
 int unit_keys(int rb) { return rb <= 32 ? 4 * kTile : 2 * kTile; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-void launch_attend(int rb, const ListArgs& a, hipStream_t s) {
+template <int PRB>
+void launch_attend(int rb, const ListArgs& a, const ListArgs& p, hipStream_t s) {
+  const int grid = PRB && p.grid > a.grid ? p.grid : a.grid;
   switch (rb) {
-    case 16: mla_attend_kernel<16><<<a.grid, 256, 0, s>>>(a); break;
-    case 32: mla_attend_kernel<32><<<a.grid, 256, 0, s>>>(a); break;
-    case 64: mla_attend_kernel<64><<<a.grid, 256, 0, s>>>(a); break;
-    default: mla_attend_kernel<128><<<a.grid, 256, 0, s>>>(a); break;
+    case 16: mla_attend_kernel<16, PRB><<<grid, 256, 0, s>>>(a, p); break;
+    case 32: mla_attend_kernel<32, PRB><<<grid, 256, 0, s>>>(a, p); break;
+    case 64: mla_attend_kernel<64, PRB><<<grid, 256, 0, s>>>(a, p); break;
+    default: mla_attend_kernel<128, PRB><<<grid, 256, 0, s>>>(a, p); break;
   }
 }
 template <int PRB>
@@ -915,10 +926,16 @@ hipError_t launch_mla_decode(const DecodeArgs& d, const DecodePlan& plan, hipStr
     p.pml = d.work + plan.ppml;
     p.ipart = a.ipart + all * kLatent;
     p.ipml = a.ipml + 2 * all;
-    launch_attend(plan.prows, p, stream);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    launch_attend(plan.rows, a, stream);
+    // (Fewer rows than a block of 128 in the whole batch: two launches, and
+    // no code of their own for every pair of forms.)
+    hipError_t e;
+    if (plan.prows == 128) {
+      launch_attend<128>(plan.rows, a, p, stream);
+    } else {
+      launch_attend<0>(plan.prows, p, p, stream);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      launch_attend<0>(plan.rows, a, a, stream);
+    }
     if ((e = hipGetLastError()) != hipSuccess) return e;
     switch (plan.prows) {
       case 16: launch_join<16>(plan.rows, a, p, stream); break;
@@ -928,7 +945,7 @@ hipError_t launch_mla_decode(const DecodeArgs& d, const DecodePlan& plan, hipStr
     }
     return hipGetLastError();
   }
-  launch_attend(plan.rows, a, stream);
+  launch_attend<0>(plan.rows, a, a, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   launch_join<0>(plan.rows, a, a, stream);
