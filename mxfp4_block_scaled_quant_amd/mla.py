@@ -15,26 +15,46 @@ from typing import Optional
 
 import torch
 
-from . import _check, _ptr, _require_cuda, _stream, lib
+from . import _check, _require_cuda, lib
 
 LATENT_DIM = 512
 ROPE_DIM = 64
 ROW_DIM = LATENT_DIM + ROPE_DIM
 
 
-def _require(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: torch.device) -> None:
-    """t has this dtype and shape (-1: any size) on `device` and unit stride along its last dimension."""
-    if t.dtype != dtype or t.device != device or t.dim() != len(shape) or any(
-            w >= 0 and n != w for n, w in zip(t.shape, shape)):
+# These calls run once per layer and decoding step, where a call's time on the
+# host is the call's time: the checks are written out (no generators), device
+# addresses go to ctypes as plain integers, and the stream's handle is asked
+# for without building a stream object.
+
+def _require(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: torch.device):
+    """t has this dtype and shape (-1: any size) on `device` and unit stride
+    along its last dimension; returns its strides."""
+    size, strides = t.shape, t.stride()
+    ok = t.dtype is dtype and t.device == device and len(size) == len(shape)
+    if ok:
+        for n, w in zip(size, shape):
+            if n != w and w >= 0:
+                ok = False
+    if not ok:
         want = ", ".join("any" if w < 0 else str(w) for w in shape)
-        raise ValueError(f"{name} must be {dtype} [{want}] on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be {dtype} [{want}] on {device}, got {t.dtype} {tuple(size)} on {t.device}")
+    if strides[-1] != 1 and size[-1] > 1 and t.numel():
         raise ValueError(f"{name} must have unit stride along its last dimension")
+    return strides
 
 
 def _require_contiguous(t: torch.Tensor, name: str) -> None:
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _addr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(device: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def mla_decode_workspace_bytes(B: int, S: int, H: int, max_tokens: int, prefix_len: int = 0) -> int:
@@ -57,31 +77,33 @@ def mla_cache_append(kv: torch.Tensor, norm_weight: torch.Tensor, cache: torch.T
     """
     _require_cuda(kv, "kv")
     dev = kv.device
-    _require(kv, "kv", torch.bfloat16, (-1, ROW_DIM), dev)
+    kv_strides = _require(kv, "kv", torch.bfloat16, (-1, ROW_DIM), dev)
     T = kv.shape[0]
     _require(norm_weight, "norm_weight", torch.bfloat16, (LATENT_DIM,), dev)
-    _require(cache, "cache", torch.bfloat16, (-1, -1, ROW_DIM), dev)
+    cache_strides = _require(cache, "cache", torch.bfloat16, (-1, -1, ROW_DIM), dev)
+    pages, page_size, _ = cache.shape
     _require(slots, "slots", torch.int64, (T,), dev)
     _require(positions, "positions", torch.int64, (T,), dev)
     _require(cos_sin, "cos_sin", torch.float32, (-1, ROPE_DIM), dev)
     _require_contiguous(cos_sin, "cos_sin")
     H = 0
+    rotated = (None, 0, 0, None, 0, 0)
     if q_pe is not None:
-        _require(q_pe, "q_pe", torch.bfloat16, (T, -1, ROPE_DIM), dev)
+        q_strides = _require(q_pe, "q_pe", torch.bfloat16, (T, -1, ROPE_DIM), dev)
         H = q_pe.shape[1]
         if q_out is None:
             q_out = torch.empty((T, H, ROPE_DIM), dtype=torch.bfloat16, device=dev)
-        else:
-            _require(q_out, "q_out", torch.bfloat16, (T, H, ROPE_DIM), dev)
+        o_strides = _require(q_out, "q_out", torch.bfloat16, (T, H, ROPE_DIM), dev)
+        if H:
+            rotated = (q_pe.data_ptr(), q_strides[0], q_strides[1], q_out.data_ptr(), o_strides[0], o_strides[1])
     elif q_out is not None:
         raise ValueError("q_out is given without q_pe")
-    with_q = q_pe is not None and H > 0
-    _check("mla_cache_append", lib().mla_cache_append(
-        _ptr(kv), kv.stride(0), _ptr(norm_weight), eps, _ptr(cos_sin), cos_sin.shape[0], _ptr(positions),
-        _ptr(slots), int(interleaved),
-        _ptr(q_pe) if with_q else None, q_pe.stride(0) if with_q else 0, q_pe.stride(1) if with_q else 0,
-        _ptr(q_out) if with_q else None, q_out.stride(0) if with_q else 0, q_out.stride(1) if with_q else 0,
-        _ptr(cache), cache.shape[0], cache.shape[1], cache.stride(0), cache.stride(1), T, H, _stream(dev)))
+    status = lib().mla_cache_append(
+        kv.data_ptr(), kv_strides[0], norm_weight.data_ptr(), eps, cos_sin.data_ptr(), cos_sin.shape[0],
+        positions.data_ptr(), slots.data_ptr(), 1 if interleaved else 0, *rotated, cache.data_ptr(), pages, page_size,
+        cache_strides[0], cache_strides[1], T, H, _raw_stream(dev))
+    if status:
+        _check("mla_cache_append", status)
     return q_out
 
 
@@ -93,43 +115,47 @@ def _decode(fn, q, cache, prefix, block_table, lengths, scale, return_lse, out, 
         q = q.unsqueeze(1)
         out = None if out is None else out.unsqueeze(1)
         lse = None if lse is None else lse.unsqueeze(1)
-    _require(q, "q", torch.bfloat16, (-1, -1, -1, ROW_DIM), dev)
+    q_strides = _require(q, "q", torch.bfloat16, (-1, -1, -1, ROW_DIM), dev)
     B, S, H, _ = q.shape
-    _require(cache, "cache", torch.bfloat16, (-1, -1, ROW_DIM), dev)
-    _require(block_table, "block_table", torch.int32, (B, -1), dev)
+    cache_strides = _require(cache, "cache", torch.bfloat16, (-1, -1, ROW_DIM), dev)
+    pages, page_size, _ = cache.shape
+    table_strides = _require(block_table, "block_table", torch.int32, (B, -1), dev)
+    width = block_table.shape[1]
     _require(lengths, "lengths", torch.int32, (B,), dev)
     _require_contiguous(lengths, "lengths")
-    pages, page_size = cache.shape[0], cache.shape[1]
-    width = block_table.shape[1]
-    prefix_table, prefix_len = prefix if prefix else (None, 0)
-    if prefix_table is not None:
+    shared, prefix_len = (), 0
+    if prefix is not None:
+        prefix_table, prefix_len = prefix
         _require(prefix_table, "prefix_table", torch.int32, (-1,), dev)
         _require_contiguous(prefix_table, "prefix_table")
-        if not 0 <= prefix_len <= prefix_table.shape[0] * page_size:
-            raise ValueError(f"prefix_len {prefix_len} does not fit prefix_table's {prefix_table.shape[0]} pages")
+        prefix_pages = prefix_table.shape[0]
+        if not 0 <= prefix_len <= prefix_pages * page_size:
+            raise ValueError(f"prefix_len {prefix_len} does not fit prefix_table's {prefix_pages} pages")
+        shared = (prefix_table.data_ptr(), prefix_pages, prefix_len)
     if out is None:
         out = torch.empty((B, S, H, LATENT_DIM), dtype=torch.bfloat16, device=dev)
-    else:
-        _require(out, "out", torch.bfloat16, (B, S, H, LATENT_DIM), dev)
+    out_strides = _require(out, "out", torch.bfloat16, (B, S, H, LATENT_DIM), dev)
     if lse is not None:
         _require(lse, "lse", torch.float32, (B, S, H), dev)
         _require_contiguous(lse, "lse")
     elif return_lse:
         lse = torch.empty((B, S, H), dtype=torch.float32, device=dev)
-    need = mla_decode_workspace_bytes(B, S, H, width * page_size, prefix_len)
+    handle = lib()
+    need = handle.mla_decode_workspace_bytes(B, S, H, width * page_size, prefix_len)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif (workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous()
-          or workspace.numel() < need):
-        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {dev}")
-    args = [_ptr(q), q.stride(0), q.stride(1), q.stride(2), _ptr(cache), pages, page_size, cache.stride(0),
-            cache.stride(1)]
-    if prefix_table is not None:
-        args += [_ptr(prefix_table), prefix_table.shape[0], prefix_len]
-    args += [_ptr(block_table), max(block_table.stride(0), width), width, _ptr(lengths), B, S, H, scale, _ptr(out),
-             out.stride(0), out.stride(1), out.stride(2), _ptr(lse), _ptr(workspace), workspace.numel(),
-             _stream(dev)]
-    _check(fn, getattr(lib(), fn)(*args))
+    else:
+        _require(workspace, "workspace", torch.uint8, (-1,), dev)
+        _require_contiguous(workspace, "workspace")
+        if workspace.shape[0] < need:
+            raise ValueError(f"workspace holds {workspace.shape[0]} bytes, {need} needed")
+    status = getattr(handle, fn)(
+        q.data_ptr(), q_strides[0], q_strides[1], q_strides[2], cache.data_ptr(), pages, page_size, cache_strides[0],
+        cache_strides[1], *shared, block_table.data_ptr(), max(table_strides[0], width), width, lengths.data_ptr(),
+        B, S, H, scale, out.data_ptr(), out_strides[0], out_strides[1], out_strides[2], _addr(lse),
+        workspace.data_ptr(), workspace.shape[0], _raw_stream(dev))
+    if status:
+        _check(fn, status)
     if three:
         out = out.squeeze(1)
         lse = None if lse is None else lse.squeeze(1)
@@ -176,15 +202,15 @@ def mla_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: to
     """
     _require_cuda(q, "q")
     dev = q.device
-    _require(v, "v", torch.bfloat16, (-1, -1, -1), dev)
+    v_strides = _require(v, "v", torch.bfloat16, (-1, -1, -1), dev)
     Tk, H, dv = v.shape
     dn = {128: 128, 256: 192}.get(dv)
     if dn is None:
         raise ValueError(f"v must have 128 or 256 values a head, got {dv}")
-    _require(q, "q", torch.bfloat16, (-1, H, dn + ROPE_DIM), dev)
+    q_strides = _require(q, "q", torch.bfloat16, (-1, H, dn + ROPE_DIM), dev)
     Tq = q.shape[0]
-    _require(k_nope, "k_nope", torch.bfloat16, (Tk, H, dn), dev)
-    _require(k_pe, "k_pe", torch.bfloat16, (Tk, ROPE_DIM), dev)
+    k_strides = _require(k_nope, "k_nope", torch.bfloat16, (Tk, H, dn), dev)
+    pe_strides = _require(k_pe, "k_pe", torch.bfloat16, (Tk, ROPE_DIM), dev)
     _require(cu_q, "cu_q", torch.int32, (-1,), dev)
     B = cu_q.shape[0] - 1
     if B < 0:
@@ -194,15 +220,16 @@ def mla_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: to
     _require_contiguous(cu_k, "cu_k")
     if out is None:
         out = torch.empty((Tq, H, dv), dtype=torch.bfloat16, device=dev)
-    else:
-        _require(out, "out", torch.bfloat16, (Tq, H, dv), dev)
+    out_strides = _require(out, "out", torch.bfloat16, (Tq, H, dv), dev)
     if lse is not None:
         _require(lse, "lse", torch.float32, (Tq, H), dev)
         _require_contiguous(lse, "lse")
     elif return_lse:
         lse = torch.empty((Tq, H), dtype=torch.float32, device=dev)
-    _check("mla_prefill", lib().mla_prefill(
-        _ptr(q), q.stride(0), q.stride(1), _ptr(k_nope), k_nope.stride(0), k_nope.stride(1), _ptr(k_pe),
-        k_pe.stride(0), _ptr(v), v.stride(0), v.stride(1), _ptr(cu_q), _ptr(cu_k), B, H, Tq, Tk, dn, dv,
-        int(causal), scale, _ptr(out), out.stride(0), out.stride(1), _ptr(lse), _stream(dev)))
+    status = lib().mla_prefill(
+        q.data_ptr(), q_strides[0], q_strides[1], k_nope.data_ptr(), k_strides[0], k_strides[1], k_pe.data_ptr(),
+        pe_strides[0], v.data_ptr(), v_strides[0], v_strides[1], cu_q.data_ptr(), cu_k.data_ptr(), B, H, Tq, Tk, dn,
+        dv, 1 if causal else 0, scale, out.data_ptr(), out_strides[0], out_strides[1], _addr(lse), _raw_stream(dev))
+    if status:
+        _check("mla_prefill", status)
     return (out, lse) if return_lse else out
