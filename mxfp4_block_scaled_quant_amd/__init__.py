@@ -98,6 +98,7 @@ _SIGNATURES = {
     "mla_prefill": (_c_int, [_c_vp, _c_i64, _c_i64] * 2 + [_c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp]
                     + [_c_i64] * 6 + [_c_int, _c_f32, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp]),
     "mxfp4_testing_set_gemm_path": (_c_int, [_c_int]),
+    "mla_testing_set_rows": (_c_int, [_c_int]),
 }
 
 _lib_handle = None

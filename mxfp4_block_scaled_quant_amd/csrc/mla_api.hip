@@ -5,10 +5,16 @@
 #include <stdint.h>
 
 #include "../../include/mxfp4.h"
+#include "../../include/mxfp4_testing.h"
 #include "mla_launch.h"
 #include "mxfp4_launch.h"
 
 namespace mxfp4 {
+
+// The test hook's forced row block: per thread, like the GEMM path's.
+static thread_local int t_rows = 0;
+int get_mla_rows_override() { return t_rows; }
+
 namespace {
 
 constexpr int64_t kMaxRows = 1 << 22;      // query rows of a decode call
@@ -269,6 +275,13 @@ int mla_prefill(const void* q, int64_t q_token, int64_t q_head, const void* k_no
   p.soh = out_head;
   p.lse = (float*)lse;
   return launched(launch_mla_prefill(p, (int)dn, (int)dv, cus, (hipStream_t)stream));
+}
+
+// Test hook (include/mxfp4_testing.h): force the decode form on this thread.
+int mla_testing_set_rows(int rows) {
+  if (rows != 0 && rows != 16 && rows != 32 && rows != 64 && rows != 128) return MXFP4_ERR_ARG;
+  t_rows = rows;
+  return MXFP4_OK;
 }
 
 }  // extern "C"

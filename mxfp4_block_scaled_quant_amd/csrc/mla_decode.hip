@@ -257,19 +257,22 @@ __device__ __forceinline__ void attend_tile(uint32_t tile, const LaneAddr<RW>& l
   const TileAddr<RW> at(la, tile);
   auto key = [&](int i) { return at.key(i); };
   auto value = [&](int i) { return at.value(i); };
-  v8bf first[4];
-  read_group(first, key);
   if constexpr (RW == 16) {
+    v8bf ahead[4];
+    read_group(ahead, key);
     v4f s[2] = {};
-    pipeline<36, 4>(first, key, [&](int i, v8bf f) { s[i & 1] = mfma_rows(f, st.q[i >> 1], s[i & 1]); });
+    pipeline<36, 4>(ahead, key, [&](int i, v8bf f) { s[i & 1] = mfma_rows(f, st.q[i >> 1], s[i & 1]); });
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = s[i >> 2][i & 3];
   } else {
+    v8bf ahead[3];  // (groups of three: the registers end there)
+    read_group(ahead, key);
     v16f s;
-    pipeline<36, 4>(first, key, [&](int i, v8bf f) { score_product(s, i, f, st.q[i]); });
+    pipeline<36, 3>(ahead, key, [&](int i, v8bf f) { score_product(s, i, f, st.q[i]); });
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = s[i];
   }
+  v8bf first[4];
   read_group(first, value);
   if (!full) mask_scores<RW, NX>(x, lane, seen, bad);
   float alpha;
@@ -311,10 +314,6 @@ struct Dest {
 };
 
 template <int RB>
-__device__ __forceinline__ float* part_row(const ListArgs& a, const Dest& to, const RowId& id, int r_in_block) {
-  return to.whole ? a.ipart + flat_row(a.d, id) * kLatent : a.part + ((int64_t)to.slot * RB + r_in_block) * kLatent;
-}
-template <int RB>
 __device__ __forceinline__ void store_ml(const ListArgs& a, const Dest& to, const RowId& id, int r_in_block, float m,
                                          float l) {
   if (to.whole && !a.ipart) {
@@ -355,19 +354,16 @@ __device__ __forceinline__ void attend_split(const ListArgs& a, int b, int n, in
   };
   lookup(t0 + wv);
   for (int t = t0 + wv; t < t1; t += 4) {
-    const char* ptr[4];
     uint64_t hidden[4];
+    wait_lds();
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       bool ok;
-      ptr[g] = row_at(a.d.cache, t * kTile + 8 * g + (lane >> 3), page[g], ok) + load_chunk(lane, g);
+      const char* ptr = row_at(a.d.cache, t * kTile + 8 * g + (lane >> 3), page[g], ok) + load_chunk(lane, g);
       hidden[g] = __builtin_amdgcn_ballot_w64(!ok);
+      load_group(tile + g * 1024, ptr, std::make_integer_sequence<int, kBlocks>{});
     }
     lookup(t + 4);
-    wait_lds();
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-      load_group(tile + g * 1024, ptr[g], std::make_integer_sequence<int, kBlocks>{});
     uint32_t bad = 0;  // (seldom more than the keys past the end)
     if ((hidden[0] | hidden[1] | hidden[2] | hidden[3]) != 0) {
 #pragma unroll
@@ -379,6 +375,7 @@ __device__ __forceinline__ void attend_split(const ListArgs& a, int b, int n, in
 
   // The four waves' accumulators meet: rescaled to the rows' common maximum,
   // through the wave's own tile, summed in wave order.
+  acc_settle();
   l = rows_sum<RW>(l);
   lds_f32_t ml = (lds_f32_t)(uintptr_t)kMiscLds;
   if (lane < RW) {
@@ -400,6 +397,19 @@ __device__ __forceinline__ void attend_split(const ListArgs& a, int b, int n, in
   float mm, ll;
   joined(lane % RW, mm, ll);
   const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - mm);
+  const bool direct = to.whole && !a.ipart;
+  // Per row, for the stores: the factor of an output, and where the row goes.
+  lds_f32_t inv = (lds_f32_t)(uintptr_t)(kMiscLds + 1024);
+  lds_i64_t off = (lds_i64_t)(uintptr_t)(kMiscLds + 1024 + 32 * 4);
+  if (threadIdx.x < RW) {
+    inv[lane] = !direct ? 1.0f : ll == 0 ? 0.0f : 1.0f / ll;
+    off[lane] = direct     ? id.b * a.d.sob + id.s * a.d.sos + id.h * a.d.soh
+                : to.whole ? flat_row(a.d, id) * kLatent
+                           : ((int64_t)to.slot * RW + lane) * kLatent;
+    if (r0 + (int)lane < a.rows) store_ml<RW>(a, to, id, lane, mm, ll);
+  }
+  float* part = to.whole ? a.ipart : a.part;
+  const int rows = min(RW, a.rows - r0);
   constexpr int C = RW == 16 ? 512 : 256, LD = C * 4 + 16;  // columns per pass, padded row bytes
   constexpr int kPer = Rows<RW>::kCols * C / 512;
 #pragma unroll
@@ -411,35 +421,29 @@ __device__ __forceinline__ void attend_split(const ListArgs& a, int b, int n, in
         const uint32_t col = i * RW + (RW == 16 ? 4 * (lane >> 4) : 8 * j + 4 * (lane >> 5));
         v4f v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = st.o[pass * kPer + i][4 * j + e] * f;
+        for (int e = 0; e < 4; ++e) v[e] = acc_read(st.o[pass * kPer + i][4 * j + e]) * f;
         *(lds_v4f_t)(uintptr_t)(tile + (lane % RW) * LD + col * 4) = v;
       }
     }
     __syncthreads();
-#pragma unroll
+#pragma unroll 4
     for (int it = 0; it < RW * C / 1024; ++it) {
       const int e = it * 256 + threadIdx.x, r = e / (C / 4), col = e % (C / 4) * 4;
       v4f v = {0, 0, 0, 0};
 #pragma unroll
       for (int w = 0; w < 4; ++w) v += *(lds_v4f_t)(uintptr_t)(w * kTileBytes + r * LD + col * 4);
-      if (r0 + r < a.rows) {
-        const RowId ri = row_id(a, b, r0 + r);
-        if (to.whole && !a.ipart) {
-          float rm, rl;
-          joined(r, rm, rl);
-          const float inv = rl == 0 ? 0.0f : 1.0f / rl;
-          const uint2 w = {pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
-          *(uint2*)(a.d.out + ri.b * a.d.sob + ri.s * a.d.sos + ri.h * a.d.soh + pass * C + col) = w;
+      if (r < rows) {
+        const int64_t at = off[r] + pass * C + col;
+        if (direct) {
+          v *= inv[r];
+          *(uint2*)(a.d.out + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
         } else {
-          *(v4f*)(part_row<RW>(a, to, ri, r) + pass * C + col) = v;
+          *(v4f*)(part + at) = v;
         }
       }
     }
     __syncthreads();
   }
-  if (threadIdx.x < RW && r0 + (int)threadIdx.x < a.rows)
-    store_ml<RW>(a, to, row_id(a, b, r0 + threadIdx.x), threadIdx.x, mm, ll);
-  __syncthreads();
 }
 
 template <int RW>
@@ -623,6 +627,7 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
   wait_loads<0>();
   __syncthreads();
 
+  acc_settle();
   l = rows_sum<RW>(l);
   const int r_in_block = wv * RW + lane % RW;
   auto column = [&](int i, int j) {  // of a lane's values 4j..4j+3 of column tile i
@@ -644,7 +649,7 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
         for (int j = 0; j < RW * RW / 256; ++j) {
           v4f v;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = st.o[pass * kPer + i][4 * j + e];
+          for (int e = 0; e < 4; ++e) v[e] = acc_read(st.o[pass * kPer + i][4 * j + e]);
           *(lds_v4f_t)(uintptr_t)(mine + (lane % RW) * LD + column(i, j) * 4) = v;
         }
       }
@@ -665,7 +670,7 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
       for (int j = 0; j < RW * RW / 256; ++j) {
         v4f v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = st.o[i][4 * j + e];
+        for (int e = 0; e < 4; ++e) v[e] = acc_read(st.o[i][4 * j + e]);
         if (direct) {
           const uint2 w = {pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
           *(uint2*)(out + column(i, j)) = w;
@@ -840,7 +845,10 @@ __global__ __launch_bounds__(256) void mla_join_kernel(ListArgs a, ListArgs p) {
     a.d.lse[flat] = l > 0 ? (m + __builtin_amdgcn_logf(l)) * kLn2 : l == 0 ? kNegInf : l;
 }
 
-int rows_per_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+int rows_per_block(int64_t rows) {
+  if (const int forced = get_mla_rows_override()) return forced;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+}
 int unit_keys(int rb) { return rb <= 32 ? 4 * kTile : 2 * kTile; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

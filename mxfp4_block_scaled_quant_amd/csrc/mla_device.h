@@ -37,6 +37,7 @@ typedef __attribute__((address_space(3))) v8s* lds_v8s_t;
 typedef __attribute__((address_space(3))) v4f* lds_v4f_t;
 typedef __attribute__((address_space(3))) float* lds_f32_t;
 typedef __attribute__((address_space(3))) int* lds_i32_t;
+typedef __attribute__((address_space(3))) int64_t* lds_i64_t;
 
 // LDS by byte address (a kernel's only __shared__ array starts at 0).
 __device__ __forceinline__ v8bf lds_read16(uint32_t a) {
@@ -179,21 +180,31 @@ __device__ __forceinline__ bool softmax_step(float (&x)[NX], float c, float& m, 
   return grew;
 }
 
-// o *= alpha for accumulators that stay in accumulation registers: vector
-// instructions cannot take those, and written as plain C++ the compiler moves
-// every accumulator through vector registers on each tile, not only where
-// the maximum grew.  The leading wait covers matrix results still in flight
-// (the compiler does not count them for assembly statements).
+// Accumulators that stay in accumulation registers: vector instructions
+// cannot take those, and where plain C++ reads them the compiler moves all of
+// them through vector registers ahead of any branch, in the loop on every
+// tile.  So they are read and written one by one, by assembly statements,
+// behind a wait for matrix results still in flight (which the compiler does
+// not count for assembly statements).
+__device__ __forceinline__ void acc_settle() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
+}
+__device__ __forceinline__ float acc_read(float a) {
+  float v;
+  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
+  return v;
+}
+// o *= alpha
 template <typename V, int N>
 __device__ __forceinline__ void rescale(V (&o)[N], float alpha) {
-  asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
+  acc_settle();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
 #pragma unroll
     for (int j = 0; j < (int)(sizeof(V) / 4); ++j) {
-      float t = o[i][j], r;
-      asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(t) : "a"(t));
-      t *= alpha;
+      const float t = acc_read(o[i][j]) * alpha;
+      float r;
       asm volatile("v_accvgpr_write_b32 %0, %1" : "=a"(r) : "v"(t));
       o[i][j] = r;
     }

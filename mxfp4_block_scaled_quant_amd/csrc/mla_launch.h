@@ -67,6 +67,7 @@ struct DecodePlan {
   int grid, pgrid;
   size_t part, pml, ppart, ppml, ipart, ipml, floats;
 };
+int get_mla_rows_override();  // 0: none (set by the test hook)
 DecodePlan decode_plan(int64_t B, int64_t S, int64_t H, int64_t max_tokens, int64_t prefix_len, int cus);
 hipError_t launch_mla_decode(const DecodeArgs& p, const DecodePlan& plan, hipStream_t stream);
 
