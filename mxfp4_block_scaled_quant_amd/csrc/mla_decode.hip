@@ -95,10 +95,30 @@ __device__ __forceinline__ int scan256(int v, int& total) {
   return before + x - v;
 }
 
-// The sequence that holds unit w * total / grid of the list, the units
-// before that sequence, and this workgroup's share [lo, hi).
+// Workgroups go to the 8 XCDs in turn, each with an L2 of its own: an XCD
+// takes consecutive shares of `n`, so that the row blocks of a sequence,
+// which read the same rows, meet in one L2.
+__device__ __forceinline__ int xcd_order(int w, int n) {
+  const int x = w & 7;
+  return x * (n >> 3) + min(x, n & 7) + (w >> 3);
+}
+
+// One sequence whose row blocks are no more than the workgroups: its keys are
+// cut into the same `chunks` pieces of `size` units for every row block, piece
+// by piece (all row blocks of a piece run side by side).
+struct Single {
+  int chunks, size;
+};
+__device__ __forceinline__ bool is_single(const ListArgs& a) { return a.B == 1 && a.nt <= a.grid; }
+__device__ __forceinline__ Single single_split(const ListArgs& a, int units) {
+  const int size = (units + a.grid / a.nt - 1) / (a.grid / a.nt);
+  return {size ? (units + size - 1) / size : 0, size};
+}
+
+// This workgroup's share w of the list, units [lo, hi), the sequence that
+// holds unit lo, and the units before that sequence.
 template <int UNIT>
-__device__ __forceinline__ void find_share(const ListArgs& a, int w, int& b, int& base, int& lo, int& hi) {
+__device__ __forceinline__ void find_share(const ListArgs& a, int& w, int& b, int& base, int& lo, int& hi) {
   const int chunk = (a.B + 255) / 256, b0 = threadIdx.x * chunk, b1 = min(a.B, b0 + chunk);
   int sum = 0;
   for (int i = b0; i < b1; ++i) sum += a.nt * units_of<UNIT>(list_len(a, i));
@@ -107,6 +127,7 @@ __device__ __forceinline__ void find_share(const ListArgs& a, int w, int& b, int
   const int grid = min(a.grid, total);  // workgroups with work: each has at least one unit
   lo = hi = 0;
   if (w < grid) {
+    w = xcd_order(w, grid);
     lo = (int)((int64_t)w * total / grid);
     hi = (int)((int64_t)(w + 1) * total / grid);
   }
@@ -691,26 +712,42 @@ __device__ constexpr int unit_tiles() { return RB <= 32 ? 4 : 2; }
 template <int RB>
 __device__ __forceinline__ void attend_list(const ListArgs& a) {
   constexpr int kUnitTiles = unit_tiles<RB>(), kUnit = kUnitTiles * kTile;
-  const int w = blockIdx.x;
-  int b, base, lo, hi;
-  find_share<kUnit>(a, w, b, base, lo, hi);
+  int w = blockIdx.x, b = 0, base = 0, lo, hi;
+  const bool single = is_single(a);
+  if (!single) find_share<kUnit>(a, w, b, base, lo, hi);
+  else lo = 0, hi = 1;
   for (int cur = lo; cur < hi;) {
     const int n = __builtin_amdgcn_readfirstlane(list_len(a, b));
     const int units = units_of<kUnit>(n);
-    if (cur - base >= units * a.nt) {  // past this sequence (or it is empty)
-      base += units * a.nt;
-      ++b;
-      continue;
+    int rt, u0, u1;
+    Dest to;
+    if (single) {
+      const Single cut = single_split(a, units);
+      if (w >= cut.chunks * a.nt) break;
+      w = xcd_order(w, cut.chunks * a.nt);
+      const int k = w / a.nt;
+      rt = w - k * a.nt;
+      u0 = k * cut.size;
+      u1 = min(units, u0 + cut.size);
+      to = {cut.chunks == 1, w};
+      cur = hi;
+    } else {
+      if (cur - base >= units * a.nt) {  // past this sequence (or it is empty)
+        base += units * a.nt;
+        ++b;
+        continue;
+      }
+      rt = (cur - base) / units;
+      u0 = (cur - base) - rt * units;
+      u1 = min(units, u0 + hi - cur);
+      to = {u0 == 0 && u1 == units, 2 * w + (u0 == 0)};
+      cur += u1 - u0;
     }
-    const int rt = (cur - base) / units, u0 = (cur - base) - rt * units;
-    const int u1 = min(units, u0 + hi - cur);
-    const Dest to = {u0 == 0 && u1 == units, 2 * w + (u0 == 0)};
     const int tiles = (int)(((uint32_t)n + kTile - 1) / kTile);
     if constexpr (RB <= 32)
       attend_split<RB>(a, b, n, rt, u0 * kUnitTiles, min(tiles, u1 * kUnitTiles), to);
     else
       attend_shared<RB / 4>(a, b, n, rt, u0 * kUnitTiles, min(tiles, u1 * kUnitTiles), to);
-    cur += u1 - u0;
   }
 }
 
@@ -728,12 +765,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 
 // The workgroups that hold pieces of query row r of sequence b in a list:
 // count 0 if the sequence is empty, 1 if one workgroup held the whole item.
+// Part i lies in slot first + i * step - (i > 0) * skip.
 struct Parts {
-  int first, count;
+  int count, first, step, skip;
 };
 template <int RB>
 __device__ __forceinline__ Parts find_parts(const ListArgs& a, int b, int r) {
   constexpr int kUnit = unit_tiles<RB>() * kTile;
+  if (is_single(a)) return {single_split(a, units_of<kUnit>(list_len(a, 0))).chunks, r / RB, a.nt, 0};
   int before = 0, total = 0;  // units of the sequences before b, and of all (each wave by itself)
   for (int i = threadIdx.x & 63; i < a.B; i += 64) {
     const int u = a.nt * units_of<kUnit>(list_len(a, i));
@@ -746,12 +785,13 @@ __device__ __forceinline__ Parts find_parts(const ListArgs& a, int b, int r) {
     total += __shfl_xor(total, d);
   }
   const int units = units_of<kUnit>(list_len(a, b));
-  if (units == 0) return {0, 0};
+  if (units == 0) return {0, 0, 0, 0};
   const int u0 = before + r / RB * units;
   const int grid = min(a.grid, total);
   const int w0 = (int)((((int64_t)u0 + 1) * grid - 1) / total);
   const int w1 = (int)((((int64_t)u0 + units) * grid - 1) / total);
-  return {w0, w1 - w0 + 1};
+  // the first workgroup's second slot (the item begins there), then the others' first
+  return {w1 - w0 + 1, 2 * w0 + 1, 2, 1};
 }
 
 // One workgroup of four waves per query row joins its parts.  Wave w takes
@@ -769,7 +809,7 @@ __global__ __launch_bounds__(256) void mla_join_kernel(ListArgs a, ListArgs p) {
   const int64_t flat = flat_row(a.d, id);
   const Parts own = find_parts<RB>(a, b, r);
   if (!PRB && own.count == 1) return;
-  Parts pre = {0, 0};
+  Parts pre = {0, 0, 0, 0};
   if constexpr (PRB != 0) pre = find_parts<PRB>(p, 0, (int)flat);
   // Part i's row: (list, slot row); whole items lie by query row.
   auto part_at = [&](int i, const float*& po, const float*& pm) {
@@ -778,9 +818,8 @@ __global__ __launch_bounds__(256) void mla_join_kernel(ListArgs a, ListArgs p) {
     const Parts& q = in_prefix ? pre : own;
     i -= in_prefix ? 0 : pre.count;
     const bool whole = q.count == 1;
-    const int64_t k = whole ? flat
-                      : in_prefix ? (int64_t)(2 * (q.first + i) + (i == 0)) * PRB + (int)(flat % (PRB ? PRB : 1))
-                                  : (int64_t)(2 * (q.first + i) + (i == 0)) * RB + r % RB;
+    const int64_t slot = q.first + (int64_t)i * q.step - (i > 0 ? q.skip : 0);
+    const int64_t k = whole ? flat : in_prefix ? slot * PRB + (int)(flat % (PRB ? PRB : 1)) : slot * RB + r % RB;
     po = (whole ? g.ipart : g.part) + k * kLatent;
     pm = (whole ? g.ipml : g.pml) + 2 * k;
   };
