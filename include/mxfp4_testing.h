@@ -36,7 +36,7 @@ int mxfp4_testing_set_gemm_path(int path);
 /*
  * Forces the query rows per workgroup of mla_decode (and of both lists of
  * mla_decode_shared_prefix) on this thread: 16 or 32 (the waves share a
- * sequence's keys between them), 64 or 128 (the waves share the query rows);
+ * sequence's keys between them) or 128 (the waves share the query rows);
  * 0 = choose by the rows and keys (the default).  Workspace sizes follow.
  * Returns MXFP4_OK, or MXFP4_ERR_ARG for other values.
  */

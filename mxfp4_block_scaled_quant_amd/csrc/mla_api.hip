@@ -279,7 +279,7 @@ int mla_prefill(const void* q, int64_t q_token, int64_t q_head, const void* k_no
 
 // Test hook (include/mxfp4_testing.h): force the decode form on this thread.
 int mla_testing_set_rows(int rows) {
-  if (rows != 0 && rows != 16 && rows != 32 && rows != 64 && rows != 128) return MXFP4_ERR_ARG;
+  if (rows != 0 && rows != 16 && rows != 32 && rows != 128) return MXFP4_ERR_ARG;
   t_rows = rows;
   return MXFP4_OK;
 }

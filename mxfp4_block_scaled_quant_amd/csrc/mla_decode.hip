@@ -115,22 +115,43 @@ __device__ __forceinline__ Single single_split(const ListArgs& a, int units) {
   return {size ? (units + size - 1) / size : 0, size};
 }
 
-// This workgroup's share w of the list, units [lo, hi), the sequence that
-// holds unit lo, and the units before that sequence.
-template <int UNIT>
-__device__ __forceinline__ void find_share(const ListArgs& a, int& w, int& b, int& base, int& lo, int& hi) {
-  const int chunk = (a.B + 255) / 256, b0 = threadIdx.x * chunk, b1 = min(a.B, b0 + chunk);
-  int sum = 0;
-  for (int i = b0; i < b1; ++i) sum += a.nt * units_of<UNIT>(list_len(a, i));
-  int total;
-  int at = scan256(sum, total);
-  const int grid = min(a.grid, total);  // workgroups with work: each has at least one unit
+// Share w of `total` units over at most `most` workgroups, each with at least
+// one unit: [lo, hi), empty for workgroups without.
+__device__ __forceinline__ void share_of(int& w, int total, int most, int& lo, int& hi) {
+  const int grid = min(most, total);
   lo = hi = 0;
   if (w < grid) {
     w = xcd_order(w, grid);
     lo = (int)((int64_t)w * total / grid);
     hi = (int)((int64_t)(w + 1) * total / grid);
   }
+}
+
+// This workgroup's share w of the list, units [lo, hi), the sequence that
+// holds unit lo, and the units before that sequence.
+template <int UNIT>
+__device__ __forceinline__ void find_share(const ListArgs& a, int& w, int& b, int& base, int& lo, int& hi) {
+  if (a.B <= 64) {  // each wave by itself, one sequence a lane
+    const int lane = threadIdx.x & 63;
+    const int u = lane < a.B ? a.nt * units_of<UNIT>(list_len(a, lane)) : 0;
+    int upto = u;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int y = __shfl_up(upto, d);
+      if (lane >= d) upto += y;
+    }
+    share_of(w, __builtin_amdgcn_readlane(upto, 63), a.grid, lo, hi);
+    const uint64_t holds = __builtin_amdgcn_ballot_w64(upto - u <= lo && lo < upto);
+    b = holds ? __builtin_ctzll(holds) : 0;
+    base = __builtin_amdgcn_readlane(upto - u, b);
+    return;
+  }
+  const int chunk = (a.B + 255) / 256, b0 = threadIdx.x * chunk, b1 = min(a.B, b0 + chunk);
+  int sum = 0;
+  for (int i = b0; i < b1; ++i) sum += a.nt * units_of<UNIT>(list_len(a, i));
+  int total;
+  int at = scan256(sum, total);
+  share_of(w, total, a.grid, lo, hi);
   lds_i32_t s = (lds_i32_t)(uintptr_t)kMiscLds;
   if (at <= lo && lo < at + sum) {
     int i = b0;
@@ -536,114 +557,97 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
     bad[i] = locate(t0 + i, mine, all);
     load(stage_of(t0 + i));
   }
-  if constexpr (RW == 16) {
-    for (int t = t0; t < t1; ++t) {
-      wait_loads<18>();  // two later tiles stay in flight
-      wait_lds();
-      wave_barrier();    // tile t is whole, and tile t - 1 no longer read
-      refill(t + 3);
-      int mine, all;
-      lookup(t + 3, mine, all);
-      bad[3] = locate(t + 3, mine, all);
-      load(stage_of(t + 3));
-      attend_tile<RW>(stage_of(t), la, st, m, l, a.d.c, lane, bad[0] == 0 && (t + 1) * kTile <= seen_all,
-                      seen - t * kTile, bad[0]);
+  // One wave a SIMD: nothing else fills the matrix unit while this wave
+  // does anything but issue products.  So tile t's softmax runs between the
+  // value products of tile t - 1, and the loads of tile t + 2 and the
+  // addresses of tile t + 3 between the score products of tile t.
+  auto full = [&](int t) { return bad[0] == 0 && (t + 1) * kTile <= seen_all; };
+  v8bf p[2];            // the probabilities of the tile before,
+  bool grew = false;    // whether its maxima rose, and by what the
+  float alpha = 1;      // accumulators are to be scaled then
+  wait_loads<18>();
+  wave_barrier();
+  {
+    const TileAddr<RW> at(la, stage_of(t0));
+    auto key = [&](int i) { return at.key(i); };
+    v8bf first[4];
+    read_group(first, key);
+    v16f s;
+    pipeline<36, 4>(first, key, [&](int i, v8bf f) { score_product(s, i, f, st.q[i]); });
+    float x[16];
 #pragma unroll
-      for (int i = 0; i < 3; ++i) bad[i] = bad[i + 1];
-    }
-  } else {
-    // One wave a SIMD: nothing else fills the matrix unit while this wave
-    // does anything but issue products.  So tile t's softmax runs between the
-    // value products of tile t - 1, and the loads of tile t + 2 and the
-    // addresses of tile t + 3 between the score products of tile t.
-    auto full = [&](int t) { return bad[0] == 0 && (t + 1) * kTile <= seen_all; };
-    v8bf p[2];            // the probabilities of the tile before,
-    bool grew = false;    // whether its maxima rose, and by what the
-    float alpha = 1;      // accumulators are to be scaled then
-    wait_loads<18>();
-    wave_barrier();
+    for (int i = 0; i < 16; ++i) x[i] = s[i];
+    if (!full(t0)) mask_scores<RW, 16>(x, lane, seen - t0 * kTile, bad[0]);
+    softmax_step<RW, 16>(x, a.d.c, m, l, alpha, p);  // (nothing to rescale yet)
+  }
+  refill(t0 + 3);
+  int mine, all;
+  lookup(t0 + 3, mine, all);
+  bad[3] = locate(t0 + 3, mine, all);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bad[i] = bad[i + 1];
+  for (int t = t0 + 1; t < t1; ++t) {
+    wait_loads<9>();  // tile t is there, t + 1 may be in flight
+    wait_lds();
+    wave_barrier();   // tile t is whole, and tile t - 2 no longer read
+    refill(t + 3);
+    const uint32_t fill = stage_of(t + 2);
+    v16f s;
     {
-      const TileAddr<RW> at(la, stage_of(t0));
+      const TileAddr<RW> at(la, stage_of(t));
       auto key = [&](int i) { return at.key(i); };
       v8bf first[4];
       read_group(first, key);
-      v16f s;
-      pipeline<36, 4>(first, key, [&](int i, v8bf f) { score_product(s, i, f, st.q[i]); });
-      float x[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = s[i];
-      if (!full(t0)) mask_scores<RW, 16>(x, lane, seen - t0 * kTile, bad[0]);
-      softmax_step<RW, 16>(x, a.d.c, m, l, alpha, p);  // (nothing to rescale yet)
-    }
-    refill(t0 + 3);
-    int mine, all;
-    lookup(t0 + 3, mine, all);
-    bad[3] = locate(t0 + 3, mine, all);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bad[i] = bad[i + 1];
-    for (int t = t0 + 1; t < t1; ++t) {
-      wait_loads<9>();  // tile t is there, t + 1 may be in flight
-      wait_lds();
-      wave_barrier();   // tile t is whole, and tile t - 2 no longer read
-      refill(t + 3);
-      const uint32_t fill = stage_of(t + 2);
-      v16f s;
-      {
-        const TileAddr<RW> at(la, stage_of(t));
-        auto key = [&](int i) { return at.key(i); };
-        v8bf first[4];
-        read_group(first, key);
-        pipeline<36, 4>(first, key, [&](auto ic, v8bf f) {
-          constexpr int i = ic;
-          score_product(s, i, f, st.q[i]);
-          if constexpr (i < 9) dma16_at<i * 128>(fill + wv * 1024 + i * kBlock, ptr);
-          else if constexpr (i == 15) lookup(t + 3, mine, all);
-          else if constexpr (i == 27) bad[3] = locate(t + 3, mine, all);
-        });
-      }
-      float x[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = s[i];
-      if (!full(t)) mask_scores<RW, 16>(x, lane, seen - t * kTile, bad[0]);
-      float mx = x[0], mu = 0;
-      if (grew) rescale(st.o, alpha);
-      const TileAddr<RW> at(la, stage_of(t - 1));
-      auto value = [&](int i) { return at.value(i); };
-      v8bf first[4];
-      read_group(first, value);
-      pipeline<32, 4>(first, value, [&](int i, v8bf f) {
-        st.o[i >> 1] = mfma_rows(f, p[i & 1], st.o[i >> 1]);
-        if (i == 0) {
-#pragma unroll
-          for (int j = 1; j < 16; ++j) mx = fmaxf(mx, x[j]);
-        } else if (i == 1) {
-          mx = rows_max<RW>(mx) * a.d.c;
-          const float mn = mx > m + kLag ? mx : m;
-          grew = __builtin_amdgcn_ballot_w64(mn != m) != 0;
-          alpha = mn == m ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
-          m = mn;
-          mu = m == kNegInf ? 0.0f : m;
-          l *= alpha;
-        } else if (i >= 4 && i < 20) {
-          const int e = i - 4;
-          x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], a.d.c, -mu));
-          l += x[e];
-          asm volatile("" : "+v"(x[e]));  // here, not where the values are used
-        }
+      pipeline<36, 4>(first, key, [&](auto ic, v8bf f) {
+        constexpr int i = ic;
+        score_product(s, i, f, st.q[i]);
+        if constexpr (i < 9) dma16_at<i * 128>(fill + wv * 1024 + i * kBlock, ptr);
+        else if constexpr (i == 15) lookup(t + 3, mine, all);
+        else if constexpr (i == 27) bad[3] = locate(t + 3, mine, all);
       });
-#pragma unroll
-      for (int i = 0; i < 16; ++i) p[i >> 3][i & 7] = (__bf16)x[i];
-#pragma unroll
-      for (int i = 0; i < 3; ++i) bad[i] = bad[i + 1];
     }
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = s[i];
+    if (!full(t)) mask_scores<RW, 16>(x, lane, seen - t * kTile, bad[0]);
+    float mx = x[0], mu = 0;
     if (grew) rescale(st.o, alpha);
-    {
-      const TileAddr<RW> at(la, stage_of(t1 - 1));
-      auto value = [&](int i) { return at.value(i); };
-      v8bf first[4];
-      read_group(first, value);
-      tile_values<RW>(at, first, st, p);
-    }
+    const TileAddr<RW> at(la, stage_of(t - 1));
+    auto value = [&](int i) { return at.value(i); };
+    v8bf first[4];
+    read_group(first, value);
+    pipeline<32, 4>(first, value, [&](int i, v8bf f) {
+      st.o[i >> 1] = mfma_rows(f, p[i & 1], st.o[i >> 1]);
+      if (i == 0) {
+#pragma unroll
+        for (int j = 1; j < 16; ++j) mx = fmaxf(mx, x[j]);
+      } else if (i == 1) {
+        mx = rows_max<RW>(mx) * a.d.c;
+        const float mn = mx > m + kLag ? mx : m;
+        grew = __builtin_amdgcn_ballot_w64(mn != m) != 0;
+        alpha = mn == m ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        mu = m == kNegInf ? 0.0f : m;
+        l *= alpha;
+      } else if (i >= 4 && i < 20) {
+        const int e = i - 4;
+        x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], a.d.c, -mu));
+        l += x[e];
+        asm volatile("" : "+v"(x[e]));  // here, not where the values are used
+      }
+    });
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[i >> 3][i & 7] = (__bf16)x[i];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) bad[i] = bad[i + 1];
+  }
+  if (grew) rescale(st.o, alpha);
+  {
+    const TileAddr<RW> at(la, stage_of(t1 - 1));
+    auto value = [&](int i) { return at.value(i); };
+    v8bf first[4];
+    read_group(first, value);
+    tile_values<RW>(at, first, st, p);
   }
   wait_loads<0>();
   __syncthreads();
@@ -708,11 +712,11 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
 template <int RB>
 __device__ constexpr int unit_tiles() { return RB <= 32 ? 4 : 2; }
 
-// This workgroup's share of one list.
+// Workgroup w's share of one list.
 template <int RB>
-__device__ __forceinline__ void attend_list(const ListArgs& a) {
+__device__ __forceinline__ void attend_list(const ListArgs& a, int w) {
   constexpr int kUnitTiles = unit_tiles<RB>(), kUnit = kUnitTiles * kTile;
-  int w = blockIdx.x, b = 0, base = 0, lo, hi;
+  int b = 0, base = 0, lo, hi;
   const bool single = is_single(a);
   if (!single) find_share<kUnit>(a, w, b, base, lo, hi);
   else lo = 0, hi = 1;
@@ -752,15 +756,21 @@ __device__ __forceinline__ void attend_list(const ListArgs& a) {
 }
 
 // One list (PRB = 0), or a prefix's list and then the requests' own: a
-// workgroup that has stored its prefix part starts on its requests at once.
+// workgroup that has stored its prefix part starts on its requests at once,
+// and where there is little work, the requests start from the other end and
+// meet workgroups that have no prefix part.
 template <int RB, int PRB>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void mla_attend_kernel(ListArgs a,
                                                                                                    ListArgs p) {
   __shared__ int4 lds_raw[kLdsBytes / 16];
   uint32_t anchor = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int4*)lds_raw;
   asm volatile("" : "+s"(anchor)::"memory");  // LDS is addressed by number: its array starts at 0
-  if constexpr (PRB != 0) attend_list<PRB>(p);
-  attend_list<RB>(a);
+  if constexpr (PRB != 0) {
+    attend_list<PRB>(p, blockIdx.x);
+    attend_list<RB>(a, gridDim.x - 1 - blockIdx.x);
+  } else {
+    attend_list<RB>(a, blockIdx.x);
+  }
 }
 
 // The workgroups that hold pieces of query row r of sequence b in a list:
@@ -794,17 +804,22 @@ __device__ __forceinline__ Parts find_parts(const ListArgs& a, int b, int r) {
   return {w1 - w0 + 1, 2 * w0 + 1, 2, 1};
 }
 
-// One workgroup of four waves per query row joins its parts.  Wave w takes
-// parts w, w + 4, ..: its lanes fetch 64 parts' maxima and sums at once, then
-// the wave runs over the parts' 512 values, 8 a lane; the four waves' sums
-// meet in LDS in wave order.  Rows that one workgroup of a call without a
-// prefix wrote itself are left alone; rows without any key become 0 and -inf.
-template <int RB, int PRB>
+// One workgroup of four waves per query row, or CS workgroups per row with
+// 512 / CS columns each, joins its parts.  Wave w takes parts w, w + 4, ..:
+// its lanes fetch 64 parts' maxima and sums at once, then the wave runs over
+// the parts' values, 8 / CS a lane; the four waves' sums meet in LDS in wave
+// order.  Rows that one workgroup of a call without a prefix wrote itself are
+// left alone; rows without any key become 0 and -inf.
+template <int RB, int PRB, int CS>
 __global__ __launch_bounds__(256) void mla_join_kernel(ListArgs a, ListArgs p) {
-  __shared__ v4f so[4][kLatent / 4];
+  constexpr int W = 8 / CS;                      // columns per lane
+  typedef float vec __attribute__((ext_vector_type(CS == 1 ? 4 : W)));
+  constexpr int V = CS == 1 ? 4 : W, NV = W / V;  // read as NV vectors, 64 lanes apart
+  __shared__ float so[4][512 / CS];
   __shared__ float sml[4][2];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int b = blockIdx.x / a.rows, r = blockIdx.x - b * a.rows;
+  const int c0 = blockIdx.y * (512 / CS);
   const RowId id = row_id(a, b, r);
   const int64_t flat = flat_row(a.d, id);
   const Parts own = find_parts<RB>(a, b, r);
@@ -820,12 +835,12 @@ __global__ __launch_bounds__(256) void mla_join_kernel(ListArgs a, ListArgs p) {
     const bool whole = q.count == 1;
     const int64_t slot = q.first + (int64_t)i * q.step - (i > 0 ? q.skip : 0);
     const int64_t k = whole ? flat : in_prefix ? slot * PRB + (int)(flat % (PRB ? PRB : 1)) : slot * RB + r % RB;
-    po = (whole ? g.ipart : g.part) + k * kLatent;
+    po = (whole ? g.ipart : g.part) + k * kLatent + c0;
     pm = (whole ? g.ipml : g.pml) + 2 * k;
   };
   const int count = pre.count + own.count;
   float m = kNegInf, l = 0;
-  v4f o[2] = {};
+  vec o[NV] = {};
   for (int i0 = wv; i0 < count; i0 += 256) {  // 64 parts of this wave
     const int mine = i0 + 4 * lane, n = min(64, (count - i0 + 3) / 4);
     const float *po, *pm;
@@ -847,27 +862,27 @@ __global__ __launch_bounds__(256) void mla_join_kernel(ListArgs a, ListArgs p) {
     l = l * keep + ls;
     m = mn;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e >> 2][e & 3] *= keep;
+    for (int v = 0; v < NV; ++v) o[v] *= keep;
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
       const float fi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
       part_at(i0 + 4 * i, po, pm);
-      const v4f v0 = *(const v4f*)(po + 4 * lane), v1 = *(const v4f*)(po + 256 + 4 * lane);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        o[0][e] += fi == 0 ? 0.0f : v0[e] * fi;
-        o[1][e] += fi == 0 ? 0.0f : v1[e] * fi;
+      for (int v = 0; v < NV; ++v) {
+        const vec x = *(const vec*)(po + v * 64 * V + V * lane);
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[v][e] += fi == 0 ? 0.0f : x[e] * fi;
       }
     }
   }
-  so[wv][lane] = o[0];
-  so[wv][64 + lane] = o[1];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) *(vec*)&so[wv][v * 64 * V + V * lane] = o[v];
   if (lane == 0) {
     sml[wv][0] = m;
     sml[wv][1] = l;
   }
   __syncthreads();
-  if (threadIdx.x >= 128) return;
+  if (threadIdx.x >= 128 / CS) return;
   m = fmaxf(fmaxf(sml[0][0], sml[1][0]), fmaxf(sml[2][0], sml[3][0]));
   l = 0;
   v4f t = {0, 0, 0, 0};
@@ -875,41 +890,66 @@ __global__ __launch_bounds__(256) void mla_join_kernel(ListArgs a, ListArgs p) {
   for (int w = 0; w < 4; ++w) {
     const float lw = sml[w][1], f = lw == 0 ? 0.0f : __builtin_amdgcn_exp2f(sml[w][0] - m);
     l += lw * f;
-    t += so[w][threadIdx.x] * f;
+    t += *(const v4f*)&so[w][4 * threadIdx.x] * f;
   }
   const float inv = l == 0 ? 0.0f : 1.0f / l;
   const uint2 w = {pack_bf16x2(t[0] * inv, t[1] * inv), pack_bf16x2(t[2] * inv, t[3] * inv)};
-  *(uint2*)(a.d.out + id.b * a.d.sob + id.s * a.d.sos + id.h * a.d.soh + 4 * threadIdx.x) = w;
-  if (a.d.lse && threadIdx.x == 0)
+  *(uint2*)(a.d.out + id.b * a.d.sob + id.s * a.d.sos + id.h * a.d.soh + c0 + 4 * threadIdx.x) = w;
+  if (a.d.lse && threadIdx.x == 0 && blockIdx.y == 0)
     a.d.lse[flat] = l > 0 ? (m + __builtin_amdgcn_logf(l)) * kLn2 : l == 0 ? kNegInf : l;
 }
 
-int rows_per_block(int64_t rows) {
-  if (const int forced = get_mla_rows_override()) return forced;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-}
-int unit_keys(int rb) { return rb <= 32 ? 4 * kTile : 2 * kTile; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int unit_keys(int rb) { return rb <= 32 ? 4 * kTile : 2 * kTile; }
+
+// Query rows per workgroup for B sequences of `rows` query rows and up to n
+// keys.  Blocks of 16 read a sequence's rows once per 16 query rows, but from
+// L2, with little to set up and small parts, so they win until the matrix
+// units' work counts: up to ten units of 128 keys a compute unit.  Past that,
+// 32 rows where there are no more, else 128 (the waves share the loads).
+// Measured on MI355X (us, blocks of 16 / 32 / 128): 8 sequences of 64 rows
+// and 8000 keys (7.9 units a compute unit) 41.4 / 42.3 / 44.7, one of 128
+// rows and 32000 (7.8) 42.7 / 42.8 / 55.2; 8 of 128 and 8000 (15.8) 63.6 /
+// 51.2 / 51.0, 32 of 32 and 8000 (15.8) 88.5 / 76.9 / 91.9, 8 of 64 and
+// 32000 (31) 144 / 99 / 94, 4 of 512 and 32000 (125) 370 / 214 / 156.
+int rows_per_block(int64_t B, int64_t rows, int64_t n) {
+  if (const int forced = get_mla_rows_override()) return forced;
+  if (rows <= 16 || B * cdiv(rows, 16) * cdiv(n, 128) <= 10ll * kMlaMaxCus) return 16;
+  return rows <= 32 ? 32 : 128;
+}
 
 template <int PRB>
-void launch_attend(int rb, const ListArgs& a, const ListArgs& p, hipStream_t s) {
-  const int grid = PRB && p.grid > a.grid ? p.grid : a.grid;
-  switch (rb) {
-    case 16: mla_attend_kernel<16, PRB><<<grid, 256, 0, s>>>(a, p); break;
-    case 32: mla_attend_kernel<32, PRB><<<grid, 256, 0, s>>>(a, p); break;
-    case 64: mla_attend_kernel<64, PRB><<<grid, 256, 0, s>>>(a, p); break;
-    default: mla_attend_kernel<128, PRB><<<grid, 256, 0, s>>>(a, p); break;
+void launch_attend(int rb, const ListArgs& a, const ListArgs& p, int cus, hipStream_t s) {
+  if constexpr (PRB == 0) {
+    switch (rb) {
+      case 16: mla_attend_kernel<16, 0><<<a.grid, 256, 0, s>>>(a, p); break;
+      case 32: mla_attend_kernel<32, 0><<<a.grid, 256, 0, s>>>(a, p); break;
+      default: mla_attend_kernel<128, 0><<<a.grid, 256, 0, s>>>(a, p); break;
+    }
+  } else {
+    const int grid = a.grid + p.grid < cus ? a.grid + p.grid : cus;
+    switch (rb) {
+      case 16: mla_attend_kernel<16, PRB><<<grid, 256, 0, s>>>(a, p); break;
+      case 32: mla_attend_kernel<32, PRB><<<grid, 256, 0, s>>>(a, p); break;
+      default: mla_attend_kernel<128, PRB><<<grid, 256, 0, s>>>(a, p); break;
+    }
   }
 }
-template <int PRB>
-void launch_join(int rb, const ListArgs& a, const ListArgs& p, hipStream_t s) {
-  const int grid = a.B * a.rows;
+template <int PRB, int CS>
+void launch_join_columns(int rb, const ListArgs& a, const ListArgs& p, hipStream_t s) {
+  const dim3 grid(a.B * a.rows, CS);
   switch (rb) {
-    case 16: mla_join_kernel<16, PRB><<<grid, 256, 0, s>>>(a, p); break;
-    case 32: mla_join_kernel<32, PRB><<<grid, 256, 0, s>>>(a, p); break;
-    case 64: mla_join_kernel<64, PRB><<<grid, 256, 0, s>>>(a, p); break;
-    default: mla_join_kernel<128, PRB><<<grid, 256, 0, s>>>(a, p); break;
+    case 16: mla_join_kernel<16, PRB, CS><<<grid, 256, 0, s>>>(a, p); break;
+    case 32: mla_join_kernel<32, PRB, CS><<<grid, 256, 0, s>>>(a, p); break;
+    default: mla_join_kernel<128, PRB, CS><<<grid, 256, 0, s>>>(a, p); break;
   }
+}
+// A row's parts by one workgroup, or by four where the rows are too few to
+// keep the compute units' loads in flight (16 rows of 250 parts: 17.3 -> 9.7 us).
+template <int PRB>
+void launch_join(int rb, const ListArgs& a, const ListArgs& p, int cus, hipStream_t s) {
+  if (a.B * a.rows < 2 * cus) launch_join_columns<PRB, 4>(rb, a, p, s);
+  else launch_join_columns<PRB, 1>(rb, a, p, s);
 }
 
 }  // namespace
@@ -917,8 +957,9 @@ void launch_join(int rb, const ListArgs& a, const ListArgs& p, hipStream_t s) {
 DecodePlan decode_plan(int64_t B, int64_t S, int64_t H, int64_t max_tokens, int64_t prefix_len, int cus) {
   DecodePlan d{};
   if (cus > kMlaMaxCus) cus = kMlaMaxCus;
+  d.cus = cus;
   const int64_t rows = S * H;
-  d.rows = rows_per_block(rows);
+  d.rows = rows_per_block(B, rows, max_tokens);
   int64_t units = B * cdiv(rows, d.rows) * cdiv(max_tokens, unit_keys(d.rows));
   d.grid = (int)(units < cus ? (units < 1 ? 1 : units) : cus);
   size_t at = 0;
@@ -930,7 +971,7 @@ DecodePlan decode_plan(int64_t B, int64_t S, int64_t H, int64_t max_tokens, int6
   d.part = take(2ll * d.grid * d.rows * kLatent);
   d.pml = take(2ll * d.grid * d.rows * 2);
   if (prefix_len > 0) {
-    d.prows = rows_per_block(B * rows);
+    d.prows = rows_per_block(1, B * rows, prefix_len);
     units = cdiv(B * rows, d.prows) * cdiv(prefix_len, unit_keys(d.prows));
     d.pgrid = (int)(units < cus ? units : cus);
     d.ppart = take(2ll * d.pgrid * d.prows * kLatent);
@@ -973,29 +1014,29 @@ hipError_t launch_mla_decode(const DecodeArgs& d, const DecodePlan& plan, hipStr
     p.pml = d.work + plan.ppml;
     p.ipart = a.ipart + all * kLatent;
     p.ipml = a.ipml + 2 * all;
-    // (Fewer rows than a block of 128 in the whole batch: two launches, and
-    // no code of their own for every pair of forms.)
+    // (Prefix blocks of 32 rows, a batch of 17 to 32 rows over a long prefix,
+    // take two launches: no code of their own for every pair of forms.)
     hipError_t e;
-    if (plan.prows == 128) {
-      launch_attend<128>(plan.rows, a, p, stream);
-    } else {
-      launch_attend<0>(plan.prows, p, p, stream);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-      launch_attend<0>(plan.rows, a, a, stream);
+    switch (plan.prows) {
+      case 16: launch_attend<16>(plan.rows, a, p, plan.cus, stream); break;
+      case 128: launch_attend<128>(plan.rows, a, p, plan.cus, stream); break;
+      default:
+        launch_attend<0>(plan.prows, p, p, plan.cus, stream);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        launch_attend<0>(plan.rows, a, a, plan.cus, stream);
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;
     switch (plan.prows) {
-      case 16: launch_join<16>(plan.rows, a, p, stream); break;
-      case 32: launch_join<32>(plan.rows, a, p, stream); break;
-      case 64: launch_join<64>(plan.rows, a, p, stream); break;
-      default: launch_join<128>(plan.rows, a, p, stream); break;
+      case 16: launch_join<16>(plan.rows, a, p, plan.cus, stream); break;
+      case 32: launch_join<32>(plan.rows, a, p, plan.cus, stream); break;
+      default: launch_join<128>(plan.rows, a, p, plan.cus, stream); break;
     }
     return hipGetLastError();
   }
-  launch_attend<0>(plan.rows, a, a, stream);
+  launch_attend<0>(plan.rows, a, a, plan.cus, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  launch_join<0>(plan.rows, a, a, stream);
+  launch_join<0>(plan.rows, a, a, plan.cus, stream);
   return hipGetLastError();
 }
 

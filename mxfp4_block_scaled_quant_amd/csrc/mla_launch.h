@@ -63,8 +63,8 @@ struct DecodeArgs {
 // unit of its requests and of its prefix, workgroups, and where the parts
 // lie in the workspace (float offsets).
 struct DecodePlan {
-  int rows, prows;                // 16, 32 (four waves share the keys), 64, 128 (four waves share the rows)
-  int grid, pgrid;
+  int rows, prows;                // 16, 32 (four waves share the keys), 128 (four waves share the rows)
+  int grid, pgrid, cus;
   size_t part, pml, ppart, ppml, ipart, ipml, floats;
 };
 int get_mla_rows_override();  // 0: none (set by the test hook)

@@ -63,7 +63,7 @@ def mla_decode_workspace_bytes(B: int, S: int, H: int, max_tokens: int, prefix_l
 
 def set_mla_rows(rows: int) -> None:
     """Test hook (include/mxfp4_testing.h), for the calling thread only: query
-    rows per workgroup of the decode kernels (16, 32, 64, 128; 0 = by size)."""
+    rows per workgroup of the decode kernels (16, 32, 128; 0 = by size)."""
     _check("mla_testing_set_rows", lib().mla_testing_set_rows(rows))
 
 
