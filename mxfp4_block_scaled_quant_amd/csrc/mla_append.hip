@@ -84,9 +84,7 @@ __global__ __launch_bounds__(64 * kWaves) void mla_append_kernel(AppendArgs p) {
     float ss = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) ss += __shfl_xor(ss, d);
-    const float r = rsqrtf(ss * (1.0f / kLatent) + p.eps);
+    const float r = rsqrtf(wave_sum(ss) * (1.0f / kLatent) + p.eps);
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
     *(int4*)(row + lane * 16) = pack8(x);

@@ -188,9 +188,13 @@ __device__ __forceinline__ uint32_t load_chunk(uint32_t lane) {
 __device__ __forceinline__ uint32_t load_chunk(uint32_t lane, uint32_t group) {
   return load_chunk(lane) ^ ((group & 1) << 4);
 }
-template <int... J>
-__device__ __forceinline__ void load_group(uint32_t at, const char* p, std::integer_sequence<int, J...>) {
-  (dma16_at<J * 128>(at + J * kBlock, p), ...);
+template <bool STREAM, int... J>
+__device__ __forceinline__ void load_blocks(uint32_t at, const char* p, std::integer_sequence<int, J...>) {
+  (dma16_at<J * 128, STREAM>(at + J * kBlock, p), ...);
+}
+template <bool STREAM>
+__device__ __forceinline__ void load_group(uint32_t at, const char* p) {
+  load_blocks<STREAM>(at, p, std::make_integer_sequence<int, kBlocks>{});
 }
 
 // Accumulators and query operands of RW query rows.
@@ -403,7 +407,11 @@ __device__ __forceinline__ void attend_split(const ListArgs& a, int b, int n, in
       bool ok;
       const char* ptr = row_at(a.d.cache, t * kTile + 8 * g + (lane >> 3), page[g], ok) + load_chunk(lane, g);
       hidden[g] = __builtin_amdgcn_ballot_w64(!ok);
-      load_group(tile + g * 1024, ptr, std::make_integer_sequence<int, kBlocks>{});
+      // One row block: nothing else reads these rows, and loads that leave
+      // no trace in the caches run faster (128 requests of up to 16000 rows:
+      // 218 -> 196 us, 5.4 TB/s).
+      if (a.nt == 1) load_group<true>(tile + g * 1024, ptr);
+      else load_group<false>(tile + g * 1024, ptr);
     }
     lookup(t + 4);
     uint32_t bad = 0;  // (seldom more than the keys past the end)
@@ -534,7 +542,7 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
     return (uint32_t)__builtin_amdgcn_ballot_w64((uint32_t)all >= (uint32_t)a.d.cache.pages);
   };
   auto load = [&](uint32_t stage) {
-    load_group(stage + wv * 1024, ptr, std::make_integer_sequence<int, kBlocks>{});
+    load_group<false>(stage + wv * 1024, ptr);
   };
   auto stage_of = [&](int t) { return ((t - t0) & 3) * kTileBytes; };
   auto refill = [&](int t) {  // a new window if tile t's pages lie past this one
@@ -601,7 +609,7 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
       pipeline<36, 4>(first, key, [&](auto ic, v8bf f) {
         constexpr int i = ic;
         score_product(s, i, f, st.q[i]);
-        if constexpr (i < 9) dma16_at<i * 128>(fill + wv * 1024 + i * kBlock, ptr);
+        if constexpr (i < 9) dma16_at<i * 128, false>(fill + wv * 1024 + i * kBlock, ptr);
         else if constexpr (i == 15) lookup(t + 3, mine, all);
         else if constexpr (i == 27) bad[3] = locate(t + 3, mine, all);
       });
@@ -789,11 +797,8 @@ __device__ __forceinline__ Parts find_parts(const ListArgs& a, int b, int r) {
     if (i < b) before += u;
     total += u;
   }
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    before += __shfl_xor(before, d);
-    total += __shfl_xor(total, d);
-  }
+  before = wave_sum(before);
+  total = wave_sum(total);
   const int units = units_of<kUnit>(list_len(a, b));
   if (units == 0) return {0, 0, 0, 0};
   const int u0 = before + r / RB * units;
@@ -850,16 +855,10 @@ __global__ __launch_bounds__(256) void mla_join_kernel(ListArgs a, ListArgs p) {
       pmx = pm[0];
       pl = pm[1];
     }
-    float mn = pmx;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) mn = fmaxf(mn, __shfl_xor(mn, d));
-    mn = fmaxf(mn, m);
+    const float mn = fmaxf(wave_max(pmx), m);
     const float keep = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
     const float f = pl == 0 ? 0.0f : __builtin_amdgcn_exp2f(pmx - mn);  // a part without keys counts nothing
-    float ls = pl * f;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) ls += __shfl_xor(ls, d);
-    l = l * keep + ls;
+    l = l * keep + wave_sum(pl * f);
     m = mn;
 #pragma unroll
     for (int v = 0; v < NV; ++v) o[v] *= keep;

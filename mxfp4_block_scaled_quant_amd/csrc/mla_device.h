@@ -74,11 +74,16 @@ __device__ __forceinline__ void dma16(uint32_t lds, const void* base, uint32_t v
                :: "s"(lds), "v"(voff), "s"(base) : "memory", "m0");
 }
 // (The instruction adds its immediate offset to the LDS address too.)
-template <int OFF>
+// STREAM: rows that nothing reads again are loaded past the caches.
+template <int OFF, bool STREAM>
 __device__ __forceinline__ void dma16_at(uint32_t lds, const void* p) {
   lds -= OFF;
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2"
-               :: "s"(lds), "v"(p), "i"(OFF) : "memory", "m0");
+  if constexpr (STREAM)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2 nt"
+                 :: "s"(lds), "v"(p), "i"(OFF) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2"
+                 :: "s"(lds), "v"(p), "i"(OFF) : "memory", "m0");
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -111,6 +116,31 @@ __device__ __forceinline__ float rows_sum(float x) {
   }
   const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// The larger / the sum of x over the 64 lanes, by lane permutations (no LDS):
+// the lane's pair, quad, half row and row of 16, then the two swaps.
+template <typename T, typename Op>
+__device__ __forceinline__ T wave_reduce(T x, Op op) {
+  static_assert(sizeof(T) == 4, "one register");
+  auto with = [&](int y) { x = op(x, __builtin_bit_cast(T, y)); };
+  with(__builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0xB1, 0xF, 0xF, true));   // lane ^ 1
+  with(__builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0x4E, 0xF, 0xF, true));   // lane ^ 2
+  with(__builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0x141, 0xF, 0xF, true));  // mirrored in 8
+  with(__builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0x140, 0xF, 0xF, true));  // mirrored in 16
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  x = op(__builtin_bit_cast(T, (uint32_t)a[0]), __builtin_bit_cast(T, (uint32_t)a[1]));
+  const uint32_t w = __builtin_bit_cast(uint32_t, x);
+  const auto c = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  return op(__builtin_bit_cast(T, (uint32_t)c[0]), __builtin_bit_cast(T, (uint32_t)c[1]));
+}
+template <typename T>
+__device__ __forceinline__ T wave_sum(T x) {
+  return wave_reduce(x, [](T a, T b) { return a + b; });
+}
+__device__ __forceinline__ float wave_max(float x) {
+  return wave_reduce(x, [](float a, float b) { return fmaxf(a, b); });
 }
 
 // MFMA by the number of query rows (columns): K = 32 of 16 x 16, K = 16 of
