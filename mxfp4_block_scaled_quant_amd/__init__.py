@@ -512,4 +512,4 @@ def linear(x: torch.Tensor, weight: MXFP4Weight, bias: Optional[torch.Tensor] = 
 
 
 from .mla import (mla_cache_append, mla_decode, mla_decode_shared_prefix,  # noqa: E402
-                  mla_decode_workspace_bytes, mla_prefill)
+                  mla_decode_workspace_bytes, mla_prefill, set_mla_rows)

@@ -18,9 +18,17 @@ queries, and works with symbolic sizes.
         out_dtype) -> [M, N]
     torch.ops.mxfp4.a16wfp4_bmm(x, w_pre, ws_pre, N, batch_major, out_dtype)
         -> [B, M, N] or [M, B, N]
+    torch.ops.mxfp4.mla_cache_append(kv, norm_weight, cache, slots, positions,
+        cos_sin, q_pe, q_out, eps, interleaved) -> None   (writes cache and q_out)
+    torch.ops.mxfp4.mla_decode(q, cache, block_table, lengths, scale)
+        -> (out [B, S, H, 512], lse [B, S, H])
+    torch.ops.mxfp4.mla_decode_shared_prefix(q, cache, prefix_table, prefix_len,
+        block_table, lengths, scale) -> (out, lse)
+    torch.ops.mxfp4.mla_prefill(q, k_nope, k_pe, v, cu_q, cu_k, scale, causal)
+        -> (out [Tq, H, dv], lse [Tq, H])
 
-None of the ops mutates its inputs or has an autograd formula (the path is
-inference only).
+mla_cache_append writes the cache and q_out it is given; no other op mutates
+its inputs, and none has an autograd formula (the path is inference only).
 """
 
 from __future__ import annotations
@@ -31,8 +39,9 @@ import torch
 from torch import Tensor
 
 from . import (MXFP4_LAYOUT_GEMM, MXFP4_LAYOUT_ROWMAJOR, a16wfp4_bmm, mxfp4_gemm_a4w4,
-               mxfp4_gemm_a4w4_mxfp4_out, mxfp4_linear, mxfp4_linear_prequantized, mxfp4_preshuffle_weight,
-               mxfp4_quant_1x32, mxfp4_shuffle_scales)
+               mla_cache_append, mla_decode, mla_decode_shared_prefix, mla_prefill, mxfp4_gemm_a4w4_mxfp4_out,
+               mxfp4_linear, mxfp4_linear_prequantized, mxfp4_preshuffle_weight, mxfp4_quant_1x32,
+               mxfp4_shuffle_scales)
 
 __all__ = ["gemm_data_bytes", "gemm_scale_bytes"]
 
@@ -152,3 +161,59 @@ def _(x, w_pre, ws_pre, N, batch_major=False, out_dtype=torch.bfloat16):
     B, M, _ = x.shape
     shape = (M, B, N) if batch_major else (B, M, N)
     return x.new_empty(shape, dtype=out_dtype)
+
+
+@torch.library.custom_op("mxfp4::mla_cache_append", mutates_args=("cache", "q_out"))
+def cache_append(kv: Tensor, norm_weight: Tensor, cache: Tensor, slots: Tensor, positions: Tensor, cos_sin: Tensor,
+                 q_pe: Optional[Tensor] = None, q_out: Optional[Tensor] = None, eps: float = 1e-6,
+                 interleaved: bool = True) -> None:
+    if (q_pe is None) != (q_out is None):
+        raise ValueError("q_pe and q_out are given together")
+    mla_cache_append(kv, norm_weight, cache, slots, positions, cos_sin, q_pe, q_out, eps, interleaved)
+
+
+@cache_append.register_fake
+def _(kv, norm_weight, cache, slots, positions, cos_sin, q_pe=None, q_out=None, eps=1e-6, interleaved=True):
+    return None
+
+
+@torch.library.custom_op("mxfp4::mla_decode", mutates_args=())
+def decode(q: Tensor, cache: Tensor, block_table: Tensor, lengths: Tensor, scale: float) -> Tuple[Tensor, Tensor]:
+    out, lse = mla_decode(q, cache, block_table, lengths, scale, return_lse=True)
+    return out, lse
+
+
+def _decode_fake(q):
+    return (q.new_empty((*q.shape[:-1], 512), dtype=torch.bfloat16),
+            q.new_empty(tuple(q.shape[:-1]), dtype=torch.float32))
+
+
+@decode.register_fake
+def _(q, cache, block_table, lengths, scale):
+    return _decode_fake(q)
+
+
+@torch.library.custom_op("mxfp4::mla_decode_shared_prefix", mutates_args=())
+def decode_shared_prefix(q: Tensor, cache: Tensor, prefix_table: Tensor, prefix_len: int, block_table: Tensor,
+                         lengths: Tensor, scale: float) -> Tuple[Tensor, Tensor]:
+    out, lse = mla_decode_shared_prefix(q, cache, prefix_table, prefix_len, block_table, lengths, scale,
+                                        return_lse=True)
+    return out, lse
+
+
+@decode_shared_prefix.register_fake
+def _(q, cache, prefix_table, prefix_len, block_table, lengths, scale):
+    return _decode_fake(q)
+
+
+@torch.library.custom_op("mxfp4::mla_prefill", mutates_args=())
+def prefill(q: Tensor, k_nope: Tensor, k_pe: Tensor, v: Tensor, cu_q: Tensor, cu_k: Tensor, scale: float,
+            causal: bool = True) -> Tuple[Tensor, Tensor]:
+    out, lse = mla_prefill(q, k_nope, k_pe, v, cu_q, cu_k, scale, causal=causal, return_lse=True)
+    return out, lse
+
+
+@prefill.register_fake
+def _(q, k_nope, k_pe, v, cu_q, cu_k, scale, causal=True):
+    T, H = q.shape[:2]
+    return (q.new_empty((T, H, v.shape[2]), dtype=torch.bfloat16), q.new_empty((T, H), dtype=torch.float32))

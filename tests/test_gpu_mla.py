@@ -425,3 +425,86 @@ def test_streams_and_graph_follow_new_lengths():
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         check(want[0], want[1], A.decode(bits(q), bits(cache), table, now, 0.0625))
+
+
+@pytest.mark.parametrize("rows", [16, 32, 128])
+def test_every_form_on_every_shape(rows):
+    # the row block is chosen by size: here each form runs shapes it would not
+    # be chosen for, with and without a prefix, its own lists and the joins
+    cases = [([1, 0, 130, 33], 1, 16, 16, 0), ([700], 2, 9, 48, 0), ([95, 257], 1, 64, 64, 0),
+             ([5, 70, 4], 2, 20, 64, 257), ([40, 3], 1, 128, 16, 130), ([1500], 3, 50, 64, 0)]
+    try:
+        mx.set_mla_rows(rows)
+        for lens, S, H, page, prefix in cases:
+            cache, table = paged(rows + H, list(lens) + [prefix], page)
+            ptab, own = table[-1, :max(1, -(-prefix // page))].copy(), table[:-1]
+            q = randn(H, len(lens), S, H, 576)
+            out, lse = mx.mla_decode_shared_prefix(q, cache, ints(ptab), prefix, ints(own), ints(lens), 0.0625,
+                                                   return_lse=True)
+            check(out, lse, A.decode(bits(q), bits(cache), own, lens, 0.0625, ptab, prefix))
+    finally:
+        mx.set_mla_rows(0)
+
+
+def test_decode_many_requests():
+    # more requests than a wave's lanes: the shares are found by the whole workgroup
+    lens = [(37 * i) % 211 for i in range(150)]
+    cache, table = paged(5, lens, 16)
+    q = randn(5, 150, 1, 4, 576)
+    out, lse = mx.mla_decode(q, cache, ints(table), ints(lens), 0.0625, return_lse=True)
+    check(out, lse, A.decode(bits(q), bits(cache), table, lens, 0.0625))
+
+
+def test_decode_page_window_moves():
+    # 128-row blocks keep a window of page numbers in LDS: pages of one row
+    # outrun it several times
+    n = 9000
+    cache, table = paged(2, [n], 1)
+    q = randn(3, 1, 1, 128, 576)
+    try:
+        mx.set_mla_rows(128)
+        t = ints(table)
+        out, lse = mx.mla_decode(q, cache, t, ints([n]), 0.05, return_lse=True)
+        one = mx.mla_decode(q[:, :, :16], cache, t, ints([n]), 0.05)
+    finally:
+        mx.set_mla_rows(0)
+    check(out[0, 0], lse[0, 0], _exact_on_gpu(q[0, 0], cache[t[0].long()].reshape(-1, 576)[:n], 0.05))
+    assert torch.equal(one, out[:, :, :16])
+
+
+def test_layer_example_decodes_what_it_prefills():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "latent_attention.py")
+    spec = importlib.util.spec_from_file_location("latent_attention", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    # Both orders round K-up, V-up, probabilities and outputs to bf16 (2^-8
+    # each) at different places: a dozen such roundings of the largest value.
+    for dims in ((192, 256), (128, 128)):
+        decoded, sampled, top = ex.demo(tokens=150, steps=3, samples=3, nope=dims[0], value=dims[1])
+        assert decoded <= 12 * BF * top and sampled <= 12 * BF * top
+
+
+def test_custom_ops_match_the_binding():
+    from mxfp4_block_scaled_quant_amd import ops  # noqa: F401
+    lens = [40, 7]
+    cache, table = paged(9, lens + [30], 16)
+    q = randn(1, 2, 1, 16, 576)
+    t, n, pt = ints(table[:2]), ints(lens), ints(table[2])
+    a, b = torch.ops.mxfp4.mla_decode(q, cache, t, n, 0.0625), mx.mla_decode(q, cache, t, n, 0.0625, return_lse=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    a = torch.ops.mxfp4.mla_decode_shared_prefix(q, cache, pt, 30, t, n, 0.0625)
+    b = mx.mla_decode_shared_prefix(q, cache, pt, 30, t, n, 0.0625, return_lse=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    x = [randn(2, 33, 2, 192), randn(3, 33, 2, 128), randn(4, 33, 64), randn(5, 33, 2, 128)]
+    a = torch.ops.mxfp4.mla_prefill(*x, ints([0, 33]), ints([0, 33]), 0.09)
+    b = mx.mla_prefill(*x, ints([0, 33]), ints([0, 33]), 0.09, return_lse=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    kv, w, cs = randn(5, 2, 576), randn(6, 512), torch.tensor(_angles(50), device="cuda")
+    slots, pos = torch.tensor([3, 17], device="cuda"), torch.tensor([4, 9], device="cuda")
+    one, two, qr = cache.clone(), cache.clone(), randn(7, 2, 16, 64)
+    out = torch.empty_like(qr)
+    torch.ops.mxfp4.mla_cache_append(kv, w, one, slots, pos, cs, qr, out)
+    want = mx.mla_cache_append(kv, w, two, slots, pos, cs, qr)
+    assert torch.equal(one, two) and torch.equal(out, want)

@@ -90,6 +90,16 @@ def test_workspace_query(lib):
     assert f(4, 1, 16, 4096, 1000) > f(4, 1, 16, 4096)
 
 
+def test_rows_hook(lib):
+    for bad in (-1, 8, 64, 256):
+        assert lib.mla_testing_set_rows(bad) == ARG
+    sizes = {}
+    for rows in (16, 32, 128, 0):
+        assert lib.mla_testing_set_rows(rows) == OK
+        sizes[rows] = mx.mla_decode_workspace_bytes(1, 1, 128, 64000)
+    assert sizes[16] < sizes[32] < sizes[128] == sizes[0]     # long, many rows: blocks of 128
+
+
 def test_prefill_entry(lib):
     def call(q=P, qt=16 * 192, qh=192, k=P, kt=2048, kh=128, pe=P, pt=64, v=P, vt=2048, vh=128, cq=P, ck=P, B=1,
              H=16, Tq=5, Tk=5, dn=128, dv=128, causal=1, scale=0.1, out=P, ot=2048, oh=128, lse=None):
