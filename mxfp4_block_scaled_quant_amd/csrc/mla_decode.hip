@@ -39,9 +39,9 @@ constexpr uint32_t kBlock = kTile * 128;
 constexpr int kBlocks = kRowDim / 64;
 constexpr uint32_t kTileBytes = kTile * kRowDim * 2;       // 36 KiB
 constexpr uint32_t kTabLds = 4 * kTileBytes;               // page numbers of the shared form's window
-constexpr int kTabEntries = 3584;
+constexpr int kTabEntries = 3000;
 constexpr uint32_t kMiscLds = kTabLds + kTabEntries * 4;   // scan and softmax exchange
-constexpr uint32_t kLdsBytes = kMiscLds + 2048;
+constexpr uint32_t kLdsBytes = kMiscLds + 4096;
 static_assert(kLdsBytes <= 160 * 1024, "LDS per workgroup");
 
 // What masked keys load: a key past the end or in a page the cache does not
@@ -57,7 +57,7 @@ struct ListArgs {
   int fixed, capacity;   // lengths are clamped to the capacity of a table row
   int B, rows, nt;       // nt row blocks per sequence
   int grid;
-  float *part, *pml;     // parts of items that several workgroups share: [2 grid][RB][512], [..][2]
+  float *part, *pml;     // parts of items that several workgroups share: [2 grid][RB][512], [..][4] (maximum, sums)
   float *ipart, *ipml;   // parts of whole items, by query row (nullptr: write the output)
 };
 
@@ -296,7 +296,7 @@ __device__ __forceinline__ void tile_values(const TileAddr<RW>& at, v8bf (&first
 
 // One 32-key tile in LDS: scores, softmax step, values; `full`: nothing is masked.
 template <int RW>
-__device__ __forceinline__ void attend_tile(uint32_t tile, const LaneAddr<RW>& la, Rows<RW>& st, float& m, float& l,
+__device__ __forceinline__ void attend_tile(uint32_t tile, const LaneAddr<RW>& la, Rows<RW>& st, float& m, RowSums& l,
                                             float c, uint32_t lane, bool full, int seen, uint32_t bad) {
   constexpr int NX = RW / 2;
   float x[NX];
@@ -361,14 +361,13 @@ struct Dest {
 
 template <int RB>
 __device__ __forceinline__ void store_ml(const ListArgs& a, const Dest& to, const RowId& id, int r_in_block, float m,
-                                         float l) {
+                                         const RowSums& l) {
   if (to.whole && !a.ipart) {
-    if (a.d.lse) a.d.lse[flat_row(a.d, id)] = l > 0 ? (m + __builtin_amdgcn_logf(l)) * kLn2 : l == 0 ? kNegInf : l;
+    if (a.d.lse) a.d.lse[flat_row(a.d, id)] = l.log_sum_exp(m);
     return;
   }
-  float* p = to.whole ? a.ipml + 2 * flat_row(a.d, id) : a.pml + 2 * ((int64_t)to.slot * RB + r_in_block);
-  p[0] = m;
-  p[1] = l;
+  float* p = to.whole ? a.ipml + 4 * flat_row(a.d, id) : a.pml + 4 * ((int64_t)to.slot * RB + r_in_block);
+  *(v4f*)p = v4f{m, l.exact, l.used, 0};
 }
 
 // A share's piece of one item: tiles [t0, t1) of sequence b for row block rt.
@@ -386,7 +385,8 @@ __device__ __forceinline__ void attend_split(const ListArgs& a, int b, int n, in
   Rows<RW> st;
   load_query<RW>(a, id, lane, st);
   clear(st);
-  float m = kNegInf, l = 0;
+  float m = kNegInf;
+  RowSums l;
   const LaneAddr<RW> la(lane);
   const int32_t* table = a.table + b * a.ldt;
   // Rows 8g + lane / 8 of a tile: page numbers one tile ahead.
@@ -426,33 +426,29 @@ __device__ __forceinline__ void attend_split(const ListArgs& a, int b, int n, in
   // The four waves' accumulators meet: rescaled to the rows' common maximum,
   // through the wave's own tile, summed in wave order.
   acc_settle();
-  l = rows_sum<RW>(l);
-  lds_f32_t ml = (lds_f32_t)(uintptr_t)kMiscLds;
-  if (lane < RW) {
-    ml[(wv * RW + lane) * 2] = m;
-    ml[(wv * RW + lane) * 2 + 1] = l;
-  }
+  l.exact = rows_sum<RW>(l.exact);
+  l.used = rows_sum<RW>(l.used);
+  lds_v4f_t ml = (lds_v4f_t)(uintptr_t)kMiscLds;
+  if (lane < RW) ml[wv * RW + lane] = v4f{m, l.exact, l.used, 0};
   __syncthreads();
-  auto joined = [&](int r, float& mm, float& ll) {
-    mm = kNegInf;
-    ll = 0;
+  float mm = kNegInf;
+  RowSums ll;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, ml[(w * RW + r) * 2]);
+  for (int w = 0; w < 4; ++w) mm = fmaxf(mm, ml[w * RW + lane % RW][0]);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float lw = ml[(w * RW + r) * 2 + 1];
-      ll += lw == 0 ? 0.0f : lw * __builtin_amdgcn_exp2f(ml[(w * RW + r) * 2] - mm);
-    }
-  };
-  float mm, ll;
-  joined(lane % RW, mm, ll);
+  for (int w = 0; w < 4; ++w) {
+    const v4f o = ml[w * RW + lane % RW];
+    const float fw = o[0] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(o[0] - mm);
+    ll.exact += o[1] * fw;
+    ll.used += o[2] * fw;
+  }
   const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - mm);
   const bool direct = to.whole && !a.ipart;
   // Per row, for the stores: the factor of an output, and where the row goes.
-  lds_f32_t inv = (lds_f32_t)(uintptr_t)(kMiscLds + 1024);
-  lds_i64_t off = (lds_i64_t)(uintptr_t)(kMiscLds + 1024 + 32 * 4);
+  lds_f32_t inv = (lds_f32_t)(uintptr_t)(kMiscLds + 2048);
+  lds_i64_t off = (lds_i64_t)(uintptr_t)(kMiscLds + 2048 + 32 * 4);
   if (threadIdx.x < RW) {
-    inv[lane] = !direct ? 1.0f : ll == 0 ? 0.0f : 1.0f / ll;
+    inv[lane] = direct ? ll.inverse() : 1.0f;
     off[lane] = direct     ? id.b * a.d.sob + id.s * a.d.sos + id.h * a.d.soh
                 : to.whole ? flat_row(a.d, id) * kLatent
                            : ((int64_t)to.slot * RW + lane) * kLatent;
@@ -510,7 +506,8 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
   Rows<RW> st;
   load_query<RW>(a, id, lane, st);
   clear(st);
-  float m = kNegInf, l = 0;
+  float m = kNegInf;
+  RowSums l;
   const int32_t* table = a.table + b * a.ldt;
   const int last_page = (int)page_of(a.d.cache, n - 1);
   lds_i32_t tab = (lds_i32_t)(uintptr_t)kTabLds;
@@ -636,16 +633,17 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
         alpha = mn == m ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
         m = mn;
         mu = m == kNegInf ? 0.0f : m;
-        l *= alpha;
+        l.scale(alpha);
       } else if (i >= 4 && i < 20) {
         const int e = i - 4;
         x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], a.d.c, -mu));
-        l += x[e];
+        l.exact += x[e];
         asm volatile("" : "+v"(x[e]));  // here, not where the values are used
       }
     });
 #pragma unroll
     for (int i = 0; i < 16; ++i) p[i >> 3][i & 7] = (__bf16)x[i];
+    l.used = add_rounded(p[1], add_rounded(p[0], l.used));
 #pragma unroll
     for (int i = 0; i < 3; ++i) bad[i] = bad[i + 1];
   }
@@ -661,7 +659,8 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
   __syncthreads();
 
   acc_settle();
-  l = rows_sum<RW>(l);
+  l.exact = rows_sum<RW>(l.exact);
+  l.used = rows_sum<RW>(l.used);
   const int r_in_block = wv * RW + lane % RW;
   auto column = [&](int i, int j) {  // of a lane's values 4j..4j+3 of column tile i
     return i * RW + (RW == 16 ? 4 * (int)(lane >> 4) : 8 * j + 4 * (int)(lane >> 5));
@@ -694,7 +693,7 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
     }
   } else if (r0 + (int)(lane % RW) < a.rows) {
     const bool direct = !a.ipart;
-    const float inv = l == 0 ? 0.0f : 1.0f / l;
+    const float inv = l.inverse();
     float* part = direct ? nullptr : a.ipart + flat_row(a.d, id) * kLatent;
     uint16_t* out = a.d.out + id.b * a.d.sob + id.s * a.d.sos + id.h * a.d.soh;
 #pragma unroll
@@ -821,7 +820,7 @@ __global__ __launch_bounds__(256) void mla_join_kernel(ListArgs a, ListArgs p) {
   typedef float vec __attribute__((ext_vector_type(CS == 1 ? 4 : W)));
   constexpr int V = CS == 1 ? 4 : W, NV = W / V;  // read as NV vectors, 64 lanes apart
   __shared__ float so[4][512 / CS];
-  __shared__ float sml[4][2];
+  __shared__ float sml[4][3];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int b = blockIdx.x / a.rows, r = blockIdx.x - b * a.rows;
   const int c0 = blockIdx.y * (512 / CS);
@@ -841,24 +840,26 @@ __global__ __launch_bounds__(256) void mla_join_kernel(ListArgs a, ListArgs p) {
     const int64_t slot = q.first + (int64_t)i * q.step - (i > 0 ? q.skip : 0);
     const int64_t k = whole ? flat : in_prefix ? slot * PRB + (int)(flat % (PRB ? PRB : 1)) : slot * RB + r % RB;
     po = (whole ? g.ipart : g.part) + k * kLatent + c0;
-    pm = (whole ? g.ipml : g.pml) + 2 * k;
+    pm = (whole ? g.ipml : g.pml) + 4 * k;
   };
   const int count = pre.count + own.count;
-  float m = kNegInf, l = 0;
+  float m = kNegInf;
+  RowSums l;
   vec o[NV] = {};
   for (int i0 = wv; i0 < count; i0 += 256) {  // 64 parts of this wave
     const int mine = i0 + 4 * lane, n = min(64, (count - i0 + 3) / 4);
     const float *po, *pm;
-    float pmx = kNegInf, pl = 0;
+    v4f pl = {kNegInf, 0, 0, 0};
     if (lane < n) {
       part_at(mine, po, pm);
-      pmx = pm[0];
-      pl = pm[1];
+      pl = *(const v4f*)pm;
     }
-    const float mn = fmaxf(wave_max(pmx), m);
+    const float mn = fmaxf(wave_max(pl[0]), m);
     const float keep = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
-    const float f = pl == 0 ? 0.0f : __builtin_amdgcn_exp2f(pmx - mn);  // a part without keys counts nothing
-    l = l * keep + wave_sum(pl * f);
+    const float f = pl[1] == 0 ? 0.0f : __builtin_amdgcn_exp2f(pl[0] - mn);  // a part without keys counts nothing
+    l.scale(keep);
+    l.exact += wave_sum(pl[1] * f);
+    l.used += wave_sum(pl[2] * f);
     m = mn;
 #pragma unroll
     for (int v = 0; v < NV; ++v) o[v] *= keep;
@@ -878,24 +879,26 @@ __global__ __launch_bounds__(256) void mla_join_kernel(ListArgs a, ListArgs p) {
   for (int v = 0; v < NV; ++v) *(vec*)&so[wv][v * 64 * V + V * lane] = o[v];
   if (lane == 0) {
     sml[wv][0] = m;
-    sml[wv][1] = l;
+    sml[wv][1] = l.exact;
+    sml[wv][2] = l.used;
   }
   __syncthreads();
   if (threadIdx.x >= 128 / CS) return;
   m = fmaxf(fmaxf(sml[0][0], sml[1][0]), fmaxf(sml[2][0], sml[3][0]));
-  l = 0;
+  l = RowSums();
   v4f t = {0, 0, 0, 0};
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    const float lw = sml[w][1], f = lw == 0 ? 0.0f : __builtin_amdgcn_exp2f(sml[w][0] - m);
-    l += lw * f;
+    const float f = sml[w][1] == 0 ? 0.0f : __builtin_amdgcn_exp2f(sml[w][0] - m);
+    l.exact += sml[w][1] * f;
+    l.used += sml[w][2] * f;
     t += *(const v4f*)&so[w][4 * threadIdx.x] * f;
   }
-  const float inv = l == 0 ? 0.0f : 1.0f / l;
+  const float inv = l.inverse();
   const uint2 w = {pack_bf16x2(t[0] * inv, t[1] * inv), pack_bf16x2(t[2] * inv, t[3] * inv)};
   *(uint2*)(a.d.out + id.b * a.d.sob + id.s * a.d.sos + id.h * a.d.soh + c0 + 4 * threadIdx.x) = w;
   if (a.d.lse && threadIdx.x == 0 && blockIdx.y == 0)
-    a.d.lse[flat] = l > 0 ? (m + __builtin_amdgcn_logf(l)) * kLn2 : l == 0 ? kNegInf : l;
+    a.d.lse[flat] = l.log_sum_exp(m);
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -968,15 +971,15 @@ DecodePlan decode_plan(int64_t B, int64_t S, int64_t H, int64_t max_tokens, int6
     return r;
   };
   d.part = take(2ll * d.grid * d.rows * kLatent);
-  d.pml = take(2ll * d.grid * d.rows * 2);
+  d.pml = take(2ll * d.grid * d.rows * 4);
   if (prefix_len > 0) {
     d.prows = rows_per_block(1, B * rows, prefix_len);
     units = cdiv(B * rows, d.prows) * cdiv(prefix_len, unit_keys(d.prows));
     d.pgrid = (int)(units < cus ? units : cus);
     d.ppart = take(2ll * d.pgrid * d.prows * kLatent);
-    d.ppml = take(2ll * d.pgrid * d.prows * 2);
+    d.ppml = take(2ll * d.pgrid * d.prows * 4);
     d.ipart = take(2 * B * rows * kLatent);
-    d.ipml = take(2 * B * rows * 2);
+    d.ipml = take(2 * B * rows * 4);
   }
   d.floats = at;
   return d;
@@ -1012,7 +1015,7 @@ hipError_t launch_mla_decode(const DecodeArgs& d, const DecodePlan& plan, hipStr
     p.part = d.work + plan.ppart;
     p.pml = d.work + plan.ppml;
     p.ipart = a.ipart + all * kLatent;
-    p.ipml = a.ipml + 2 * all;
+    p.ipml = a.ipml + 4 * all;
     // (Prefix blocks of 32 rows, a batch of 17 to 32 rows over a long prefix,
     // take two launches: no code of their own for every pair of forms.)
     hipError_t e;

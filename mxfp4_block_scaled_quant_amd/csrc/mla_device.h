@@ -174,13 +174,36 @@ constexpr float kLn2 = 0.6931471805599453f;
 // changes no relative rounding, and most tiles rescale nothing.
 constexpr float kLag = 8.0f;
 
+// A row's sums of probabilities: of the exact ones, for the log-sum-exp, and
+// of the bf16 ones the value product takes, for the output's division.  What
+// rounding does to a probability then moves the weights but not their sum: a
+// row that one key dominates keeps that key's value to the last bit.
+struct RowSums {
+  float exact = 0, used = 0;
+  __device__ __forceinline__ void scale(float f) {
+    exact *= f;
+    used *= f;
+  }
+  __device__ __forceinline__ float inverse() const { return used == 0 ? 0.0f : 1.0f / used; }
+  __device__ __forceinline__ float log_sum_exp(float m) const {  // m: the maximum, in units of log2
+    return exact > 0 ? (m + __builtin_amdgcn_logf(exact)) * kLn2 : exact == 0 ? kNegInf : exact;
+  }
+};
+// Two rounded probabilities a step: their dot product with ones.
+__device__ __forceinline__ float add_rounded(const v8bf& p, float sum) {
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  const v2bf one = {(__bf16)1.0f, (__bf16)1.0f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum = __builtin_amdgcn_fdot2_f32_bf16(v2bf{p[2 * i], p[2 * i + 1]}, one, sum, false);
+  return sum;
+}
+
 // Probabilities of a tile from its scores x (one query row per lane):
 // updates the row's maximum m (in units of log2, scores times c) and the
-// lane's share l of the row's sum, rounds to bf16 operands (the sum takes
-// the unrounded values: the log-sum-exp is exact to fp32).  alpha != 1 asks
-// the caller to rescale its accumulators; true if any lane's is.
+// lane's share of the row's sums, rounds to bf16 operands.  True if any
+// row's maximum rose: the caller then rescales its accumulators by alpha.
 template <int RW, int NX>
-__device__ __forceinline__ bool softmax_step(float (&x)[NX], float c, float& m, float& l, float& alpha,
+__device__ __forceinline__ bool softmax_step(float (&x)[NX], float c, float& m, RowSums& l, float& alpha,
                                              v8bf (&p)[NX / 8]) {
   float mx = x[0];
 #pragma unroll
@@ -192,13 +215,13 @@ __device__ __forceinline__ bool softmax_step(float (&x)[NX], float c, float& m, 
     const float mn = fmaxf(m, mx);
     alpha = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
     m = mn;
-    l *= alpha;
+    l.scale(alpha);
   }
   const float mu = m == kNegInf ? 0.0f : m;  // a row that has seen nothing yet
 #pragma unroll
   for (int i = 0; i < NX; ++i) {
     x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c, -mu));
-    l += x[i];
+    l.exact += x[i];
   }
 #pragma unroll
   for (int i = 0; i < NX / 8; ++i) {
@@ -206,6 +229,7 @@ __device__ __forceinline__ bool softmax_step(float (&x)[NX], float c, float& m, 
 #pragma unroll
     for (int j = 0; j < 8; ++j) t[j] = (__bf16)x[8 * i + j];
     p[i] = t;
+    l.used = add_rounded(t, l.used);
   }
   return grew;
 }

