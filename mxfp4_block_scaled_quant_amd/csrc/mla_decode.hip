@@ -285,10 +285,13 @@ __device__ __forceinline__ void score_product(v16f& s, int i, v8bf f, v8bf q) {
   else mfma_vgpr<false, false>(s, f, q);
 }
 
+// Products between LDS reads and their use: the short ones need more of them.
 template <int RW>
-__device__ __forceinline__ void tile_values(const TileAddr<RW>& at, v8bf (&first)[4], Rows<RW>& st,
+constexpr int kValueGroup = RW == 16 ? 8 : 4;
+template <int RW>
+__device__ __forceinline__ void tile_values(const TileAddr<RW>& at, v8bf (&first)[kValueGroup<RW>], Rows<RW>& st,
                                             const v8bf (&p)[RW / 16]) {
-  pipeline<32, 4>(first, [&](int i) { return at.value(i); }, [&](int i, v8bf f) {
+  pipeline<32, kValueGroup<RW>>(first, [&](int i) { return at.value(i); }, [&](int i, v8bf f) {
     if constexpr (RW == 16) st.o[i] = mfma_rows(f, p[0], st.o[i]);
     else st.o[i >> 1] = mfma_rows(f, p[i & 1], st.o[i >> 1]);
   });
@@ -304,10 +307,10 @@ __device__ __forceinline__ void attend_tile(uint32_t tile, const LaneAddr<RW>& l
   auto key = [&](int i) { return at.key(i); };
   auto value = [&](int i) { return at.value(i); };
   if constexpr (RW == 16) {
-    v8bf ahead[4];
+    v8bf ahead[6];
     read_group(ahead, key);
     v4f s[2] = {};
-    pipeline<36, 4>(ahead, key, [&](int i, v8bf f) { s[i & 1] = mfma_rows(f, st.q[i >> 1], s[i & 1]); });
+    pipeline<36, 6>(ahead, key, [&](int i, v8bf f) { s[i & 1] = mfma_rows(f, st.q[i >> 1], s[i & 1]); });
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = s[i >> 2][i & 3];
   } else {
@@ -318,7 +321,7 @@ __device__ __forceinline__ void attend_tile(uint32_t tile, const LaneAddr<RW>& l
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = s[i];
   }
-  v8bf first[4];
+  v8bf first[kValueGroup<RW>];
   read_group(first, value);
   if (!full) mask_scores<RW, NX>(x, lane, seen, bad);
   float alpha;
@@ -382,9 +385,6 @@ __device__ __forceinline__ void attend_split(const ListArgs& a, int b, int n, in
   const int seen = a.lens ? causal + id.s : n;
   const int seen_all = a.lens ? causal + r0 / a.d.H : n;
 
-  Rows<RW> st;
-  load_query<RW>(a, id, lane, st);
-  clear(st);
   float m = kNegInf;
   RowSums l;
   const LaneAddr<RW> la(lane);
@@ -399,6 +399,9 @@ __device__ __forceinline__ void attend_split(const ListArgs& a, int b, int n, in
     }
   };
   lookup(t0 + wv);
+  Rows<RW> st;  // (behind the page numbers, which the first rows wait for)
+  load_query<RW>(a, id, lane, st);
+  clear(st);
   for (int t = t0 + wv; t < t1; t += 4) {
     uint64_t hidden[4];
     wait_lds();
@@ -406,7 +409,7 @@ __device__ __forceinline__ void attend_split(const ListArgs& a, int b, int n, in
     for (int g = 0; g < 4; ++g) {
       bool ok;
       const char* ptr = row_at(a.d.cache, t * kTile + 8 * g + (lane >> 3), page[g], ok) + load_chunk(lane, g);
-      hidden[g] = __builtin_amdgcn_ballot_w64(!ok);
+      hidden[g] = __builtin_amdgcn_ballot_w64(!ok && t * kTile + 8 * g + (int)(lane >> 3) < n);
       // One row block: nothing else reads these rows, and loads that leave
       // no trace in the caches run faster (128 requests of up to 16000 rows:
       // 218 -> 196 us, 5.4 TB/s).
@@ -414,7 +417,7 @@ __device__ __forceinline__ void attend_split(const ListArgs& a, int b, int n, in
       else load_group<false>(tile + g * 1024, ptr);
     }
     lookup(t + 4);
-    uint32_t bad = 0;  // (seldom more than the keys past the end)
+    uint32_t bad = 0;  // keys in pages that the cache does not have (those past the end are not `seen`)
     if ((hidden[0] | hidden[1] | hidden[2] | hidden[3]) != 0) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) bad |= (uint32_t)((hidden[i >> 3] >> (8 * (i & 7))) & 1) << i;
@@ -430,7 +433,7 @@ __device__ __forceinline__ void attend_split(const ListArgs& a, int b, int n, in
   l.used = rows_sum<RW>(l.used);
   lds_v4f_t ml = (lds_v4f_t)(uintptr_t)kMiscLds;
   if (lane < RW) ml[wv * RW + lane] = v4f{m, l.exact, l.used, 0};
-  __syncthreads();
+  lds_barrier();
   float mm = kNegInf;
   RowSums ll;
 #pragma unroll
@@ -471,7 +474,7 @@ __device__ __forceinline__ void attend_split(const ListArgs& a, int b, int n, in
         *(lds_v4f_t)(uintptr_t)(tile + (lane % RW) * LD + col * 4) = v;
       }
     }
-    __syncthreads();
+    lds_barrier();
 #pragma unroll 4
     for (int it = 0; it < RW * C / 1024; ++it) {
       const int e = it * 256 + threadIdx.x, r = e / (C / 4), col = e % (C / 4) * 4;
@@ -488,7 +491,7 @@ __device__ __forceinline__ void attend_split(const ListArgs& a, int b, int n, in
         }
       }
     }
-    __syncthreads();
+    lds_barrier();
   }
 }
 
@@ -629,8 +632,8 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
       } else if (i == 1) {
         mx = rows_max<RW>(mx) * a.d.c;
         const float mn = mx > m + kLag ? mx : m;
-        grew = __builtin_amdgcn_ballot_w64(mn != m) != 0;
-        alpha = mn == m ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+        alpha = mn == m || m == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+        grew = __builtin_amdgcn_ballot_w64(alpha != 1.0f) != 0;
         m = mn;
         mu = m == kNegInf ? 0.0f : m;
         l.scale(alpha);
@@ -713,7 +716,7 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
     }
   }
   if (lane < RW && r0 + (int)lane < a.rows) store_ml<RB>(a, to, id, r_in_block, m, l);
-  __syncthreads();
+  lds_barrier();
 }
 
 template <int RB>

@@ -66,12 +66,13 @@ __host__ __device__ constexpr uint32_t bitrev4(uint32_t r) {
 
 // Direct loads of 16 bytes per lane to LDS at `lds` + 16 lane, from a
 // uniform base plus a lane's byte offset, or OFF bytes past a lane's own
-// address.  (M0 holds the LDS base; one wait state after it is written.  A
+// address.  (M0 holds the LDS base; one wait state after it is written;
+// nothing else in these kernels uses it.  A
 // base that a vector instruction wrote would need five: the compiler does
 // not count them into an assembly statement, so there are four here.)
 __device__ __forceinline__ void dma16(uint32_t lds, const void* base, uint32_t voff) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2"
-               :: "s"(lds), "v"(voff), "s"(base) : "memory", "m0");
+               :: "s"(lds), "v"(voff), "s"(base) : "memory");
 }
 // (The instruction adds its immediate offset to the LDS address too.)
 // STREAM: rows that nothing reads again are loaded past the caches.
@@ -80,10 +81,10 @@ __device__ __forceinline__ void dma16_at(uint32_t lds, const void* p) {
   lds -= OFF;
   if constexpr (STREAM)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2 nt"
-                 :: "s"(lds), "v"(p), "i"(OFF) : "memory", "m0");
+                 :: "s"(lds), "v"(p), "i"(OFF) : "memory");
   else
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2"
-                 :: "s"(lds), "v"(p), "i"(OFF) : "memory", "m0");
+                 :: "s"(lds), "v"(p), "i"(OFF) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -94,6 +95,12 @@ __device__ __forceinline__ void wave_barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+
+// A barrier for LDS alone: stores to memory stay under way across it.
+__device__ __forceinline__ void lds_barrier() {
+  wait_lds();
+  wave_barrier();
 }
 
 // The larger / the sum of x over the lanes that share a query row: lanes
@@ -211,9 +218,9 @@ __device__ __forceinline__ bool softmax_step(float (&x)[NX], float c, float& m, 
   mx = rows_max<RW>(mx) * c;
   bool grew = false;
   if (__builtin_amdgcn_ballot_w64(mx > m + kLag)) {
-    grew = true;
     const float mn = fmaxf(m, mx);
-    alpha = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+    alpha = m == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+    grew = __builtin_amdgcn_ballot_w64(alpha != 1.0f) != 0;  // (no row's first keys: zeros need no scaling)
     m = mn;
     l.scale(alpha);
   }
