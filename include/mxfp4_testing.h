@@ -41,6 +41,14 @@ int mxfp4_testing_set_gemm_path(int path);
  * Returns MXFP4_OK, or MXFP4_ERR_ARG for other values.
  */
 int mla_testing_set_rows(int rows);
+
+/*
+ * Forces mla_prefill's query rows per workgroup on this thread: 32 (its waves
+ * share the keys between them) or 128 (and more: its waves share the rows);
+ * 0 = choose by the rows (the default).
+ * Returns MXFP4_OK, or MXFP4_ERR_ARG for other values.
+ */
+int mla_testing_set_prefill_rows(int rows);
 #pragma GCC visibility pop
 
 #ifdef __cplusplus

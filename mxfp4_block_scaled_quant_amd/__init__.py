@@ -99,6 +99,7 @@ _SIGNATURES = {
                     + [_c_i64] * 6 + [_c_int, _c_f32, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp]),
     "mxfp4_testing_set_gemm_path": (_c_int, [_c_int]),
     "mla_testing_set_rows": (_c_int, [_c_int]),
+    "mla_testing_set_prefill_rows": (_c_int, [_c_int]),
 }
 
 _lib_handle = None
@@ -512,4 +513,4 @@ def linear(x: torch.Tensor, weight: MXFP4Weight, bias: Optional[torch.Tensor] = 
 
 
 from .mla import (mla_cache_append, mla_decode, mla_decode_shared_prefix,  # noqa: E402
-                  mla_decode_workspace_bytes, mla_prefill, set_mla_rows)
+                  mla_decode_workspace_bytes, mla_prefill, set_mla_prefill_rows, set_mla_rows)

@@ -13,6 +13,7 @@ namespace mxfp4 {
 
 // The test hook's forced row block: per thread, like the GEMM path's.
 static thread_local int t_rows = 0;
+static thread_local int t_prefill_rows = 0;
 int get_mla_rows_override() { return t_rows; }
 
 namespace {
@@ -274,13 +275,19 @@ int mla_prefill(const void* q, int64_t q_token, int64_t q_head, const void* k_no
   p.sot = out_token;
   p.soh = out_head;
   p.lse = (float*)lse;
-  return launched(launch_mla_prefill(p, (int)dn, (int)dv, cus, (hipStream_t)stream));
+  return launched(launch_mla_prefill(p, (int)dn, (int)dv, t_prefill_rows, cus, (hipStream_t)stream));
 }
 
-// Test hook (include/mxfp4_testing.h): force the decode form on this thread.
+// Test hooks (include/mxfp4_testing.h): force the forms on this thread.
 int mla_testing_set_rows(int rows) {
   if (rows != 0 && rows != 16 && rows != 32 && rows != 128) return MXFP4_ERR_ARG;
   t_rows = rows;
+  return MXFP4_OK;
+}
+
+int mla_testing_set_prefill_rows(int rows) {
+  if (rows != 0 && rows != 32 && rows != 128) return MXFP4_ERR_ARG;
+  t_prefill_rows = rows;
   return MXFP4_OK;
 }
 

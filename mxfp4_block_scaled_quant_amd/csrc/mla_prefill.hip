@@ -6,8 +6,22 @@
 // One pass over the keys with a running maximum and sum (fp32).  A workgroup
 // takes a block of query rows of one head of one sequence, 32 rows a wave,
 // and walks the keys in 32-key tiles that all its waves share in a ring of
-// LDS stages; loads run ahead of the barrier that hands a tile over.  Bound
-// by the matrix units: 2 (dn + 64 + dv) operations per (query, key) pair.
+// four LDS stages; loads run three tiles ahead of the barrier that hands a
+// tile over.  Later rows see more keys and start first.
+//
+// Bound by the matrix units, and they by the card's power: 2 (dn + 64 + dv)
+// operations per (query, key) pair, 16384 causal tokens of 16 heads at
+// 192 + 64 and 256: 1.94-2.03 ms, 1.08-1.13 PFLOP/s; 2 x 1900-2048 tokens after 14003
+// others at 128 + 64 and 128: 0.65-0.69 ms, 0.9.  The clock falls to 1.65 GHz
+// under it; the same launch on zeros reaches 1.35 PFLOP/s, and a library
+// product of random 8192 x 8192 matrices 1.44.  One stage costs 32 KiB at
+// values of 256 and 20 KiB at 128, so a compute unit holds one workgroup of
+// eight waves or two of four; four waves with two stages at 256 measured the
+// same, as did softmax steps spread between the products.
+//
+// Few query rows leave most compute units idle that way, each workgroup
+// walking all of its keys alone: there the four waves of a workgroup take 32
+// rows together and a quarter of the keys each (mla_prefill_few_kernel).
 #include "mla_device.h"
 #include "mla_launch.h"
 
@@ -69,12 +83,93 @@ __device__ __forceinline__ bool find_block(const MlaPrefillArgs& a, int blk, int
   return false;
 }
 
+// The rows of sequence b.  Offsets are clamped to the packed tensors: bad ones
+// cannot leave them.
+struct Span {
+  int64_t q0, k0;
+  int nq, nk;
+  __device__ __forceinline__ Span(const MlaPrefillArgs& a, int b) {
+    q0 = max((int64_t)0, min(a.Tq, (int64_t)a.cu_q[b]));
+    k0 = max((int64_t)0, min(a.Tk, (int64_t)a.cu_k[b]));
+    nq = (int)(max(q0, min(a.Tq, (int64_t)a.cu_q[b + 1])) - q0);
+    nk = (int)(max(k0, min(a.Tk, (int64_t)a.cu_k[b + 1])) - k0);
+  }
+};
+
+// A row's outputs: columns 32 i + 8 j + 4 (lane / 32) + (0..3) are 4 j.. of
+// the lane's accumulator of column tile i.
+__device__ __forceinline__ void store_columns(uint16_t* out, uint32_t lane, int i, int j, v4f o, float inv) {
+  const uint2 w = {pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
+  *(uint2*)(out + 32 * i + 8 * j + 4 * (lane >> 5)) = w;
+}
+
+// A wave's work on one tile of keys in LDS, for its 32 query rows: scores,
+// softmax step, values.  G: LDS operands read ahead.
+template <int DN, int DV, int G>
+struct Tile {
+  using St = Stage<DN, DV>;
+  static constexpr int kSteps = (DN + kRope) / 16, kCols = DV / 32;
+  // Lane addresses within a stage.  Rows start at multiples of their length,
+  // so a step's chunk is one XOR away and its row group an immediate offset.
+  uint32_t lane, ka, kb, va;
+  __device__ __forceinline__ explicit Tile(uint32_t lane) : lane(lane) {
+    const uint32_t kr = lane & 31, hh = lane >> 5, i16 = lane & 15, vr = 4 * hh + (i16 >> 2);
+    ka = kr * 256 + ((hh ^ bitrev4(kr & 15)) << 4);
+    kb = St::kB + kr * 128 + ((hh ^ ((kr >> 1) & 7)) << 4);
+    va = St::kV + vr * (DV * 2) + (i16 & 1) * 8 +
+         (((2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1)) ^ bitrev4(vr)) << 4);
+  }
+  // `at`: the tile in LDS; `key`: its first key; `seen`: keys the lane's row
+  // sees; `masked`: some row of the wave does not see all of the tile;
+  // `scored()` runs between the last read of the keys and the first of the values.
+  template <typename Scored>
+  __device__ __forceinline__ void attend(uint32_t at, int key, const v8bf (&q)[kSteps], v16f (&o)[kCols], float& m,
+                                         RowSums& l, float c, int seen, bool masked, Scored scored) const {
+    // (opaque, so that the steps' addresses are computed here and not kept)
+    uint32_t ta = ka + at, tb = kb + at, tv = va + at;
+    asm volatile("" : "+v"(ta), "+v"(tb), "+v"(tv));
+    auto key_frag = [&](int k) {
+      if (k < 8) return lds_read16(ta ^ ((2 * k) << 4));
+      const int i = k < DN / 16 ? k - 8 : k - DN / 16;
+      return lds_read16((tb ^ ((2 * i) << 4)) + (k < DN / 16 ? 0 : St::kPe - St::kB));
+    };
+    v8bf first[G];
+    read_group(first, key_frag);
+    v16f s = {};
+    pipeline<kSteps, G>(first, key_frag, [&](int k, v8bf f) { s = mfma_rows(f, q[k], s); });
+    scored();
+    // Step i of the values: column tile i / 2 over keys 0-15 or 16-31.
+    auto value_frag = [&](int i) {
+      const int ct = i >> 1;
+      const uint32_t c0 = ((4 * ct) & 15) << 4, c1 = (ct >> 2) * 256 + (i & 1) * 16 * DV * 2;
+      return join_keys(lds_read_tr((tv ^ c0) + c1), lds_read_tr((tv ^ (c0 | 16)) + c1 + 8 * DV * 2));
+    };
+    read_group(first, value_frag);
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = s[i];
+    if (masked) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (key + key_of<32>(i, lane) >= seen) x[i] = kNegInf;
+    }
+    float alpha;
+    v8bf p[2];
+    if (softmax_step<32, 16>(x, c, m, l, alpha, p)) {
+#pragma unroll
+      for (int i = 0; i < kCols; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] *= alpha;
+    }
+    pipeline<2 * kCols, G>(first, value_frag, [&](int i, v8bf f) { o[i >> 1] = mfma_rows(f, p[i & 1], o[i >> 1]); });
+  }
+};
+
 template <int DN, int DV, int NW, int NS>
 __global__ __launch_bounds__(64 * NW, 2) void mla_prefill_kernel(MlaPrefillArgs a) {
   using St = Stage<DN, DV>;
   using C = Cfg<DN, DV, NW, NS>;
   constexpr int R = 32 * NW, kSteps = (DN + kRope) / 16, kCols = DV / 32;
-  constexpr int G = DV == 256 ? 2 : 4;  // LDS operands read ahead: what the registers leave
   __shared__ int4 lds_raw[C::kLds / 16];
   uint32_t anchor = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int4*)lds_raw;
   asm volatile("" : "+s"(anchor)::"memory");  // LDS is addressed by number: its array starts at 0
@@ -86,10 +181,7 @@ __global__ __launch_bounds__(64 * NW, 2) void mla_prefill_kernel(MlaPrefillArgs 
   if (!find_block<R>(a, blockIdx.x / a.H, b, blk)) return;
   b = __builtin_amdgcn_readfirstlane(b);
   blk = __builtin_amdgcn_readfirstlane(blk);
-  // Offsets are clamped to the packed tensors: bad ones cannot leave them.
-  const int64_t q0 = max((int64_t)0, min(a.Tq, (int64_t)a.cu_q[b])), q1 = max(q0, min(a.Tq, (int64_t)a.cu_q[b + 1]));
-  const int64_t k0 = max((int64_t)0, min(a.Tk, (int64_t)a.cu_k[b])), k1 = max(k0, min(a.Tk, (int64_t)a.cu_k[b + 1]));
-  const int nq = (int)(q1 - q0), nk = (int)(k1 - k0);
+  const auto [q0, k0, nq, nk] = Span(a, b);
   const int r0 = blk * R;                      // first query row of the block
   if (r0 >= nq) return;
   const int wr0 = r0 + wv * 32;                // of the wave
@@ -152,13 +244,7 @@ __global__ __launch_bounds__(64 * NW, 2) void mla_prefill_kernel(MlaPrefillArgs 
 #pragma unroll
   for (int t = 0; t < NS - 1; ++t)
     if (t < nt) issue(t, t * St::kBytes);
-  // Lane addresses within a stage.  Rows start at multiples of their length,
-  // so a step's chunk is one XOR away and its row group an immediate offset.
-  const uint32_t kr = lane & 31, hh = lane >> 5, i16 = lane & 15, vr = 4 * hh + (i16 >> 2);
-  uint32_t ka = kr * 256 + ((hh ^ bitrev4(kr & 15)) << 4);
-  uint32_t kb = St::kB + kr * 128 + ((hh ^ ((kr >> 1) & 7)) << 4);
-  uint32_t va = St::kV + vr * (DV * 2) + (i16 & 1) * 8 +
-                (((2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1)) ^ bitrev4(vr)) << 4);
+  const Tile<DN, DV, DV == 256 ? 2 : 4> at_tile(lane);  // (groups: what the registers leave)
   uint32_t tile = 0, fill = (NS - 1) * St::kBytes;  // this tile's stage, and the next to load
   for (int t = 0; t < nt; ++t) {
     if (t + 2 < nt) wait_loads<2 * C::kPer>();
@@ -172,42 +258,7 @@ __global__ __launch_bounds__(64 * NW, 2) void mla_prefill_kernel(MlaPrefillArgs 
     tile = tile + St::kBytes == NS * St::kBytes ? 0 : tile + St::kBytes;
     if (t >= wave_tiles) continue;
 
-    // (opaque, so that the steps' addresses are computed here and not kept)
-    uint32_t ta = ka + at, tb = kb + at, tv = va + at;
-    asm volatile("" : "+v"(ta), "+v"(tb), "+v"(tv));
-    auto key_frag = [&](int k) {
-      if (k < 8) return lds_read16(ta ^ ((2 * k) << 4));
-      const int i = k < DN / 16 ? k - 8 : k - DN / 16;
-      return lds_read16((tb ^ ((2 * i) << 4)) + (k < DN / 16 ? 0 : St::kPe - St::kB));
-    };
-    v8bf first[G];
-    read_group(first, key_frag);
-    v16f s = {};
-    pipeline<kSteps, G>(first, key_frag, [&](int k, v8bf f) { s = mfma_rows(f, q[k], s); });
-    // Step i of the values: column tile i / 2 over keys 0-15 or 16-31.
-    auto value_frag = [&](int i) {
-      const int ct = i >> 1;
-      const uint32_t c0 = ((4 * ct) & 15) << 4, c1 = (ct >> 2) * 256 + (i & 1) * 16 * DV * 2;
-      return join_keys(lds_read_tr((tv ^ c0) + c1), lds_read_tr((tv ^ (c0 | 16)) + c1 + 8 * DV * 2));
-    };
-    read_group(first, value_frag);
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = s[i];
-    if ((t + 1) * kTile > seen_first) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (t * kTile + key_of<32>(i, lane) >= seen) x[i] = kNegInf;
-    }
-    float alpha;
-    v8bf p[2];
-    if (softmax_step<32, 16>(x, a.c, m, l, alpha, p)) {
-#pragma unroll
-      for (int i = 0; i < kCols; ++i)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) o[i][j] *= alpha;
-    }
-    pipeline<2 * kCols, G>(first, value_frag, [&](int i, v8bf f) { o[i >> 1] = mfma_rows(f, p[i & 1], o[i >> 1]); });
+    at_tile.attend(at, t * kTile, q, o, m, l, a.c, seen, (t + 1) * kTile > seen_first, [] {});
   }
 
   l.exact = rows_sum<32>(l.exact);
@@ -218,22 +269,165 @@ __global__ __launch_bounds__(64 * NW, 2) void mla_prefill_kernel(MlaPrefillArgs 
 #pragma unroll
   for (int i = 0; i < kCols; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint2 w = {pack_bf16x2(o[i][4 * j] * inv, o[i][4 * j + 1] * inv),
-                       pack_bf16x2(o[i][4 * j + 2] * inv, o[i][4 * j + 3] * inv)};
-      *(uint2*)(out + 32 * i + 8 * j + 4 * (lane >> 5)) = w;
-    }
+    for (int j = 0; j < 4; ++j)
+      store_columns(out, lane, i, j, v4f{o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]}, inv);
   if (a.lse && lane < 32)
     a.lse[(q0 + row) * a.H + h] = l.log_sum_exp(m);
 }
 
+// The same for few query rows: a workgroup takes 32 of them, its four waves
+// walk every fourth tile of their keys, each through a ring of LDS stages of
+// its own (no barriers), and join their sums at the end, in the waves' order.
+template <int DN, int DV, int NS>
+__global__ __launch_bounds__(256, 1) void mla_prefill_few_kernel(MlaPrefillArgs a) {
+  using St = Stage<DN, DV>;
+  constexpr int kSteps = (DN + kRope) / 16, kCols = DV / 32, kMine = kCols / 4;
+  constexpr uint32_t kSums = 4 * 32 * DV * 4;  // after the waves' outputs: maxima, sums
+  constexpr uint32_t kLds = 4 * NS * St::kBytes > kSums + 4 * 64 * 16 ? 4 * NS * St::kBytes : kSums + 4 * 64 * 16;
+  static_assert(kLds <= 160 * 1024, "LDS per workgroup");
+  __shared__ int4 lds_raw[kLds / 16];
+  uint32_t anchor = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int4*)lds_raw;
+  asm volatile("" : "+s"(anchor)::"memory");  // LDS is addressed by number: its array starts at 0
+
+  const uint32_t lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = blockIdx.x % a.H;
+  int b, blk;
+  if (!find_block<32>(a, blockIdx.x / a.H, b, blk)) return;
+  b = __builtin_amdgcn_readfirstlane(b);
+  blk = __builtin_amdgcn_readfirstlane(blk);
+  const auto [q0, k0, nq, nk] = Span(a, b);
+  const int r0 = blk * 32;
+  if (r0 >= nq) return;
+  const int row = r0 + (int)(lane & 31);
+  const int past = a.causal ? nk - nq + 1 : nk;
+  auto sees = [&](int r) { return a.causal ? min(nk, past + r) : nk; };
+  const int seen = sees(row), seen_first = sees(r0);
+  const int nt = (max(0, sees(min(r0 + 32, nq) - 1)) + kTile - 1) / kTile;
+
+  // A tile's loads, 1 KiB each: a part's base (the tile's first row) and the
+  // lane's offset, which names a row and the row's permuted chunk.
+  const char* base[3] = {(const char*)(a.k + k0 * a.skt + h * a.skh), (const char*)(a.k_pe + k0 * a.spt),
+                         (const char*)(a.v + k0 * a.svt + h * a.svh)};
+  const uint32_t pitch[3] = {(uint32_t)a.skt * 2, (uint32_t)a.spt * 2, (uint32_t)a.svt * 2};
+  constexpr int kKeyLoads = St::kV / 1024, kValueLoads = St::kLoads - kKeyLoads;
+  auto issue = [&](int t, uint32_t lds, auto values) {
+    const int left = nk - t * kTile;  // rows of the tile that exist: past them the last one is loaded again
+    const char* tile[3];
+#pragma unroll
+    for (int p = 0; p < 3; ++p) tile[p] = base[p] + (int64_t)t * kTile * pitch[p];
+#pragma unroll
+    for (int i = values ? kKeyLoads : 0; i < (values ? St::kLoads : kKeyLoads); ++i) {
+      const uint32_t at = i * 1024;
+      const bool second = DN > 128 && at >= St::kB && at < St::kPe;
+      const int part = at < St::kPe ? 0 : at < St::kV ? 1 : 2;
+      const int shift = at < St::kB ? 4 : at < St::kV ? 3 : DV == 256 ? 5 : 4;  // log2 of a row's chunks
+      const uint32_t start = at < St::kB ? 0 : second ? St::kB : at < St::kV ? St::kPe : St::kV;
+      const uint32_t r = ((at - start) >> (shift + 4)) + (lane >> shift), ch = lane & ((1u << shift) - 1);
+      const uint32_t o = (uint32_t)min((int)r, left - 1) * pitch[part] + (second ? 256 : 0) +
+                         ((ch ^ (shift == 3 ? (r >> 1) & 7 : bitrev4(r & 15))) << 4);
+      dma16(lds + at, tile[part], o);
+    }
+  };
+  const uint32_t ring = wv * NS * St::kBytes;
+#pragma unroll
+  for (int i = 0; i < NS; ++i)
+    if (wv + 4 * i < nt) {
+      issue(wv + 4 * i, ring + i * St::kBytes, std::false_type{});
+      issue(wv + 4 * i, ring + i * St::kBytes, std::true_type{});
+    }
+
+  v8bf q[kSteps];
+  {
+    const uint16_t* p = a.q + (q0 + min(row, nq - 1)) * a.sqt + h * a.sqh + 8 * (lane >> 5);
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) q[k] = __builtin_bit_cast(v8bf, *(const int4*)(p + k * 16));
+  }
+  v16f o[kCols] = {};
+  float m = kNegInf;
+  RowSums l;
+  const Tile<DN, DV, 4> at_tile(lane);
+  uint32_t at = ring;
+  for (int t = wv; t < nt; t += 4) {
+    // A tile's keys and values are waited for apart, and each part of the
+    // stage is filled again once it is read.
+    const bool next = NS == 2 && t + 4 < nt, refill = t + 4 * NS < nt;
+    if (next) wait_loads<kValueLoads + St::kLoads>();
+    else wait_loads<kValueLoads>();
+    at_tile.attend(at, t * kTile, q, o, m, l, a.c, seen, (t + 1) * kTile > seen_first, [&] {
+      wait_lds();
+      if (refill) {
+        issue(t + 4 * NS, at, std::false_type{});
+        wait_loads<(NS - 1) * St::kLoads + kKeyLoads>();
+      } else if (next) {
+        wait_loads<St::kLoads>();
+      } else {
+        wait_loads<0>();
+      }
+    });
+    wait_lds();
+    if (refill) issue(t + 4 * NS, at, std::true_type{});
+    at = at + St::kBytes == ring + NS * St::kBytes ? ring : at + St::kBytes;
+  }
+
+  lds_barrier();  // the stages become the waves' outputs
+  float4* const sums = (float4*)((char*)lds_raw + kSums);
+  float4* const parts = (float4*)lds_raw;
+  sums[wv * 64 + lane] = {m, rows_sum<32>(l.exact), rows_sum<32>(l.used), 0};
+#pragma unroll
+  for (int i = 0; i < kCols; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      parts[((wv * kCols + i) * 4 + j) * 64 + lane] = {o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]};
+  lds_barrier();
+  float4 w[4];
+  float top = kNegInf, f[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = sums[i * 64 + lane];
+    top = fmaxf(top, w[i].x);
+  }
+  RowSums all;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[i] = w[i].x == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(w[i].x - top);
+    all.exact += f[i] * w[i].y;
+    all.used += f[i] * w[i].z;
+  }
+  if (row >= nq) return;
+  const float inv = all.inverse();  // (a row that sees no key: 0 and -inf)
+  uint16_t* out = a.out + (q0 + row) * a.sot + h * a.soh;
+#pragma unroll
+  for (int i = 0; i < kMine; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v4f sum = {};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 x = parts[((k * kCols + wv * kMine + i) * 4 + j) * 64 + lane];
+        sum += v4f{x.x, x.y, x.z, x.w} * f[k];
+      }
+      store_columns(out, lane, wv * kMine + i, j, sum, inv);
+    }
+  if (a.lse && wv == 0 && lane < 32) a.lse[(q0 + row) * a.H + h] = all.log_sum_exp(top);
+}
+
 }  // namespace
 
-hipError_t launch_mla_prefill(const MlaPrefillArgs& p, int dn, int dv, int cus, hipStream_t stream) {
-  (void)cus;
+hipError_t launch_mla_prefill(const MlaPrefillArgs& p, int dn, int dv, int rows, int cus, hipStream_t stream) {
   // at most one part-filled block per sequence
-  auto grid = [&](int rows) { return dim3((unsigned)((p.Tq / rows + (p.Tq < p.B ? p.Tq : p.B)) * p.H)); };
-  if (dn == 192) mla_prefill_kernel<192, 256, 8, 4><<<grid(256), 512, 0, stream>>>(p);
+  auto blocks = [&](int rows) { return (p.Tq / rows + (p.Tq < p.B ? p.Tq : p.B)) * p.H; };
+  auto grid = [&](int rows) { return dim3((unsigned)blocks(rows)); };
+  // The waves share 32 rows' keys where one workgroup per compute unit, or
+  // two with keys enough to share, take all rows (16 heads, us, shared keys
+  // against shared rows: 333 tokens 9.3, 14.5; 1000 22, 34; 32 after 4000
+  // others 42, 114; but 8 x 333 40, 23 and one of 20 5.7, 5.3).
+  const int64_t mean_rows = p.B ? (p.Tq + p.B - 1) / p.B : 0, mean_keys = p.B ? p.Tk / p.B : 0;
+  const int64_t few_blocks = p.B * ((mean_rows + 31) / 32) * p.H;
+  const bool few = rows ? rows == 32 : few_blocks <= cus * (mean_keys >= 256 ? 2 : mean_keys > kTile ? 1 : 0);
+  if (few && dn == 192) mla_prefill_few_kernel<192, 256, 1><<<grid(32), 256, 0, stream>>>(p);
+  else if (few) mla_prefill_few_kernel<128, 128, 2><<<grid(32), 256, 0, stream>>>(p);
+  else if (dn == 192) mla_prefill_kernel<192, 256, 8, 4><<<grid(256), 512, 0, stream>>>(p);
   else mla_prefill_kernel<128, 128, 4, 4><<<grid(128), 256, 0, stream>>>(p);
   return hipGetLastError();
 }

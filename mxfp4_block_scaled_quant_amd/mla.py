@@ -71,6 +71,12 @@ def set_mla_rows(rows: int) -> None:
     _check("mla_testing_set_rows", lib().mla_testing_set_rows(rows))
 
 
+def set_mla_prefill_rows(rows: int) -> None:
+    """Test hook (include/mxfp4_testing.h), for the calling thread only: query
+    rows per workgroup of the prefill kernels (32, 128; 0 = by size)."""
+    _check("mla_testing_set_prefill_rows", lib().mla_testing_set_prefill_rows(rows))
+
+
 def mla_cache_append(kv: torch.Tensor, norm_weight: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor,
                      positions: torch.Tensor, cos_sin: torch.Tensor, q_pe: Optional[torch.Tensor] = None,
                      q_out: Optional[torch.Tensor] = None, eps: float = 1e-6,

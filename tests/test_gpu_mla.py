@@ -256,8 +256,15 @@ PREFILL = [
 ]
 
 
+@pytest.fixture(params=[32, 128])
+def prefill_rows(request):
+    mx.set_mla_prefill_rows(request.param)
+    yield request.param
+    mx.set_mla_prefill_rows(0)
+
+
 @pytest.mark.parametrize("nq,nk,H,dn,dv,causal", PREFILL)
-def test_prefill(nq, nk, H, dn, dv, causal):
+def test_prefill(nq, nk, H, dn, dv, causal, prefill_rows):
     Tq, Tk = sum(nq), sum(nk)
     q, kn, kp, v = randn(1, Tq, H, dn + 64), randn(2, Tk, H, dn), randn(3, Tk, 64), randn(4, Tk, H, dv)
     out, lse = mx.mla_prefill(q, kn, kp, v, ints(cu(nq)), ints(cu(nk)), 0.09, causal=causal, return_lse=True)
@@ -285,13 +292,13 @@ def _prefill_on_gpu(q, kn, kp, v, scale, past):
 
 @pytest.mark.parametrize("n,past,H,dn,dv", [(1000, 0, 3, 128, 128), (777, 1500, 2, 192, 256), (2049, 0, 9, 192, 256),
                                             (513, 3000, 16, 128, 128)])
-def test_prefill_long(n, past, H, dn, dv):
+def test_prefill_long(n, past, H, dn, dv, prefill_rows):
     q, kn, kp, v = randn(1, n, H, dn + 64), randn(2, n + past, H, dn), randn(3, n + past, 64), randn(4, n + past, H, dv)
     out, lse = mx.mla_prefill(q, kn, kp, v, ints([0, n]), ints([0, n + past]), 0.08, return_lse=True)
     check(out, lse, _prefill_on_gpu(q, kn, kp, v, 0.08, past))
 
 
-def test_prefill_many_sequences():
+def test_prefill_many_sequences(prefill_rows):
     nq = [(7 * i) % 50 for i in range(150)]              # more sequences than one scan step of the block search
     T, H = sum(nq), 2
     q, kn, kp, v = randn(1, T, H, 192), randn(2, T, H, 128), randn(3, T, 64), randn(4, T, H, 128)
@@ -300,7 +307,7 @@ def test_prefill_many_sequences():
 
 
 @pytest.mark.parametrize("dn,dv", [(128, 128), (192, 256)])
-def test_prefill_strides_and_neighbours(dn, dv):
+def test_prefill_strides_and_neighbours(dn, dv, prefill_rows):
     # projections' layouts: keys and values interleaved in one tensor, heads
     # outside tokens; what lies behind a sequence's keys must not matter
     n, nk, H = 45, 83, 3
