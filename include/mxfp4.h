@@ -377,7 +377,9 @@ int mla_cache_append(const void* kv, int64_t ldkv, const void* norm_weight, floa
  * them, token s sees rows [0, n - S + 1 + s):
  *   z_i = scale * (q[b,s,h] . row_i),  out[b,s,h] = round(sum_i softmax(z)_i row_i[:512]),
  *   lse[b,s,h] = ln(sum_i exp(z_i)).
- * A token that sees no row gives 0 and -inf.  Scores, maxima, sums and
+ * A token that sees no row gives 0 and -inf.  Nothing past a request's length
+ * has any effect, but a later token's own row that is not finite can make the
+ * tokens before it NaN (0 times its value).  Scores, maxima, sums and
  * accumulators are fp32; the probabilities enter the value product rounded
  * to bf16.  The result does not depend on timing.
  *
@@ -426,6 +428,9 @@ int mla_decode_shared_prefix(const void* q, int64_t q_batch, int64_t q_token, in
  * [0, nk - nq + 1 + i) (the queries are the last tokens); else all nk.
  *   out[t, h] = round(softmax(scale * q . k) v),  lse[t, h] as above.
  * A query that sees no key gives 0 and -inf.  Arithmetic as in mla_decode.
+ * Values of keys that causal hides from a query are multiplied by an exact 0:
+ * a later row of the same sequence that is not finite can make it NaN (rows
+ * of other sequences never do).
  *
  *   q         bf16 [Tq, H, dn + 64], k_nope bf16 [Tk, H, dn], k_pe bf16
  *             [Tk, 64], v bf16 [Tk, H, dv], out bf16 [Tq, H, dv]: strides of

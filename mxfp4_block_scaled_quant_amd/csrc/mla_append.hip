@@ -2,7 +2,11 @@
 // the latent (fp32 sum of squares over 512 values), rotates the key part and
 // every head's query part by the token's position, and writes the row into
 // its page slot.  One pass, each byte once; bound by HBM for many tokens and
-// by one load's latency for few.
+// by one load's latency for few: 16001 tokens of 16 heads (107 MB) 24.6 us,
+// 4.35 TB/s, where a 1 GiB copy reaches 5.2 and 107 MB is too few bytes for
+// its start and end to vanish; non-temporal stores and loads of the next
+// token ahead measured the same.  64 tokens: 4 us, and the call's host side
+// takes longer.
 //
 // Lane l holds latent elements 8l..8l+7 (one 16-byte load: the row is 1 KiB
 // a wave).  A 64-element rotated part is four units of two 16-byte pieces

@@ -59,9 +59,8 @@ struct DecodeArgs {
   float* lse;                     // [B, S, H] or nullptr
   float* work;
 };
-// The split of a call: query rows per workgroup and 32-key tiles per work
-// unit of its requests and of its prefix, workgroups, and where the parts
-// lie in the workspace (float offsets).
+// The split of a call: query rows per workgroup of its requests and of its
+// prefix, workgroups, and where the parts lie in the workspace (float offsets).
 struct DecodePlan {
   int rows, prows;                // 16, 32 (four waves share the keys), 128 (four waves share the rows)
   int grid, pgrid, cus;

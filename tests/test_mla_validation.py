@@ -100,6 +100,13 @@ def test_rows_hook(lib):
     assert sizes[16] < sizes[32] < sizes[128] == sizes[0]     # long, many rows: blocks of 128
 
 
+def test_prefill_rows_hook(lib):
+    for bad in (-1, 16, 64, 256):
+        assert lib.mla_testing_set_prefill_rows(bad) == ARG
+    for rows in (32, 128, 0):
+        assert lib.mla_testing_set_prefill_rows(rows) == OK
+
+
 def test_prefill_entry(lib):
     def call(q=P, qt=16 * 192, qh=192, k=P, kt=2048, kh=128, pe=P, pt=64, v=P, vt=2048, vh=128, cq=P, ck=P, B=1,
              H=16, Tq=5, Tk=5, dn=128, dv=128, causal=1, scale=0.1, out=P, ot=2048, oh=128, lse=None):
