@@ -8,10 +8,10 @@
 // per byte at 16 query rows (bound by HBM), 242 at 128 (near the ridge of
 // the matrix units), and a prefix that all requests share is bound by the
 // matrix units.  Measured on MI355X: 128 requests of 16 heads over up to
-// 16000 rows (1.06 GB) 192 us, 5.5 TB/s; 6 of 40000 to 65000 76 us, 4.6 TB/s;
+// 16000 rows (1.06 GB) 191 us, 5.6 TB/s; 6 of 40000 to 65000 76 us, 4.6 TB/s;
 // one of 777 rows 14 us, the time of two launches and one pass of each; 12
-// requests of 4 tokens x 128 heads over 1500 to 8191 rows 111 us and 96
-// requests of 16 heads sharing 24571 rows 128 us, 0.65 PFLOP/s: at 32 query
+// requests of 4 tokens x 128 heads over 1500 to 8191 rows 105 us and 96
+// requests of 16 heads sharing 24571 rows 122 us, 0.69 PFLOP/s: at 32 query
 // rows a wave one wave is all that a SIMD's registers hold, a 32-key tile
 // takes it over 2 us (its products are half of that), and the 64 MB of parts
 // and their join are some 25 us of each.
@@ -818,46 +818,57 @@ __device__ __forceinline__ Parts find_parts(const ListArgs& a, int b, int r) {
   return {w1 - w0 + 1, 2 * w0 + 1, 2, 1};
 }
 
-// One workgroup of four waves per query row, or CS workgroups per row with
-// 512 / CS columns each, joins its parts.  Wave w takes parts w, w + 4, ..:
-// its lanes fetch 64 parts' maxima and sums at once, then the wave runs over
-// the parts' values, 8 / CS a lane; the four waves' sums meet in LDS in wave
-// order.  Rows that one workgroup of a call without a prefix wrote itself are
-// left alone; rows without any key become 0 and -inf.
-template <int RB, int PRB, int CS>
-__global__ __launch_bounds__(256) void mla_join_kernel(ListArgs a, ListArgs p) {
+// Where a query row's parts of one list lie: part i is row
+// first + i * step - (i > 0) * skip; whole items lie by query row.
+struct RowParts {
+  const float *part, *pml;
+  int count;
+  int64_t first;
+  int step, skip;
+};
+template <int RB>
+__device__ __forceinline__ RowParts row_parts(const ListArgs& a, int b, int r, int64_t flat) {
+  const Parts q = find_parts<RB>(a, b, r);
+  const bool whole = q.count == 1;
+  return {whole ? a.ipart : a.part, whole ? a.ipml : a.pml, q.count, whole ? flat : (int64_t)q.first * RB + r % RB,
+          q.step * RB, q.skip * RB};
+}
+
+// Joins the parts of query row r of sequence b, columns c0 .. c0 + 512 / CS: a
+// wave's lanes fetch 64 parts' maxima and sums at once, then it runs over the
+// parts' values, 8 / CS a lane.  ALONE: one wave takes all parts; otherwise
+// wave w of a workgroup takes parts w, w + 4, .., and the four waves' sums
+// meet in LDS in wave order.  Rows that one workgroup of a call without a
+// prefix wrote itself are left alone; rows without any key become 0 and -inf.
+template <int RB, int PRB, int CS, bool ALONE>
+__device__ __forceinline__ void join_row(const ListArgs& a, const ListArgs& p, int b, int r, int c0, float (*so)[512 / CS],
+                                         float (*sml)[3]) {
   constexpr int W = 8 / CS;                      // columns per lane
   typedef float vec __attribute__((ext_vector_type(CS == 1 ? 4 : W)));
   constexpr int V = CS == 1 ? 4 : W, NV = W / V;  // read as NV vectors, 64 lanes apart
-  __shared__ float so[4][512 / CS];
-  __shared__ float sml[4][3];
+  constexpr int kStride = ALONE ? 1 : 4;         // waves that share the parts
+  constexpr int kAhead = ALONE ? 8 : 4;          // parts under way
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int b = blockIdx.x / a.rows, r = blockIdx.x - b * a.rows;
-  const int c0 = blockIdx.y * (512 / CS);
   const RowId id = row_id(a, b, r);
   const int64_t flat = flat_row(a.d, id);
-  const Parts own = find_parts<RB>(a, b, r);
+  const RowParts own = row_parts<RB>(a, b, r, flat);
   if (!PRB && own.count == 1) return;
-  Parts pre = {0, 0, 0, 0};
-  if constexpr (PRB != 0) pre = find_parts<PRB>(p, 0, (int)flat);
-  // Part i's row: (list, slot row); whole items lie by query row.
-  auto part_at = [&](int i, const float*& po, const float*& pm) {
+  RowParts pre = {};
+  if constexpr (PRB != 0) pre = row_parts<PRB>(p, 0, (int)flat, flat);
+  auto part_at = [&](int i, const float*& po, const float*& pm) {  // the prefix's parts, then the request's own
     const bool in_prefix = PRB != 0 && i < pre.count;
-    const ListArgs& g = in_prefix ? p : a;
-    const Parts& q = in_prefix ? pre : own;
+    const RowParts& q = in_prefix ? pre : own;
     i -= in_prefix ? 0 : pre.count;
-    const bool whole = q.count == 1;
-    const int64_t slot = q.first + (int64_t)i * q.step - (i > 0 ? q.skip : 0);
-    const int64_t k = whole ? flat : in_prefix ? slot * PRB + (int)(flat % (PRB ? PRB : 1)) : slot * RB + r % RB;
-    po = (whole ? g.ipart : g.part) + k * kLatent + c0;
-    pm = (whole ? g.ipml : g.pml) + 4 * k;
+    const int64_t k = q.first + (int64_t)i * q.step - (i > 0 ? q.skip : 0);
+    po = q.part + k * kLatent + c0;
+    pm = q.pml + 4 * k;
   };
   const int count = pre.count + own.count;
   float m = kNegInf;
   RowSums l;
   vec o[NV] = {};
-  for (int i0 = wv; i0 < count; i0 += 256) {  // 64 parts of this wave
-    const int mine = i0 + 4 * lane, n = min(64, (count - i0 + 3) / 4);
+  for (int i0 = ALONE ? 0 : wv; i0 < count; i0 += 64 * kStride) {  // 64 parts of this wave
+    const int mine = i0 + kStride * lane, n = min(64, (count - i0 + kStride - 1) / kStride);
     const float *po, *pm;
     v4f pl = {kNegInf, 0, 0, 0};
     if (lane < n) {
@@ -873,10 +884,10 @@ __global__ __launch_bounds__(256) void mla_join_kernel(ListArgs a, ListArgs p) {
     m = mn;
 #pragma unroll
     for (int v = 0; v < NV; ++v) o[v] *= keep;
-#pragma unroll 4
+#pragma unroll kAhead
     for (int i = 0; i < n; ++i) {
       const float fi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
-      part_at(i0 + 4 * i, po, pm);
+      part_at(i0 + kStride * i, po, pm);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const vec x = *(const vec*)(po + v * 64 * V + V * lane);
@@ -884,6 +895,17 @@ __global__ __launch_bounds__(256) void mla_join_kernel(ListArgs a, ListArgs p) {
         for (int e = 0; e < V; ++e) o[v][e] += fi == 0 ? 0.0f : x[e] * fi;
       }
     }
+  }
+  uint16_t* out = a.d.out + id.b * a.d.sob + id.s * a.d.sos + id.h * a.d.soh + c0;
+  if constexpr (ALONE) {
+    const float inv = l.inverse();
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const uint2 w = {pack_bf16x2(o[v][0] * inv, o[v][1] * inv), pack_bf16x2(o[v][2] * inv, o[v][3] * inv)};
+      *(uint2*)(out + v * 64 * V + V * lane) = w;
+    }
+    if (a.d.lse && lane == 0) a.d.lse[flat] = l.log_sum_exp(m);
+    return;
   }
 #pragma unroll
   for (int v = 0; v < NV; ++v) *(vec*)&so[wv][v * 64 * V + V * lane] = o[v];
@@ -906,9 +928,27 @@ __global__ __launch_bounds__(256) void mla_join_kernel(ListArgs a, ListArgs p) {
   }
   const float inv = l.inverse();
   const uint2 w = {pack_bf16x2(t[0] * inv, t[1] * inv), pack_bf16x2(t[2] * inv, t[3] * inv)};
-  *(uint2*)(a.d.out + id.b * a.d.sob + id.s * a.d.sos + id.h * a.d.soh + c0 + 4 * threadIdx.x) = w;
-  if (a.d.lse && threadIdx.x == 0 && blockIdx.y == 0)
-    a.d.lse[flat] = l.log_sum_exp(m);
+  *(uint2*)(out + 4 * threadIdx.x) = w;
+  if (a.d.lse && threadIdx.x == 0 && c0 == 0) a.d.lse[flat] = l.log_sum_exp(m);
+}
+
+// One workgroup of four waves per query row, or CS workgroups per row with
+// 512 / CS columns each.
+template <int RB, int PRB, int CS>
+__global__ __launch_bounds__(256) void mla_join_kernel(ListArgs a, ListArgs p) {
+  __shared__ float so[4][512 / CS];
+  __shared__ float sml[4][3];
+  const int b = blockIdx.x / a.rows, r = blockIdx.x - b * a.rows;
+  join_row<RB, PRB, CS, false>(a, p, b, r, blockIdx.y * (512 / CS), so, sml);
+}
+
+// One wave per query row, where the rows are many.
+template <int RB, int PRB>
+__global__ __launch_bounds__(256) void mla_join_waves_kernel(ListArgs a, ListArgs p) {
+  const int at = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (at >= a.B * a.rows) return;
+  const int b = at / a.rows, r = at - b * a.rows;
+  join_row<RB, PRB, 1, true>(a, p, b, r, 0, nullptr, nullptr);
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -956,12 +996,25 @@ void launch_join_columns(int rb, const ListArgs& a, const ListArgs& p, hipStream
     default: mla_join_kernel<128, PRB, CS><<<grid, 256, 0, s>>>(a, p); break;
   }
 }
+template <int PRB>
+void launch_join_waves(int rb, const ListArgs& a, const ListArgs& p, hipStream_t s) {
+  const int grid = (a.B * a.rows + 3) / 4;
+  switch (rb) {
+    case 16: mla_join_waves_kernel<16, PRB><<<grid, 256, 0, s>>>(a, p); break;
+    case 32: mla_join_waves_kernel<32, PRB><<<grid, 256, 0, s>>>(a, p); break;
+    default: mla_join_waves_kernel<128, PRB><<<grid, 256, 0, s>>>(a, p); break;
+  }
+}
 // A row's parts by one workgroup, or by four where the rows are too few to
-// keep the compute units' loads in flight (16 rows of 250 parts: 17.3 -> 9.7 us).
+// keep the compute units' loads in flight (16 rows of 250 parts: 17.3 -> 9.7
+// us), or by one wave where workgroups of a row each would not all fit the
+// chip (16 heads, a workgroup against a wave a row: 64 requests 5.4, 7.0 us;
+// 160 9.0, 6.4; 512 24, 12).
 template <int PRB>
 void launch_join(int rb, const ListArgs& a, const ListArgs& p, int cus, hipStream_t s) {
   if (a.B * a.rows < 2 * cus) launch_join_columns<PRB, 4>(rb, a, p, s);
-  else launch_join_columns<PRB, 1>(rb, a, p, s);
+  else if (a.B * a.rows < 8 * cus) launch_join_columns<PRB, 1>(rb, a, p, s);
+  else launch_join_waves<PRB>(rb, a, p, s);
 }
 
 }  // namespace

@@ -237,6 +237,28 @@ def test_decode_shared_prefix_long():
         check(out[b, 0], lse[b, 0], _exact_on_gpu(q[b, 0], rows, 0.05))
 
 
+@pytest.mark.parametrize("prefix", [0, 2900])
+def test_many_rows_whose_parts_single_waves_join(prefix):
+    lens = [(53 * i) % 300 for i in range(149)]           # 149 requests of 17 heads: an odd number of rows
+    lens[7], lens[40] = 30011, 0                          # one request spread over many workgroups, one empty
+    cache, table = paged(55, lens + [prefix], 64)
+    ptab, t = ints(table[-1, :max(-(-prefix // 64), 1)]), ints(table[:-1])
+    q = randn(56, 149, 1, 17, 576)
+    args = (ptab, prefix) if prefix else ()
+    f = mx.mla_decode_shared_prefix if prefix else mx.mla_decode
+    out, lse = f(q, cache, *args, t, ints(lens), 0.05, return_lse=True)
+    assert torch.equal(out, f(q, cache, *args, t, ints(lens), 0.05))
+    shared = cache[ptab.long()].reshape(-1, 576)[:prefix]
+    for b in (0, 1, 7, 39, 41, 100, 147, 148):
+        rows = torch.cat([shared, cache[t[b].long()].reshape(-1, 576)[:lens[b]]])
+        if len(rows):
+            check(out[b, 0], lse[b, 0], _exact_on_gpu(q[b, 0], rows, 0.05))
+    if not prefix:
+        assert not out[[0, 40]].any() and (lse[[0, 40]] == float("-inf")).all()
+    else:
+        check(out[40, 0], lse[40, 0], _exact_on_gpu(q[40, 0], shared, 0.05))
+
+
 def cu(lens):
     return np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
 
