@@ -35,6 +35,8 @@ Modules:
   (index maps plus padding), and the pages' prior-art scale tile order.
 * :mod:`oracle.linalg` -- the W4A4 GEMM and the A16WFP4 BMM in fp64, and the
   per-element tolerance term sum |a_i * b_i|.
+* :mod:`oracle.attention` -- latent attention in fp64 (cache write, absorbed
+  attention with and without a shared prefix, prompts).
 
 Parity status per function is stated in each module header.  One quantity is
 "parity unpinned": the internal precision of the hardware's scaled FP4 dot
@@ -42,4 +44,4 @@ product, which is not a function of this oracle and is only measured against
 the tolerance.
 """
 
-from . import formats, quant, layout, linalg  # noqa: F401
+from . import attention, formats, quant, layout, linalg  # noqa: F401
