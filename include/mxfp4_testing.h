@@ -44,7 +44,7 @@ int mla_testing_set_rows(int rows);
 
 /*
  * Forces mla_prefill's query rows per workgroup on this thread: 32 (its waves
- * share the keys between them) or 128 (and more: its waves share the rows);
+ * share the keys between them) or 128 (its waves share the rows);
  * 0 = choose by the rows (the default).
  * Returns MXFP4_OK, or MXFP4_ERR_ARG for other values.
  */

@@ -89,7 +89,7 @@ struct MlaPrefillArgs {
   int64_t sot, soh;
   float* lse;                     // [Tq, H] or nullptr
 };
-// rows: per workgroup, 32 or 128 (and more); 0 = by the rows.
+// rows: per workgroup, 32 or 128; 0 = by the rows.
 hipError_t launch_mla_prefill(const MlaPrefillArgs& p, int dn, int dv, int rows, int cus, hipStream_t stream);
 
 }  // namespace mxfp4

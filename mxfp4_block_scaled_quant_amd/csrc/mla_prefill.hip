@@ -4,20 +4,22 @@
 // heads share (never copied per head).
 //
 // One pass over the keys with a running maximum and sum (fp32).  A workgroup
-// takes a block of query rows of one head of one sequence, 32 rows a wave,
-// and walks the keys in 32-key tiles that all its waves share in a ring of
-// four LDS stages; loads run three tiles ahead of the barrier that hands a
-// tile over.  Later rows see more keys and start first.
+// takes 128 query rows of one head of one sequence, 32 rows a wave, and walks
+// the keys in 32-key tiles that its waves share in a ring of LDS stages; loads
+// run ahead of the barrier that hands a tile over.  A stage is 32 KiB at
+// values of 256 (two stages) and 20 KiB at 128 (four), so that a compute unit
+// holds two workgroups, and one's start and barriers pass under the other's
+// products.  Eight waves with four stages at 256 measured 1 to 3% slower, and
+// softmax steps spread between the products, or a wave priority for them, the
+// same.
 //
 // Bound by the matrix units, and they by the card's power: 2 (dn + 64 + dv)
 // operations per (query, key) pair, 16384 causal tokens of 16 heads at
-// 192 + 64 and 256: 1.94-2.03 ms, 1.08-1.13 PFLOP/s; 2 x 1900-2048 tokens after 14003
-// others at 128 + 64 and 128: 0.65-0.69 ms, 0.9.  The clock falls to 1.65 GHz
-// under it; the same launch on zeros reaches 1.35 PFLOP/s, and a library
-// product of random 8192 x 8192 matrices 1.44.  One stage costs 32 KiB at
-// values of 256 and 20 KiB at 128, so a compute unit holds one workgroup of
-// eight waves or two of four; four waves with two stages at 256 measured the
-// same, as did softmax steps spread between the products.
+// 192 + 64 and 256: 1.93-1.98 ms, 1.11-1.14 PFLOP/s; 2 x 1900-2048 tokens
+// after 14003 others at 128 + 64 and 128: 0.63 ms, 0.96; 9 prompts of 17 to
+// 4001 tokens at 192 + 64 and 256: 0.39 ms, 0.87.  The clock falls to 1.65
+// GHz under it; the same launch on zeros reaches 1.35 PFLOP/s, and a library
+// product of random 8192 x 8192 matrices 1.44.
 //
 // Few query rows leave most compute units idle that way, each workgroup
 // walking all of its keys alone: there the four waves of a workgroup take 32
@@ -28,7 +30,7 @@
 namespace mxfp4 {
 namespace {
 
-constexpr int kTile = 32;
+constexpr int kTile = 32, kWaves = 4;
 
 // LDS of one stage: the keys' first 128 values (256-byte rows), the next 64
 // (DN = 192; 128-byte rows), the rotated 64, then the values (DV * 2-byte rows).
@@ -41,44 +43,65 @@ struct Stage {
   static constexpr int kLoads = kBytes / 1024;                      // wave loads of a tile
 };
 
-template <int DN, int DV, int NW, int NS>
+template <int DN, int DV, int NS>
 struct Cfg {
   using St = Stage<DN, DV>;
-  static constexpr int kPer = St::kLoads / NW;
-  static_assert(St::kLoads % NW == 0, "equal loads per wave");
+  static constexpr int kPer = St::kLoads / kWaves;
+  static_assert(NS == 2 || NS == 4, "the kernel's waits");
+  static_assert(St::kLoads % kWaves == 0, "equal loads per wave");
   static constexpr uint32_t kLds = NS * St::kBytes;
-  static_assert(kLds <= 160 * 1024, "LDS per workgroup");
+  static_assert(kLds <= 80 * 1024, "two workgroups a compute unit");
 };
 
-// The sequence that holds query block `blk` of R rows and the block's number
-// in it (from the last: later rows see more keys, so they start first);
-// false past the end.
+// Query block `blk` of R rows, counted by the keys it sees from the most down
+// (whatever sequence it is of: where all blocks run at once, long and short
+// ones then share the compute units; the chunks above 0.67 -> 0.63 ms), 64
+// sequences at a time: its sequence and its number there; false past the end.
+// A block's level is its keys' end in units of R: per sequence the blocks of a
+// level and above are counted without a list, so the level that holds `blk` is
+// found by bisection, one sequence a lane.
 template <int R>
 __device__ __forceinline__ bool find_block(const MlaPrefillArgs& a, int blk, int& b, int& i) {
   const int lane = threadIdx.x & 63;
-  int before = 0;
   for (int s = 0; s < a.B; s += 64) {
     const int k = s + lane;
-    int n = 0;
+    int n = 0, first = 0;  // blocks, and the level of the first (causal) or of all
     if (k < a.B) {
-      const int64_t nq = (int64_t)a.cu_q[k + 1] - a.cu_q[k];
+      const int64_t nq = (int64_t)a.cu_q[k + 1] - a.cu_q[k], nk = (int64_t)a.cu_k[k + 1] - a.cu_k[k];
       n = nq > 0 ? (int)((nq + R - 1) / R) : 0;
+      first = (int)((a.causal ? nk - nq : nk) >> __builtin_ctz(R));
     }
-    int x = n;
+    const int total = wave_sum(n);
+    if (blk >= total) {
+      blk -= total;
+      continue;
+    }
+    if (a.B == 1) {
+      b = 0;
+      i = total - 1 - blk;
+      return true;
+    }
+    auto from = [&](int level) {  // the lane's blocks at `level` or above
+      return a.causal ? max(0, min(n, n + first - level)) : level <= first ? n : 0;
+    };
+    int lo = wave_reduce(n ? first : 0x7FFFFFFF, [](int x, int y) { return min(x, y); });
+    int hi = wave_reduce(n ? first + (a.causal ? n : 1) : -0x7FFFFFFF, [](int x, int y) { return max(x, y); });
+    while (hi - lo > 1) {  // blocks from lo: more than blk; from hi: no more
+      const int mid = lo + (hi - lo) / 2;
+      if (wave_sum(from(mid)) > blk) lo = mid;
+      else hi = mid;
+    }
+    const int above = from(hi), here = from(lo) - above, rank = blk - wave_sum(above);
+    int x = here;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int y = __shfl_up(x, d);
       if (lane >= d) x += y;
     }
-    const uint64_t hit = __builtin_amdgcn_ballot_w64(before + x > blk);
-    if (hit) {
-      const int f = __builtin_ctzll(hit);
-      b = s + f;
-      const int end = before + __builtin_amdgcn_readlane(x, f);
-      i = end - 1 - blk;
-      return true;
-    }
-    before += __builtin_amdgcn_readlane(x, 63);
+    const int f = __builtin_ctzll(__builtin_amdgcn_ballot_w64(x > rank));
+    b = s + f;
+    i = __builtin_amdgcn_readlane(n - 1 - above, f) - (rank - __builtin_amdgcn_readlane(x - here, f));
+    return true;
   }
   return false;
 }
@@ -165,11 +188,11 @@ struct Tile {
   }
 };
 
-template <int DN, int DV, int NW, int NS>
-__global__ __launch_bounds__(64 * NW, 2) void mla_prefill_kernel(MlaPrefillArgs a) {
+template <int DN, int DV, int NS>
+__global__ __launch_bounds__(64 * kWaves, 2) void mla_prefill_kernel(MlaPrefillArgs a) {
   using St = Stage<DN, DV>;
-  using C = Cfg<DN, DV, NW, NS>;
-  constexpr int R = 32 * NW, kSteps = (DN + kRope) / 16, kCols = DV / 32;
+  using C = Cfg<DN, DV, NS>;
+  constexpr int R = 32 * kWaves, kSteps = (DN + kRope) / 16, kCols = DV / 32;
   __shared__ int4 lds_raw[C::kLds / 16];
   uint32_t anchor = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int4*)lds_raw;
   asm volatile("" : "+s"(anchor)::"memory");  // LDS is addressed by number: its array starts at 0
@@ -247,8 +270,8 @@ __global__ __launch_bounds__(64 * NW, 2) void mla_prefill_kernel(MlaPrefillArgs 
   const Tile<DN, DV, DV == 256 ? 2 : 4> at_tile(lane);  // (groups: what the registers leave)
   uint32_t tile = 0, fill = (NS - 1) * St::kBytes;  // this tile's stage, and the next to load
   for (int t = 0; t < nt; ++t) {
-    if (t + 2 < nt) wait_loads<2 * C::kPer>();
-    else if (t + 1 < nt) wait_loads<C::kPer>();
+    if (NS == 4 && t + 2 < nt) wait_loads<2 * C::kPer>();  // tile t is there, the next may be under way
+    else if (NS == 4 && t + 1 < nt) wait_loads<C::kPer>();
     else wait_loads<0>();
     wait_lds();
     wave_barrier();
@@ -421,14 +444,14 @@ hipError_t launch_mla_prefill(const MlaPrefillArgs& p, int dn, int dv, int rows,
   // The waves share 32 rows' keys where one workgroup per compute unit, or
   // two with keys enough to share, take all rows (16 heads, us, shared keys
   // against shared rows: 333 tokens 9.3, 14.5; 1000 22, 34; 32 after 4000
-  // others 42, 114; but 8 x 333 40, 23 and one of 20 5.7, 5.3).
+  // others 42, 114; but 8 x 333 40, 22 and one of 20 5.7, 5.3).
   const int64_t mean_rows = p.B ? (p.Tq + p.B - 1) / p.B : 0, mean_keys = p.B ? p.Tk / p.B : 0;
   const int64_t few_blocks = p.B * ((mean_rows + 31) / 32) * p.H;
   const bool few = rows ? rows == 32 : few_blocks <= cus * (mean_keys >= 256 ? 2 : mean_keys > kTile ? 1 : 0);
   if (few && dn == 192) mla_prefill_few_kernel<192, 256, 1><<<grid(32), 256, 0, stream>>>(p);
   else if (few) mla_prefill_few_kernel<128, 128, 2><<<grid(32), 256, 0, stream>>>(p);
-  else if (dn == 192) mla_prefill_kernel<192, 256, 8, 4><<<grid(256), 512, 0, stream>>>(p);
-  else mla_prefill_kernel<128, 128, 4, 4><<<grid(128), 256, 0, stream>>>(p);
+  else if (dn == 192) mla_prefill_kernel<192, 256, 2><<<grid(128), 256, 0, stream>>>(p);
+  else mla_prefill_kernel<128, 128, 4><<<grid(128), 256, 0, stream>>>(p);
   return hipGetLastError();
 }
 
