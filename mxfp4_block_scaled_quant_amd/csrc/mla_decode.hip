@@ -8,17 +8,17 @@
 // per byte at 16 query rows (bound by HBM), 242 at 128 (near the ridge of
 // the matrix units), and a prefix that all requests share is bound by the
 // matrix units.  Measured on MI355X: 128 requests of 16 heads over up to
-// 16000 rows (1.06 GB) 191 us, 5.6 TB/s; 6 of 40000 to 65000 76 us, 4.6 TB/s;
+// 16000 rows (1.06 GB) 188 us, 5.6 TB/s; 6 of 40000 to 65000 76 us, 4.6 TB/s;
 // one of 777 rows 14 us, the time of two launches and one pass of each; 12
-// requests of 4 tokens x 128 heads over 1500 to 8191 rows 105 us and 96
-// requests of 16 heads sharing 24571 rows 122 us, 0.69 PFLOP/s: at 32 query
+// requests of 4 tokens x 128 heads over 1500 to 8191 rows 100 us and 96
+// requests of 16 heads sharing 24571 rows 121 us, 0.7 PFLOP/s: at 32 query
 // rows a wave one wave is all that a SIMD's registers hold, a 32-key tile
 // takes it over 2 us (its products are half of that), and the 64 MB of parts
 // and their join are some 25 us of each.
 //
 // Work is cut along the keys.  The list of all requests' key units (128 keys
-// for 16 and 32 query rows, 64 above) is dealt to the workgroups in equal
-// contiguous shares, computed by each workgroup from the lengths on the
+// for 16 and 32 query rows, 64 above, and an item's setup) is dealt to the
+// workgroups in equal contiguous shares, computed by each workgroup from the lengths on the
 // device, so ragged batches stay balanced and a captured graph follows new
 // lengths.  A workgroup that holds a whole (request, row block) writes its
 // output; otherwise the fp32 accumulators, maxima and sums go to the
@@ -122,6 +122,25 @@ __device__ __forceinline__ Single single_split(const ListArgs& a, int units) {
   return {size ? (units + size - 1) / size : 0, size};
 }
 
+template <int RB>
+__host__ __device__ constexpr int unit_tiles() { return RB <= 32 ? 4 : 2; }
+
+// What an item costs a workgroup before and after its keys, in units: the
+// shares count it, so that a workgroup that ends one item and starts another
+// has fewer keys (us with 0, 2, 4, 6 units for 128 rows: 12 requests of 4
+// tokens x 128 heads 110, 104.5, 102, 102.5; with 0, 1, 2 for 16 rows: 128
+// requests 192.5, 188.5, 188; one or two units a workgroup are cut less
+// evenly for it: 8 equal requests of 128 heads and 1000 keys 21.7 -> 24.7,
+// 100 of 16 heads and 100 to 700 keys 31.7 -> 27.9).
+template <int RB>
+__host__ __device__ constexpr int setup_units() { return RB <= 32 ? 1 : 4; }
+// Units of an item of n keys in the list that the shares cut (0: no keys).
+template <int RB>
+__device__ __forceinline__ int item_units(int n) {
+  const int units = units_of<unit_tiles<RB>() * kTile>(n);
+  return units ? units + setup_units<RB>() : 0;
+}
+
 // Share w of `total` units over at most `most` workgroups, each with at least
 // one unit: [lo, hi), empty for workgroups without.
 __device__ __forceinline__ void share_of(int& w, int total, int most, int& lo, int& hi) {
@@ -136,11 +155,11 @@ __device__ __forceinline__ void share_of(int& w, int total, int most, int& lo, i
 
 // This workgroup's share w of the list, units [lo, hi), the sequence that
 // holds unit lo, and the units before that sequence.
-template <int UNIT>
+template <int RB>
 __device__ __forceinline__ void find_share(const ListArgs& a, int& w, int& b, int& base, int& lo, int& hi) {
   if (a.B <= 64) {  // each wave by itself, one sequence a lane
     const int lane = threadIdx.x & 63;
-    const int u = lane < a.B ? a.nt * units_of<UNIT>(list_len(a, lane)) : 0;
+    const int u = lane < a.B ? a.nt * item_units<RB>(list_len(a, lane)) : 0;
     int upto = u;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -155,7 +174,7 @@ __device__ __forceinline__ void find_share(const ListArgs& a, int& w, int& b, in
   }
   const int chunk = (a.B + 255) / 256, b0 = threadIdx.x * chunk, b1 = min(a.B, b0 + chunk);
   int sum = 0;
-  for (int i = b0; i < b1; ++i) sum += a.nt * units_of<UNIT>(list_len(a, i));
+  for (int i = b0; i < b1; ++i) sum += a.nt * item_units<RB>(list_len(a, i));
   int total;
   int at = scan256(sum, total);
   share_of(w, total, a.grid, lo, hi);
@@ -163,7 +182,7 @@ __device__ __forceinline__ void find_share(const ListArgs& a, int& w, int& b, in
   if (at <= lo && lo < at + sum) {
     int i = b0;
     for (;; ++i) {
-      const int u = a.nt * units_of<UNIT>(list_len(a, i));
+      const int u = a.nt * item_units<RB>(list_len(a, i));
       if (lo < at + u) break;
       at += u;
     }
@@ -726,16 +745,14 @@ __device__ __forceinline__ void attend_shared(const ListArgs& a, int b, int n, i
   lds_barrier();
 }
 
-template <int RB>
-__device__ constexpr int unit_tiles() { return RB <= 32 ? 4 : 2; }
-
 // Workgroup w's share of one list.
 template <int RB>
 __device__ __forceinline__ void attend_list(const ListArgs& a, int w) {
   constexpr int kUnitTiles = unit_tiles<RB>(), kUnit = kUnitTiles * kTile;
+  constexpr int kSetup = setup_units<RB>();
   int b = 0, base = 0, lo, hi;
   const bool single = is_single(a);
-  if (!single) find_share<kUnit>(a, w, b, base, lo, hi);
+  if (!single) find_share<RB>(a, w, b, base, lo, hi);
   else lo = 0, hi = 1;
   for (int cur = lo; cur < hi;) {
     const int n = __builtin_amdgcn_readfirstlane(list_len(a, b));
@@ -753,16 +770,19 @@ __device__ __forceinline__ void attend_list(const ListArgs& a, int w) {
       to = {cut.chunks == 1, w};
       cur = hi;
     } else {
-      if (cur - base >= units * a.nt) {  // past this sequence (or it is empty)
-        base += units * a.nt;
+      const int item = item_units<RB>(n);
+      if (cur - base >= item * a.nt) {  // past this sequence (or it is empty)
+        base += item * a.nt;
         ++b;
         continue;
       }
-      rt = (cur - base) / units;
-      u0 = (cur - base) - rt * units;
-      u1 = min(units, u0 + hi - cur);
+      rt = (cur - base) / item;
+      const int at = (cur - base) - rt * item, end = min(item, at + hi - cur);
+      cur += end - at;
+      u0 = max(0, at - kSetup);
+      u1 = max(0, end - kSetup);
+      if (u0 == u1) continue;  // (nothing but the item's setup)
       to = {u0 == 0 && u1 == units, 2 * w + (u0 == 0)};
-      cur += u1 - u0;
     }
     const int tiles = (int)(((uint32_t)n + kTile - 1) / kTile);
     if constexpr (RB <= 32)
@@ -802,18 +822,18 @@ __device__ __forceinline__ Parts find_parts(const ListArgs& a, int b, int r) {
   if (is_single(a)) return {single_split(a, units_of<kUnit>(list_len(a, 0))).chunks, r / RB, a.nt, 0};
   int before = 0, total = 0;  // units of the sequences before b, and of all (each wave by itself)
   for (int i = threadIdx.x & 63; i < a.B; i += 64) {
-    const int u = a.nt * units_of<kUnit>(list_len(a, i));
+    const int u = a.nt * item_units<RB>(list_len(a, i));
     if (i < b) before += u;
     total += u;
   }
   before = wave_sum(before);
   total = wave_sum(total);
-  const int units = units_of<kUnit>(list_len(a, b));
-  if (units == 0) return {0, 0, 0, 0};
-  const int u0 = before + r / RB * units;
+  const int item = item_units<RB>(list_len(a, b));
+  if (item == 0) return {0, 0, 0, 0};
+  const int u0 = before + r / RB * item;
   const int grid = min(a.grid, total);
-  const int w0 = (int)((((int64_t)u0 + 1) * grid - 1) / total);
-  const int w1 = (int)((((int64_t)u0 + units) * grid - 1) / total);
+  const int w0 = (int)((((int64_t)u0 + setup_units<RB>() + 1) * grid - 1) / total);
+  const int w1 = (int)((((int64_t)u0 + item) * grid - 1) / total);
   // the first workgroup's second slot (the item begins there), then the others' first
   return {w1 - w0 + 1, 2 * w0 + 1, 2, 1};
 }
@@ -952,7 +972,8 @@ __global__ __launch_bounds__(256) void mla_join_waves_kernel(ListArgs a, ListArg
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int unit_keys(int rb) { return rb <= 32 ? 4 * kTile : 2 * kTile; }
+int unit_keys(int rb) { return rb <= 32 ? unit_tiles<16>() * kTile : unit_tiles<128>() * kTile; }
+int setup_keys(int rb) { return rb <= 32 ? setup_units<16>() * unit_keys(rb) : setup_units<128>() * unit_keys(rb); }
 
 // Query rows per workgroup for B sequences of `rows` query rows and up to n
 // keys.  Blocks of 16 read a sequence's rows once per 16 query rows, but from
@@ -1025,7 +1046,8 @@ DecodePlan decode_plan(int64_t B, int64_t S, int64_t H, int64_t max_tokens, int6
   d.cus = cus;
   const int64_t rows = S * H;
   d.rows = rows_per_block(B, rows, max_tokens);
-  int64_t units = B * cdiv(rows, d.rows) * cdiv(max_tokens, unit_keys(d.rows));
+  // (one sequence's shares are cut without the setup: Single)
+  int64_t units = B * cdiv(rows, d.rows) * cdiv(max_tokens + (B > 1 ? setup_keys(d.rows) : 0), unit_keys(d.rows));
   d.grid = (int)(units < cus ? (units < 1 ? 1 : units) : cus);
   size_t at = 0;
   auto take = [&](int64_t n) {
