@@ -386,8 +386,9 @@ int mla_cache_append(const void* kv, int64_t ldkv, const void* norm_weight, floa
  *   q         bf16, element (b, s, h, i < 576) at b*q_batch + s*q_token +
  *             h*q_head + i (ELEMENTS, % 8, 16-byte aligned): the absorbed
  *             query (a16wfp4_bmm's K-up) and its rotated part
- *   block_table  int32 [B, max_pages], row stride ldt: request b's pages in
- *             order.  A page number outside [0, pages) hides its rows.
+ *   block_table  int32 [B, max_pages], row stride ldt >= max_pages, or 0 (one
+ *             row for all requests): request b's pages in order.  A page
+ *             number outside [0, pages) hides its rows.
  *   lengths   int32 [B], clamped to [0, max_pages * page_size]
  *   scale     finite, > 0
  *   out       bf16 (b, s, h, i < 512), strides as for q; rows must not overlap

@@ -96,7 +96,7 @@ int decode_call(const void* q, int64_t q_batch, int64_t q_token, int64_t q_head,
   if (page_size < 1 || max_pages < 0 || max_pages > kMaxTokens || page_size > kMaxTokens) return MXFP4_ERR_SHAPE;
   if (max_pages * page_size > kMaxTokens || !decode_shape(B, S, H, max_pages * page_size, prefix_len))
     return MXFP4_ERR_SHAPE;
-  if (ldt < max_pages || ldt > kMaxStride) return MXFP4_ERR_SHAPE;
+  if ((ldt < max_pages && ldt != 0) || ldt > kMaxStride) return MXFP4_ERR_SHAPE;
   if (prefix_pages < 0 || prefix_pages > kMaxTokens || prefix_pages * page_size < prefix_len) return MXFP4_ERR_SHAPE;
   if (!stride_ok(q_batch) || !stride_ok(q_token) || !stride_ok(q_head) || !stride_ok(out_batch) ||
       !stride_ok(out_token) || !stride_ok(out_head))

@@ -157,6 +157,11 @@ def _decode(fn, q, cache, prefix, block_table, lengths, scale, return_lse, out, 
         _require(block_table, "block_table", _I32, (B, -1), dev)
         _require(lengths, "lengths", _I32, (B,), dev)
         _require_contiguous(lengths, "lengths")
+    # (One request's row stride means nothing.)
+    ldt = table_strides[0] if B > 1 else width
+    if 0 < ldt < width:
+        raise ValueError("block_table's rows may be one row for all requests (stride 0), but must not overlap in "
+                         f"part: row stride {ldt}, width {width}")
     shared, prefix_len = (), 0
     if prefix is not None:
         prefix_table, prefix_len = prefix
@@ -187,7 +192,7 @@ def _decode(fn, q, cache, prefix, block_table, lengths, scale, return_lse, out, 
             raise ValueError(f"workspace holds {workspace.shape[0]} bytes, {need} needed")
     status = getattr(handle, fn)(
         q.data_ptr(), q_strides[0], q_strides[1], q_strides[2], cache.data_ptr(), pages, page_size, cache_strides[0],
-        cache_strides[1], *shared, block_table.data_ptr(), max(table_strides[0], width), width, lengths.data_ptr(),
+        cache_strides[1], *shared, block_table.data_ptr(), ldt, width, lengths.data_ptr(),
         B, S, H, scale, out.data_ptr(), out_strides[0], out_strides[1], out_strides[2], _addr(lse),
         workspace.data_ptr(), workspace.shape[0], _raw_stream(dev))
     if status:
@@ -204,8 +209,9 @@ def mla_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, 
     """Attention of the last S tokens of each request over its cached rows (absorbed form).
 
     q bf16 [B, S, H, 576] or [B, H, 576] (any strides but the last):
-    the absorbed query and its rotated part.  block_table int32 [B, max_pages],
-    lengths int32 [B]: rows in the cache, the S tokens' own included.
+    the absorbed query and its rotated part.  block_table int32 [B, max_pages]
+    (one row ``expand``ed over requests that share their pages is read as it
+    is), lengths int32 [B]: rows in the cache, the S tokens' own included.
     Returns out bf16 [B, S, H, 512] (the input of the V-up product; [B, H,
     512] for a 3-D q), with ``return_lse`` also the fp32 log-sum-exp.
     ``workspace``: uint8, >= :func:`mla_decode_workspace_bytes`.
