@@ -337,9 +337,10 @@ int a16wfp4_bmm(const void* x, int64_t sxb, int64_t sxm,
  * and value of every head) and the rotated key part (64 values).  The cache
  * is paged: page p's row i at cache[p*cache_page + i*cache_row] (ELEMENTS;
  * multiples of 8, rows of 576 that do not overlap, 16-byte aligned), any
- * page size >= 1.  Page numbers and lengths are int32, positions and slots
- * int64, all on the device: they are read when the kernels run, so a
- * captured graph follows them.
+ * page size >= 1.  Of a dimension of one element the stride is not used and
+ * may be anything, here and for all tensors below.  Page numbers and lengths
+ * are int32, positions and slots int64, all on the device: they are read when
+ * the kernels run, so a captured graph follows them.
  *
  * mla_cache_append writes T tokens' rows.  For token t with x = kv[t]:
  *   row[:512] = round(x[:512] / sqrt(mean(x[:512]^2) + eps) * norm_weight)

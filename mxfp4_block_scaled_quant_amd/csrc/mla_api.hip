@@ -26,6 +26,9 @@ constexpr int64_t kMaxStride = 1ll << 40;  // elements: products with sizes stay
 inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
+// The stride of a dimension of n elements: one element's is never used, and a
+// view may have any number there.
+inline int64_t used(int64_t stride, int64_t n) { return n > 1 ? stride : 0; }
 inline int launched(hipError_t e) { return e == hipSuccess ? MXFP4_OK : MXFP4_ERR_LAUNCH; }
 
 // Whether rows of `width` elements at the given strides keep apart: walking
@@ -93,6 +96,10 @@ int decode_call(const void* q, int64_t q_batch, int64_t q_token, int64_t q_head,
                 int64_t out_token, int64_t out_head, void* lse, void* workspace, size_t workspace_bytes,
                 void* stream) {
   if (!(scale > 0.0f) || isinf(scale)) return MXFP4_ERR_ARG;
+  q_batch = used(q_batch, B), out_batch = used(out_batch, B), ldt = used(ldt, B);
+  q_token = used(q_token, S), out_token = used(out_token, S);
+  q_head = used(q_head, H), out_head = used(out_head, H);
+  cache_page = used(cache_page, pages), cache_row = used(cache_row, page_size);
   if (page_size < 1 || max_pages < 0 || max_pages > kMaxTokens || page_size > kMaxTokens) return MXFP4_ERR_SHAPE;
   if (max_pages * page_size > kMaxTokens || !decode_shape(B, S, H, max_pages * page_size, prefix_len))
     return MXFP4_ERR_SHAPE;
@@ -158,6 +165,9 @@ int mla_cache_append(const void* kv, int64_t ldkv, const void* norm_weight, floa
                      int64_t cache_row, int64_t T, int64_t H, void* stream) {
   if (interleaved != 0 && interleaved != 1) return MXFP4_ERR_ARG;
   if (!(eps >= 0.0f) || isinf(eps)) return MXFP4_ERR_ARG;
+  ldkv = used(ldkv, T), q_token = used(q_token, T), qo_token = used(qo_token, T);
+  q_head = used(q_head, H), qo_head = used(qo_head, H);
+  cache_page = used(cache_page, pages), cache_row = used(cache_row, page_size);
   if (T < 0 || T > kMaxInt || H < 0 || H > (1 << 20) || max_position < 0 || max_position > kMaxStride)
     return MXFP4_ERR_SHAPE;
   if ((T > 1 && ldkv < kRowDim) || !stride_ok(ldkv)) return MXFP4_ERR_SHAPE;
@@ -236,6 +246,9 @@ int mla_prefill(const void* q, int64_t q_token, int64_t q_head, const void* k_no
   if (B < 0 || B > (1 << 24) || H < 1 || H > (1 << 16) || Tq < 0 || Tk < 0 || Tq > kMaxTokens || Tk > kMaxTokens ||
       (Tq / 64 + (Tq < B ? Tq : B)) * H > kMaxInt)
     return MXFP4_ERR_SHAPE;
+  q_token = used(q_token, Tq), out_token = used(out_token, Tq);
+  k_token = used(k_token, Tk), pe_token = used(pe_token, Tk), v_token = used(v_token, Tk);
+  q_head = used(q_head, H), k_head = used(k_head, H), v_head = used(v_head, H), out_head = used(out_head, H);
   const int64_t in[] = {q_token, q_head, k_token, k_head, pe_token, v_token, v_head, out_token, out_head};
   for (int64_t s : in)
     if (!stride_ok(s)) return MXFP4_ERR_SHAPE;

@@ -96,3 +96,42 @@ def test_entry_takes_one_table_row_for_all_requests(lib, prefix):
     assert decode_entry(lib, prefix, ldt=0, width=0) == DEVICE
     assert decode_entry(lib, prefix, ldt=-1) == SHAPE and decode_entry(lib, prefix, ldt=3) == SHAPE
     assert decode_entry(lib, prefix, ldt=-1, width=0) == SHAPE
+
+
+@pytest.mark.parametrize("prefix", [False, True])
+def test_decode_entry_ignores_strides_of_single_elements(lib, prefix):
+    # a dimension of one element: its stride may be anything a view has
+    for stride in (1, 3, 580, 1 << 41):
+        assert decode_entry(lib, prefix, B=1, qb=stride, ob=stride) == DEVICE
+        assert decode_entry(lib, prefix, S=1, qs=stride, os=stride) == DEVICE
+        assert decode_entry(lib, prefix, H=1, qh=stride, oh=stride) == DEVICE
+        assert decode_entry(lib, prefix, B=1, ldt=stride) == DEVICE
+        assert decode_entry(lib, prefix, pages=1, cp=stride) == DEVICE
+        assert decode_entry(lib, prefix, page=1, cr=stride, cp=576) == DEVICE
+    # and of two is still checked
+    assert decode_entry(lib, prefix, B=2, qb=580) == ALIGN and decode_entry(lib, prefix, pages=2, cp=580) == SHAPE
+    assert decode_entry(lib, prefix, S=2, qs=580, ob=2 * 16 * 512) == ALIGN and decode_entry(lib, prefix, cr=1) == SHAPE
+
+
+def test_append_entry_ignores_strides_of_single_elements(lib):
+    def call(ldkv=576, qt=1024, qh=64, ot=1024, oh=64, pages=4, page=16, cp=16 * 576, cr=576, T=3, H=16):
+        return lib.mla_cache_append(P, ldkv, P, 1e-6, P, 100, P, P, 1, P, qt, qh, P, ot, oh, P, pages, page, cp, cr, T,
+                                    H, None)
+
+    for stride in (1, 3, 580, 1 << 41):
+        assert call(T=1, ldkv=stride, qt=stride, ot=stride) == DEVICE
+        assert call(H=1, qh=stride, oh=stride) == DEVICE
+        assert call(pages=1, cp=stride) == DEVICE and call(page=1, cr=stride, cp=576) == DEVICE
+    assert call(T=2, ldkv=580) == ALIGN and call(T=2, qt=1028) == ALIGN
+
+
+def test_prefill_entry_ignores_strides_of_single_elements(lib):
+    def call(qt=16 * 192, qh=192, kt=2048, kh=128, pt=64, vt=2048, vh=128, H=16, Tq=5, Tk=5, ot=2048, oh=128):
+        return lib.mla_prefill(P, qt, qh, P, kt, kh, P, pt, P, vt, vh, P, P, 1, H, Tq, Tk, 128, 128, 1, 0.1, P, ot, oh,
+                               None, None)
+
+    for stride in (1, 3, 580, 1 << 41):
+        assert call(Tq=1, qt=stride, ot=stride) == DEVICE
+        assert call(Tk=1, kt=stride, pt=stride, vt=stride) == DEVICE
+        assert call(H=1, qh=stride, kh=stride, vh=stride, oh=stride) == DEVICE
+    assert call(Tq=2, qt=580) == ALIGN and call(Tk=2, vt=580) == ALIGN and call(H=2, kh=580) == ALIGN
