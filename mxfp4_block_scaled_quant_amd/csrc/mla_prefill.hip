@@ -53,6 +53,21 @@ struct Cfg {
   static_assert(kLds <= 80 * 1024, "two workgroups a compute unit");
 };
 
+// The rows of sequence b.  Offsets are clamped to the packed tensors: bad ones
+// cannot leave them, as long as every use of the offsets goes through here (a
+// block counted from the offsets themselves can lie at rows below 0, where the
+// products of wild ones wrap).
+struct Span {
+  int64_t q0, k0;
+  int nq, nk;
+  __device__ __forceinline__ Span(const MlaPrefillArgs& a, int b) {
+    q0 = max((int64_t)0, min(a.Tq, (int64_t)a.cu_q[b]));
+    k0 = max((int64_t)0, min(a.Tk, (int64_t)a.cu_k[b]));
+    nq = (int)(max(q0, min(a.Tq, (int64_t)a.cu_q[b + 1])) - q0);
+    nk = (int)(max(k0, min(a.Tk, (int64_t)a.cu_k[b + 1])) - k0);
+  }
+};
+
 // Query block `blk` of R rows, counted by the keys it sees from the most down
 // (whatever sequence it is of: where all blocks run at once, long and short
 // ones then share the compute units; the chunks above 0.67 -> 0.63 ms), 64
@@ -67,9 +82,9 @@ __device__ __forceinline__ bool find_block(const MlaPrefillArgs& a, int blk, int
     const int k = s + lane;
     int n = 0, first = 0;  // blocks, and the level of the first (causal) or of all
     if (k < a.B) {
-      const int64_t nq = (int64_t)a.cu_q[k + 1] - a.cu_q[k], nk = (int64_t)a.cu_k[k + 1] - a.cu_k[k];
-      n = nq > 0 ? (int)((nq + R - 1) / R) : 0;
-      first = (int)((a.causal ? nk - nq : nk) >> __builtin_ctz(R));
+      const Span rows(a, k);
+      n = (rows.nq + R - 1) / R;
+      first = (a.causal ? rows.nk - rows.nq : rows.nk) >> __builtin_ctz(R);
     }
     const int total = wave_sum(n);
     if (blk >= total) {
@@ -105,19 +120,6 @@ __device__ __forceinline__ bool find_block(const MlaPrefillArgs& a, int blk, int
   }
   return false;
 }
-
-// The rows of sequence b.  Offsets are clamped to the packed tensors: bad ones
-// cannot leave them.
-struct Span {
-  int64_t q0, k0;
-  int nq, nk;
-  __device__ __forceinline__ Span(const MlaPrefillArgs& a, int b) {
-    q0 = max((int64_t)0, min(a.Tq, (int64_t)a.cu_q[b]));
-    k0 = max((int64_t)0, min(a.Tk, (int64_t)a.cu_k[b]));
-    nq = (int)(max(q0, min(a.Tq, (int64_t)a.cu_q[b + 1])) - q0);
-    nk = (int)(max(k0, min(a.Tk, (int64_t)a.cu_k[b + 1])) - k0);
-  }
-};
 
 // A row's outputs: columns 32 i + 8 j + 4 (lane / 32) + (0..3) are 4 j.. of
 // the lane's accumulator of column tile i.
