@@ -53,7 +53,9 @@ static_assert(kLdsBytes <= 160 * 1024, "LDS per workgroup");
 
 // What masked keys load: a key past the end or in a page the cache does not
 // have scores -inf and must add 0 * value with a finite value.
-__device__ const uint16_t zero_row[kRowDim] = {};
+// (16-byte loads read it: so its elements are 16 bytes.)
+__device__ const int4 zero_row[kRowDim / 8] = {};
+static_assert(sizeof(zero_row) == kRowDim * 2 && alignof(decltype(zero_row)) == 16, "a row, in 16-byte pieces");
 
 // One list of work: `B` sequences of rows, `rows` query rows each.
 struct ListArgs {
@@ -956,7 +958,7 @@ __device__ __forceinline__ void join_row(const ListArgs& a, const ListArgs& p, i
 // 512 / CS columns each.
 template <int RB, int PRB, int CS>
 __global__ __launch_bounds__(256) void mla_join_kernel(ListArgs a, ListArgs p) {
-  __shared__ float so[4][512 / CS];
+  __shared__ alignas(16) float so[4][512 / CS];  // (read 16 bytes at a time)
   __shared__ float sml[4][3];
   const int b = blockIdx.x / a.rows, r = blockIdx.x - b * a.rows;
   join_row<RB, PRB, CS, false>(a, p, b, r, blockIdx.y * (512 / CS), so, sml);
