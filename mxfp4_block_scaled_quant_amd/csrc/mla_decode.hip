@@ -858,10 +858,12 @@ __device__ __forceinline__ RowParts row_parts(const ListArgs& a, int b, int r, i
 
 // Joins the parts of query row r of sequence b, columns c0 .. c0 + 512 / CS: a
 // wave's lanes fetch 64 parts' maxima and sums at once, then it runs over the
-// parts' values, 8 / CS a lane.  ALONE: one wave takes all parts; otherwise
-// wave w of a workgroup takes parts w, w + 4, .., and the four waves' sums
-// meet in LDS in wave order.  Rows that one workgroup of a call without a
-// prefix wrote itself are left alone; rows without any key become 0 and -inf.
+// parts' values, 8 / CS a lane, one part after another (the loop is not
+// unrolled: its lane read keeps the compiler from it).  ALONE: one wave takes
+// all parts; otherwise wave w of a workgroup takes parts w, w + 4, .., and the
+// four waves' sums meet in LDS in wave order.  Rows that one workgroup of a
+// call without a prefix wrote itself are left alone; rows without any key
+// become 0 and -inf.
 template <int RB, int PRB, int CS, bool ALONE>
 __device__ __forceinline__ void join_row(const ListArgs& a, const ListArgs& p, int b, int r, int c0, float (*so)[512 / CS],
                                          float (*sml)[3]) {
@@ -869,7 +871,6 @@ __device__ __forceinline__ void join_row(const ListArgs& a, const ListArgs& p, i
   typedef float vec __attribute__((ext_vector_type(CS == 1 ? 4 : W)));
   constexpr int V = CS == 1 ? 4 : W, NV = W / V;  // read as NV vectors, 64 lanes apart
   constexpr int kStride = ALONE ? 1 : 4;         // waves that share the parts
-  constexpr int kAhead = ALONE ? 8 : 4;          // parts under way
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const RowId id = row_id(a, b, r);
   const int64_t flat = flat_row(a.d, id);
@@ -906,7 +907,6 @@ __device__ __forceinline__ void join_row(const ListArgs& a, const ListArgs& p, i
     m = mn;
 #pragma unroll
     for (int v = 0; v < NV; ++v) o[v] *= keep;
-#pragma unroll kAhead
     for (int i = 0; i < n; ++i) {
       const float fi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
       part_at(i0 + kStride * i, po, pm);
