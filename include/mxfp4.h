@@ -394,6 +394,10 @@ int mla_cache_append(const void* kv, int64_t ldkv, const void* norm_weight, floa
  *   scale     finite, > 0
  *   out       bf16 (b, s, h, i < 512), strides as for q; rows must not overlap
  *   lse       fp32 [B, S, H] contiguous, or NULL
+ *   max_pages the table's width also chooses the kernel's row blocks, for
+ *             requests that fill it; pass no wider a table than is needed
+ *             (32 requests of 64 heads and 1000 rows: 30 us in a table of
+ *             1024 rows, 38 in one of 131072)
  *   workspace mla_decode_workspace_bytes bytes (max_tokens = max_pages *
  *             page_size, prefix_len 0), 16-byte aligned; scratch of this call
  *   B >= 0 (0 enqueues nothing), S, H >= 1, B*S*H <= 2^22,
@@ -401,7 +405,7 @@ int mla_cache_append(const void* kv, int64_t ldkv, const void* norm_weight, floa
  *
  * mla_decode_shared_prefix: the rows of prefix_table's pages (prefix_len of
  * them, int32 table of prefix_pages) come before every request's own rows
- * and are seen by all tokens; they are read once for the whole batch.  With
+ * and are seen by all tokens; they are read for the batch together.  With
  * lengths >= S the result is that of mla_decode over the joined rows.
  * lengths counts a request's own rows only; workspace for the same prefix_len.
  */

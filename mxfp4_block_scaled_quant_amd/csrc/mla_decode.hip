@@ -4,10 +4,12 @@
 // values, also the value, so a request's S tokens x H heads are S*H query
 // rows over ONE sequence of rows:
 //   z = scale q . row,  out = softmax(z) rows[:, :512],  lse = ln sum exp z.
-// Each row is read once from HBM for 2 * S*H * (576 + 512) operations: 30
-// per byte at 16 query rows (bound by HBM), 242 at 128 (near the ridge of
-// the matrix units), and a prefix that all requests share is bound by the
-// matrix units.  Measured on MI355X: 128 requests of 16 heads over up to
+// Each row has to be read once for 2 * S*H * (576 + 512) operations: 30 per
+// byte at 16 query rows (bound by HBM), 242 at 128 (near the ridge of the
+// matrix units), and a prefix that all requests share is bound by the matrix
+// units.  A sequence's row blocks read it each for themselves, from L2 where
+// they meet in one: 12 requests of 4 row blocks fetch 2.8 times their rows'
+// bytes from HBM, one row block each 1.0 times.  Measured on MI355X: 128 requests of 16 heads over up to
 // 16000 rows (1.06 GB) 188 us, 5.6 TB/s; 6 of 40000 to 65000 76 us, 4.6 TB/s;
 // one of 777 rows 14 us, the time of two launches and one pass of each; 12
 // requests of 4 tokens x 128 heads over 1500 to 8191 rows 100 us and 96
@@ -18,9 +20,9 @@
 //
 // Work is cut along the keys.  The list of all requests' key units (128 keys
 // for 16 and 32 query rows, 64 above, and an item's setup) is dealt to the
-// workgroups in equal contiguous shares, computed by each workgroup from the lengths on the
-// device, so ragged batches stay balanced and a captured graph follows new
-// lengths.  A workgroup that holds a whole (request, row block) writes its
+// workgroups in equal contiguous shares, computed by each workgroup from the
+// lengths on the device, so ragged batches stay balanced and a captured graph
+// follows new lengths.  A workgroup that holds a whole (request, row block) writes its
 // output; otherwise the fp32 accumulators, maxima and sums go to the
 // workspace, and a second kernel joins a row's parts in key order (results
 // do not depend on timing).
@@ -986,7 +988,11 @@ int setup_keys(int rb) { return rb <= 32 ? setup_units<16>() * unit_keys(rb) : s
 // and 8000 keys (7.9 units a compute unit) 41.4 / 42.3 / 44.7, one of 128
 // rows and 32000 (7.8) 42.7 / 42.8 / 55.2; 8 of 128 and 8000 (15.8) 63.6 /
 // 51.2 / 51.0, 32 of 32 and 8000 (15.8) 88.5 / 76.9 / 91.9, 8 of 64 and
-// 32000 (31) 144 / 99 / 94, 4 of 512 and 32000 (125) 370 / 214 / 156.
+// 32000 (31) 144 / 99 / 94, 4 of 512 and 32000 (125) 370 / 214 / 156.  n is
+// what the page table can hold, the lengths being known on the device alone
+// (and the workspace is sized before them), so short requests in a wide table
+// take the form of long ones: 32 requests of 64 rows and 1000 keys 29.6 us in
+// a table of 1024 rows, 37.8 in one of 131072.
 int rows_per_block(int64_t B, int64_t rows, int64_t n) {
   if (const int forced = get_mla_rows_override()) return forced;
   if (rows <= 16 || B * cdiv(rows, 16) * cdiv(n, 128) <= 10ll * kMlaMaxCus) return 16;

@@ -13,13 +13,18 @@
 // softmax steps spread between the products, or a wave priority for them, the
 // same.
 //
-// Bound by the matrix units, and they by the card's power: 2 (dn + 64 + dv)
-// operations per (query, key) pair, 16384 causal tokens of 16 heads at
-// 192 + 64 and 256: 1.93-1.98 ms, 1.11-1.14 PFLOP/s; 2 x 1900-2048 tokens
-// after 14003 others at 128 + 64 and 128: 0.63 ms, 0.96; 9 prompts of 17 to
-// 4001 tokens at 192 + 64 and 256: 0.39 ms, 0.87.  The clock falls to 1.65
-// GHz under it; the same launch on zeros reaches 1.35 PFLOP/s, and a library
-// product of random 8192 x 8192 matrices 1.44.
+// 2 (dn + 64 + dv) operations per (query, key) pair.  16384 causal tokens of
+// 16 heads at 192 + 64 and 256: 1.93-2.12 ms, 1.04-1.14 PFLOP/s; 2 x 1900-2048
+// tokens after 14003 others at 128 + 64 and 128: 0.63-0.68 ms, 0.90-0.96; 9
+// prompts of 17 to 4001 tokens at 192 + 64 and 256: 0.39-0.41 ms, 0.83-0.87; a
+// library product of random 8192 x 8192 matrices 1.44.  What bounds them
+// differs.  The long prompt keeps the matrix units busy 64% of the time, and
+// the card's power holds the clock at 1.5 to 1.8 GHz under it (the same launch
+// on zeros reaches 1.35 PFLOP/s).  The chunks keep them busy 47% at 2.1 GHz:
+// there 6.6 vector instructions go with each product (softmax and addresses of
+// a tile, for 20 products a wave instead of 32), against 4.6 at 256 values.
+// The ragged prompts keep them busy 48% at 2.05 GHz, with 5.2 instructions a
+// product and the masked tiles and last blocks of nine sequences.
 //
 // Few query rows leave most compute units idle that way, each workgroup
 // walking all of its keys alone: there the four waves of a workgroup take 32

@@ -89,7 +89,9 @@ def mla_cache_append(kv: torch.Tensor, norm_weight: torch.Tensor, cache: torch.T
     angles, then their sin).  ``slots`` int64 [T]: page * page_size + row; a
     negative slot writes no row.  ``q_pe`` bf16 [T, H, 64] (any strides) is
     rotated into ``q_out`` (allocated when not given; it may be ``q_pe``
-    itself, or the last 64 columns of an absorbed query).
+    itself, or the last 64 columns of an absorbed query).  Nothing is written
+    for a token whose position lies outside the table: its rows of an allocated
+    ``q_out`` are not initialised.
     """
     _require_cuda(kv, "kv")
     dev = kv.device
@@ -214,7 +216,9 @@ def mla_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, 
     is), lengths int32 [B]: rows in the cache, the S tokens' own included.
     Returns out bf16 [B, S, H, 512] (the input of the V-up product; [B, H,
     512] for a 3-D q), with ``return_lse`` also the fp32 log-sum-exp.
-    ``workspace``: uint8, >= :func:`mla_decode_workspace_bytes`.
+    ``workspace``: uint8, >= :func:`mla_decode_workspace_bytes`.  The table's
+    width, not the lengths, chooses the kernel's row blocks: a narrow view of a
+    wide table (``table[:, :pages_in_use]``) is faster where requests are short.
     """
     return _decode("mla_decode", q, cache, None, block_table, lengths, scale, return_lse, out, lse, workspace)
 
@@ -224,7 +228,7 @@ def mla_decode_shared_prefix(q: torch.Tensor, cache: torch.Tensor, prefix_table:
                              return_lse: bool = False, out: Optional[torch.Tensor] = None,
                              lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
     """:func:`mla_decode` where ``prefix_len`` rows (pages ``prefix_table``, int32 1-D)
-    come before every request's own; they are read once for the batch.
+    come before every request's own; they are read for the batch together.
     ``lengths`` and ``block_table`` describe the requests' own rows only."""
     return _decode("mla_decode_shared_prefix", q, cache, (prefix_table, prefix_len), block_table, lengths, scale,
                    return_lse, out, lse, workspace)
