@@ -454,6 +454,100 @@ int mla_prefill(const void* q, int64_t q_token, int64_t q_head, const void* k_no
                 int64_t dv, int causal, float scale, void* out, int64_t out_token,
                 int64_t out_head, void* lse, void* stream);
 
+/* ---- Feed-forward: routing to experts, their products, and the linear with
+ * an epilogue.  Same conventions as above; a row stride is not read where
+ * there is one row. ---- */
+
+/* Activations of an epilogue: v; v / (1 + exp(-v)); v/2 (1 + erf(v / sqrt 2));
+ * v/2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))); max(v, 0). */
+enum {
+  MXFP4_ACT_NONE = 0,
+  MXFP4_ACT_SILU = 1,
+  MXFP4_ACT_GELU = 2,
+  MXFP4_ACT_GELU_TANH = 3,
+  MXFP4_ACT_RELU = 4
+};
+
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+/*
+ * A token's experts.  An expert whose logit or bias is -inf or NaN is not
+ * available; +inf counts as the largest finite number.
+ *   s = softmax of the logits over the available experts, or 1 / (1 + exp(-x))
+ *   c = s + bias (chooses only; the weights come from s)
+ *   groups > 1: group g is experts [g E/groups, (g+1) E/groups); its score is
+ *     the sum of its group_top (1 or 2) largest available c; the top_groups
+ *     best of them stay, equal ones by number
+ *   ids     the top_k best of what stays by c in 64 bits, equal ones by
+ *           logit, then by number, the best first; -1 where none is left
+ *   weights scale * s, divided by the sum of the chosen s if renormalize;
+ *           0 where the id is -1
+ *
+ *   logits  bf16 or fp32 (logits_dtype MXFP4_OUT_BF16 / _F32) [tokens, experts],
+ *           row stride ld ELEMENTS; bias fp32 [experts] or NULL
+ *   weights fp32, ids int32 [tokens, top_k], row strides ldw and ldi
+ *   tokens >= 0 (0 enqueues nothing), 1 <= experts <= 1024, 1 <= top_k <= 64
+ *   and <= the experts of the groups that stay, groups <= 64 dividing experts.
+ */
+int moe_route(const void* logits, int64_t ld, int logits_dtype, const void* bias,
+              int64_t tokens, int64_t experts, int64_t top_k, int scoring, int64_t groups,
+              int64_t top_groups, int64_t group_top, int renormalize, float scale, void* weights,
+              int64_t ldw, void* ids, int64_t ldi, void* stream);
+
+/*
+ * The chosen experts' products.  For token t and choice j with
+ * e = ids[t, j] in [0, experts):
+ *   v = dq(Q(x_t)) dq(U_e)^T + up_bias[e]
+ *   h = bf16(act(v)), gated: bf16(act(v[:inner]) * v[inner:])
+ *   y = dq(Q(h)) dq(D_e)^T + down_bias[e]
+ *   out_t = round(residual_t + sum_j weights[t, j] y)
+ * with Q the quantisation of mxfp4_quant_1x32, products and sums in fp32, the
+ * sum in the order of j.  A choice whose id is outside [0, experts) (an
+ * expert of another GPU, a token of padding) adds nothing.
+ *
+ *   x         bf16 [tokens, hidden], row stride ldx (% 8), 16-byte aligned
+ *   ids       int32, weights fp32 [tokens, top_k], row strides ldi and ldw
+ *   up_pre    preshuffled MXFP4 [experts, inner or 2 * inner (gated), hidden]
+ *   down_pre  preshuffled MXFP4 [experts, hidden, inner]
+ *             (mxfp4_preshuffle_weight with batch = experts)
+ *   up_bias, down_bias  bf16 [experts, rows of the weight], or NULL
+ *   residual  bf16 [tokens, hidden] (row stride ldr % 4, 8-byte aligned), or
+ *             NULL; it may be out itself
+ *   out       bf16 [tokens, hidden], row stride ldo (% 4), 8-byte aligned
+ *   workspace mxfp4_moe_workspace_bytes bytes, 256-byte aligned; scratch of
+ *             this call
+ *   tokens >= 0 (0 enqueues nothing), tokens * top_k <= 2^24, top_k <= 64,
+ *   experts <= 1024, hidden and inner multiples of 32 up to 2^20; an expert's
+ *   weight stays below 2 GiB.
+ */
+size_t mxfp4_moe_workspace_bytes(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden,
+                                 int64_t inner);
+int mxfp4_moe(const void* x, int64_t ldx, const void* ids, int64_t ldi, const void* weights,
+              int64_t ldw, const void* up_pre, const void* up_scales, const void* up_bias,
+              const void* down_pre, const void* down_scales, const void* down_bias,
+              const void* residual, int64_t ldr, void* out, int64_t ldo, int64_t tokens,
+              int64_t top_k, int64_t experts, int64_t hidden, int64_t inner, int activation,
+              int gated, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mxfp4_linear with an epilogue:
+ *   v = dq(Q(x)) dq(W)^T + bias
+ *   out = round(act(v) + residual), gated: round(act(v[:, :N/2]) * v[:, N/2:] + residual)
+ * the sums, the activation and the residual in fp32, rounded once.
+ *
+ *   N         rows of the weight; gated halves the output's columns, and N is
+ *             then a multiple of 32
+ *   residual  bf16 [M, N or N/2], row stride ldr, or NULL; it may be a bf16
+ *             out itself
+ *   workspace mxfp4_linear_act_workspace_bytes bytes, 256-byte aligned
+ *   the rest as in mxfp4_linear.
+ */
+size_t mxfp4_linear_act_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int mxfp4_linear_act(const void* x, int64_t ldx, const void* w_pre, const void* ws_pre,
+                     const void* bias, int activation, int gated, const void* residual,
+                     int64_t ldr, void* out, int64_t ldo, int out_dtype, int64_t M, int64_t N,
+                     int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+
 #pragma GCC visibility pop
 
 #ifdef __cplusplus

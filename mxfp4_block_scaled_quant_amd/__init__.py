@@ -28,6 +28,10 @@ Entry points (same names as the C ABI):
   between the absorbed products: cache write, attention over the paged
   latents, with a shared prefix, and over expanded keys and values
   (:mod:`mxfp4_block_scaled_quant_amd.mla`)
+* :func:`moe_route`, :func:`mxfp4_moe`, :func:`mxfp4_linear_act` -- the
+  feed-forward half: a token's experts and their weights, the experts'
+  products, and the linear with bias, activation (gated or not) and residual
+  in its epilogue (:mod:`mxfp4_block_scaled_quant_amd.moe`)
 
 Convenience: :func:`quantize_weight` (quant + preshuffle, once at load) and
 :func:`linear` (:func:`mxfp4_linear` over any leading dimensions).  The same
@@ -97,6 +101,14 @@ _SIGNATURES = {
                                  + [_c_vp, _c_i64, _c_i64] + _MLA_REQUESTS),
     "mla_prefill": (_c_int, [_c_vp, _c_i64, _c_i64] * 2 + [_c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp]
                     + [_c_i64] * 6 + [_c_int, _c_f32, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp]),
+    "moe_route": (_c_int, [_c_vp, _c_i64, _c_int, _c_vp] + [_c_i64] * 3 + [_c_int] + [_c_i64] * 3
+                  + [_c_int, _c_f32, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp]),
+    "mxfp4_moe_workspace_bytes": (_c_size, [_c_i64] * 5),
+    "mxfp4_moe": (_c_int, [_c_vp, _c_i64] * 3 + [_c_vp] * 6 + [_c_vp, _c_i64] * 2 + [_c_i64] * 5
+                  + [_c_int, _c_int, _c_vp, _c_size, _c_vp]),
+    "mxfp4_linear_act_workspace_bytes": (_c_size, [_c_i64] * 3),
+    "mxfp4_linear_act": (_c_int, [_c_vp, _c_i64, _c_vp, _c_vp, _c_vp, _c_int, _c_int, _c_vp, _c_i64, _c_vp, _c_i64,
+                                  _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_size, _c_vp]),
     "mxfp4_testing_set_gemm_path": (_c_int, [_c_int]),
     "mla_testing_set_rows": (_c_int, [_c_int]),
     "mla_testing_set_prefill_rows": (_c_int, [_c_int]),
@@ -514,3 +526,5 @@ def linear(x: torch.Tensor, weight: MXFP4Weight, bias: Optional[torch.Tensor] = 
 
 from .mla import (mla_cache_append, mla_decode, mla_decode_shared_prefix,  # noqa: E402
                   mla_decode_workspace_bytes, mla_prefill, set_mla_prefill_rows, set_mla_rows)
+from .moe import (moe_route, mxfp4_linear_act, mxfp4_linear_act_workspace_bytes, mxfp4_moe,  # noqa: E402
+                  mxfp4_moe_workspace_bytes)

@@ -1,0 +1,372 @@
+// Routing to experts: scores, choice by group and score, renormalised
+// weights (gfx950).
+//
+// Per token, over its E logits x (one that is NaN or -inf, or whose bias is,
+// is not available; +inf counts as the largest finite value):
+//   s = softmax(x) over the available, or 1 / (1 + exp(-x));  c = s + bias
+//   group g = experts [g E/G, (g+1) E/G): its score is its largest available
+//   c, or the sum of its two largest; the best `kept` groups stay
+//   the best top_k by (c, x), equal ones by index; w = s (/ their sum) * scale
+//
+// L lanes hold one token's experts, V consecutive ones each, in registers:
+// one read of the logits, and every step of the choice is a few lane
+// permutations (DPP within 16 lanes) of a register value.  Each of the top_k
+// rounds finds the largest value left, then the lowest index that holds it,
+// and takes it out.
+//
+// The choice is that of 64-bit scores.  Without a bias (or with the same one
+// everywhere) the order of a token's scores is the logits' own, and they are
+// compared instead.  With one, fp32 scores decide wherever the values they
+// compare differ by more than twice their error (the margins below); where
+// one comparison of a wave's tokens does not, the wave chooses again in 64
+// bits.
+#include <float.h>
+
+#include "moe_launch.h"
+#include "mxfp4_device.h"
+
+namespace mxfp4 {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// Bounds of the difference of two fp32 scores c from that of the exact ones:
+// base + |c| * kMarginRel (c = s + bias is rounded once: 2^-24 |c| each).
+// A sigmoid's exponent is off by |x| 2^-23 relative, its power by an ulp,
+// the quotient by two: s (1 - s) (|x| + 2) 2^-23 + 3 * 2^-24 < 2^-21.5 each.
+// A softmax term is off by (|x - max| 2 + 2) 2^-23 relative, its sum by the
+// terms' error and one rounding per addition (at most 16 + 6): < 2.1e-6 of
+// s <= 1 each.
+constexpr float kMarginSigmoid = 1.0e-6f;
+constexpr float kMarginSoftmax = 5.0e-6f;
+constexpr float kMarginRel = 2.5e-7f;
+
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, true);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(int, v)));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  int w[2];
+  __builtin_memcpy(w, &v, 8);
+  w[0] = dpp<CTRL>(w[0]);
+  w[1] = dpp<CTRL>(w[1]);
+  __builtin_memcpy(&v, w, 8);
+  return v;
+}
+
+// The lane that step S of a reduction over 2^S neighbours pairs this one
+// with: lane ^ 1, lane ^ 2, then the mirror image in 8 and in 16 lanes (as
+// good as ^ 4 and ^ 8 once the lanes of a half agree), lane ^ 16, lane ^ 32.
+template <int S, typename T>
+__device__ __forceinline__ T partner(T v) {
+  if constexpr (S == 0) return dpp<0xB1>(v);
+  if constexpr (S == 1) return dpp<0x4E>(v);
+  if constexpr (S == 2) return dpp<0x141>(v);
+  if constexpr (S == 3) return dpp<0x140>(v);
+  if constexpr (S == 4) return __shfl_xor(v, 16);
+  if constexpr (S == 5) return __shfl_xor(v, 32);
+}
+
+constexpr int log2of(int n) { return n <= 1 ? 0 : 1 + log2of(n / 2); }
+
+// Reductions over the L lanes of a token; every lane has the result.
+template <int L, int S = 0, typename T>
+__device__ __forceinline__ T all_max(T v) {
+  if constexpr (S == log2of(L)) return v;
+  else {
+    const T o = partner<S>(v);
+    return all_max<L, S + 1>(o > v ? o : v);
+  }
+}
+template <int L, int S = 0, typename T>
+__device__ __forceinline__ T all_min(T v) {
+  if constexpr (S == log2of(L)) return v;
+  else {
+    const T o = partner<S>(v);
+    return all_min<L, S + 1>(o < v ? o : v);
+  }
+}
+template <int L, int S = 0, typename T>
+__device__ __forceinline__ T all_sum(T v) {
+  if constexpr (S == log2of(L)) return v;
+  else return all_sum<L, S + 1>(v + partner<S>(v));
+}
+
+// The two largest of two pairs (a >= b).
+template <typename F>
+__device__ __forceinline__ void merge2(F& a, F& b, F oa, F ob) {
+  const F lo = a < oa ? a : oa;
+  const F hb = b > ob ? b : ob;
+  a = a > oa ? a : oa;
+  b = lo > hb ? lo : hb;
+}
+// ... over the 2^n lanes that share a group (n uniform).
+template <int L, int S = 0, typename F>
+__device__ __forceinline__ void merge_lanes(F& a, F& b, int n) {
+  if constexpr (S < log2of(L)) {
+    if (S < n) {
+      const F oa = partner<S>(a), ob = partner<S>(b);
+      merge2(a, b, oa, ob);
+      merge_lanes<L, S + 1>(a, b, n);
+    }
+  }
+}
+
+__device__ __forceinline__ float exp_of(float v) { return __builtin_amdgcn_exp2f(v * kLog2e); }
+__device__ __forceinline__ double exp_of(double v) { return exp(v); }
+__device__ __forceinline__ float quotient(float a, float b) { return a * __builtin_amdgcn_rcpf(b); }
+__device__ __forceinline__ double quotient(double a, double b) { return a / b; }
+
+template <typename F>
+struct Lowest;
+template <>
+struct Lowest<float> {
+  static constexpr float v = -__builtin_huge_valf();
+};
+template <>
+struct Lowest<double> {
+  static constexpr double v = -__builtin_huge_val();
+};
+
+// What the choice needs of the call, the same in every lane.
+struct Choice {
+  int experts, top_k, groups, kept, group_top;
+  int size;          // experts of a group
+  int lanes2;        // log2 of the lanes that hold one group, -1: groups do not fill whole lanes
+  bool by_logit;     // the logits' order is the scores'
+};
+
+// The choice for one token in precision F.  x: the lane's logits (-inf where
+// not available), b: their biases.  Returns the expert of round `lane`
+// (lane < top_k; -1: none left); `unsure` is set where a comparison was
+// closer than fp32 can tell (F = float only).
+template <int L, int V, bool SIGMOID, typename F>
+__device__ __forceinline__ int choose(const Choice& p, const float (&x)[V], const float (&b)[V], int lane,
+                                      bool& unsure) {
+  constexpr F kLow = Lowest<F>::v;
+  constexpr bool kFast = sizeof(F) == 4;
+  constexpr float kBase = SIGMOID ? kMarginSigmoid : kMarginSoftmax;
+  F key[V];
+  const bool grouped = p.groups > 1;  // groups are compared by their scores
+  if (!p.by_logit || grouped) {
+    if constexpr (SIGMOID) {
+#pragma unroll
+      for (int r = 0; r < V; ++r) key[r] = quotient((F)1, (F)1 + exp_of(-(F)x[r]));
+    } else {
+      float m = x[0];
+#pragma unroll
+      for (int r = 1; r < V; ++r) m = fmaxf(m, x[r]);
+      m = all_max<L>(m);
+      F z = 0;
+#pragma unroll
+      for (int r = 0; r < V; ++r) {
+        key[r] = x[r] > -__builtin_huge_valf() ? exp_of((F)x[r] - (F)m) : (F)0;
+        z += key[r];
+      }
+      z = all_sum<L>(z);
+      const F inv = quotient((F)1, z);
+#pragma unroll
+      for (int r = 0; r < V; ++r) key[r] *= inv;
+    }
+#pragma unroll
+    for (int r = 0; r < V; ++r) key[r] = x[r] > -__builtin_huge_valf() ? key[r] + (F)b[r] : kLow;
+  } else {
+#pragma unroll
+    for (int r = 0; r < V; ++r) key[r] = (F)x[r];
+  }
+
+  if (p.groups > 1) {
+    // every lane g < groups gets group g's score
+    F mine = kLow;
+    if (p.lanes2 >= 0) {
+      F a = kLow, c = kLow;
+#pragma unroll
+      for (int r = 0; r < V; ++r) merge2(a, c, key[r], kLow);
+      merge_lanes<L>(a, c, p.lanes2);
+      const F score = (p.group_top == 2 && c > kLow) ? a + c : a;
+      mine = __shfl(score, (lane << p.lanes2) & (L - 1), L);
+    } else {
+      for (int g = 0; g < p.groups; ++g) {
+        F a = kLow, c = kLow;
+#pragma unroll
+        for (int r = 0; r < V; ++r) {
+          const int e = lane * V + r;
+          merge2(a, c, (e >= g * p.size && e < (g + 1) * p.size) ? key[r] : kLow, kLow);
+        }
+        merge_lanes<L>(a, c, log2of(L));
+        const F score = (p.group_top == 2 && c > kLow) ? a + c : a;
+        if (lane == g) mine = score;
+      }
+    }
+    if (lane >= p.groups) mine = kLow;
+    int ahead = 0;
+    for (int g = 0; g < p.groups; ++g) {
+      const F other = __shfl(mine, g, L);
+      ahead += (other > mine || (other == mine && g < lane)) ? 1 : 0;
+    }
+    const bool stays = lane < p.groups && ahead < p.kept && mine > kLow;
+    if constexpr (kFast) {
+      const float lo = all_min<L>(stays ? mine : __builtin_huge_valf());
+      const float hi = all_max<L>(stays ? kLow : mine);
+      // (written so that inf - inf counts as too close)
+      if (hi > kLow && !(lo - hi > 2 * kBase + 2 * kMarginRel * fabsf(hi))) unsure = true;
+    }
+    const uint64_t votes = __ballot(stays);
+    const uint64_t here = votes >> ((threadIdx.x & 63) & ~(L - 1));
+    int g = lane * V / p.size, at = lane * V - g * p.size;
+#pragma unroll
+    for (int r = 0; r < V; ++r) {
+      const bool in = g < p.groups && (here >> (g & 63) & 1);
+      key[r] = in ? (p.by_logit ? (F)x[r] : key[r]) : kLow;
+      if (++at == p.size) at = 0, ++g;
+    }
+  }
+
+  int id = -1;
+  F before = kLow;
+  const bool check = kFast && !p.by_logit;
+  for (int j = 0; j < p.top_k + (check ? 1 : 0); ++j) {
+    F best = key[0];
+#pragma unroll
+    for (int r = 1; r < V; ++r) best = key[r] > best ? key[r] : best;
+    best = all_max<L>(best);
+    if constexpr (kFast) {
+      if (check && j > 0 && best > kLow && !(before - best > kBase + kMarginRel * fabsf(best))) unsure = true;
+      before = best;
+    }
+    int at = 1 << 20;
+    if constexpr (kFast) {
+#pragma unroll
+      for (int r = V - 1; r >= 0; --r) at = key[r] == best ? lane * V + r : at;
+    } else {
+      float bx = -__builtin_huge_valf();
+#pragma unroll
+      for (int r = 0; r < V; ++r) bx = key[r] == best ? fmaxf(bx, x[r]) : bx;
+      bx = all_max<L>(bx);
+#pragma unroll
+      for (int r = V - 1; r >= 0; --r) at = (key[r] == best && x[r] == bx) ? lane * V + r : at;
+    }
+    at = all_min<L>(at);
+    if (lane == j) id = best > kLow ? at : -1;
+#pragma unroll
+    for (int r = 0; r < V; ++r) key[r] = lane * V + r == at ? kLow : key[r];
+  }
+  return id;
+}
+
+template <int L, int V, bool SIGMOID, bool F32>
+__global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs p, int lanes2) {
+  constexpr float kLow = -__builtin_huge_valf();
+  const int lane = threadIdx.x & (L - 1);
+  const int64_t token = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  const bool live = token < p.tokens;
+  const int64_t row = (live ? token : p.tokens - 1) * p.ld;
+
+  float x[V], b[V];
+  float lo = -kLow, hi = kLow;
+#pragma unroll
+  for (int r = 0; r < V; ++r) {
+    const int e = lane * V + r;
+    const int at = e < p.experts ? e : p.experts - 1;
+    x[r] = F32 ? static_cast<const float*>(p.logits)[row + at]
+               : bf16_to_f32(static_cast<const uint16_t*>(p.logits)[row + at]);
+    b[r] = p.bias ? p.bias[at] : 0.f;
+    lo = fminf(lo, b[r]);
+    hi = fmaxf(hi, b[r]);
+    // false for a NaN
+    const bool open = e < p.experts && x[r] > kLow && b[r] > kLow;
+    x[r] = open ? fminf(x[r], FLT_MAX) : kLow;
+  }
+  Choice c;
+  c.experts = p.experts, c.top_k = p.top_k, c.groups = p.groups, c.kept = p.kept, c.group_top = p.group_top;
+  c.size = p.experts / p.groups;
+  c.lanes2 = lanes2;
+  // (every lane reads the last expert's bias at least, so lo <= hi)
+  c.by_logit = !p.bias || all_min<64>(lo) == all_max<64>(hi);
+
+  bool unsure = false;
+  int id = choose<L, V, SIGMOID, float>(c, x, b, lane, unsure);
+  if (__any(unsure)) {
+    bool never = false;
+    id = choose<L, V, SIGMOID, double>(c, x, b, lane, never);
+  }
+
+  const bool mine = lane < p.top_k && id >= 0;
+  float xi = kLow;
+  if (mine)
+    xi = fminf(F32 ? static_cast<const float*>(p.logits)[row + id]
+                   : bf16_to_f32(static_cast<const uint16_t*>(p.logits)[row + id]),
+               FLT_MAX);
+  float w = 0.f;
+  if (p.renormalize) {
+    // s / sum s with a common factor taken out, so that small scores do not
+    // vanish: exp(x) / (1 + exp(x)) below 0 (times exp(-top) where every
+    // chosen logit is below 0)
+    const float top = all_max<L>(xi);
+    if (SIGMOID) {
+      const float shift = fminf(top, 0.f);
+      w = xi > 0.f ? 1.f / (1.f + expf(-xi)) : expf(xi - shift) / (1.f + expf(xi));
+    } else {
+      w = expf(xi - top);
+    }
+    if (!mine) w = 0.f;
+    const float total = all_sum<L>(w);
+    w = mine ? w / total * p.scale : 0.f;
+  } else if (SIGMOID) {
+    w = mine ? p.scale / (1.f + expf(-xi)) : 0.f;
+  } else {
+    float m = x[0];
+#pragma unroll
+    for (int r = 1; r < V; ++r) m = fmaxf(m, x[r]);
+    m = all_max<L>(m);
+    float z = 0.f;
+#pragma unroll
+    for (int r = 0; r < V; ++r) z += x[r] > kLow ? expf(x[r] - m) : 0.f;
+    z = all_sum<L>(z);
+    w = mine ? expf(xi - m) / z * p.scale : 0.f;
+  }
+  if (live && lane < p.top_k) {
+    p.weights[token * p.ldw + lane] = w;
+    p.ids[token * p.ldi + lane] = id;
+  }
+}
+
+template <int L, int V>
+hipError_t launch_lv(const RouteArgs& p, bool f32, bool sigmoid, hipStream_t stream) {
+  const int size = p.experts / p.groups;
+  int lanes2 = -1;
+  if (size % V == 0)
+    for (int n = 0; (1 << n) <= L; ++n)
+      if (size == V << n) lanes2 = n;
+  const dim3 grid((unsigned)((p.tokens + 256 / L - 1) / (256 / L)));
+  if (sigmoid && f32)
+    moe_route_kernel<L, V, true, true><<<grid, 256, 0, stream>>>(p, lanes2);
+  else if (sigmoid)
+    moe_route_kernel<L, V, true, false><<<grid, 256, 0, stream>>>(p, lanes2);
+  else if (f32)
+    moe_route_kernel<L, V, false, true><<<grid, 256, 0, stream>>>(p, lanes2);
+  else
+    moe_route_kernel<L, V, false, false><<<grid, 256, 0, stream>>>(p, lanes2);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_moe_route(const RouteArgs& p, bool f32, bool sigmoid, hipStream_t stream) {
+  // Lane j keeps round j's expert and lane g group g's score, so a token has
+  // at least as many lanes as either.
+  const int need = p.top_k > p.groups ? p.top_k : p.groups;
+  if (need <= 16 && p.experts <= 64) return launch_lv<16, 4>(p, f32, sigmoid, stream);
+  if (need <= 16 && p.experts <= 128) return launch_lv<16, 8>(p, f32, sigmoid, stream);
+  if (need <= 16 && p.experts <= 256) return launch_lv<16, 16>(p, f32, sigmoid, stream);
+  if (p.experts <= 256) return launch_lv<64, 4>(p, f32, sigmoid, stream);
+  return launch_lv<64, 16>(p, f32, sigmoid, stream);
+}
+
+}  // namespace mxfp4

@@ -135,6 +135,23 @@ __device__ __forceinline__ int4 quant_block32(const int4 (&v)[4], uint32_t& b) {
   return c;
 }
 
+// The activations of an epilogue (MXFP4_ACT_* of the C ABI), in fp32.  The
+// sigmoid forms divide through the power and reciprocal instructions (an ulp
+// each); gelu's tail is taken from erfc, which keeps its relative precision.
+enum { kActNone = 0, kActSilu = 1, kActGelu = 2, kActGeluTanh = 3, kActRelu = 4 };
+__device__ __forceinline__ float sigmoid_f32(float v) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * v));
+}
+__device__ __forceinline__ float activate(float v, int act) {
+  switch (act) {
+    case kActSilu: return v * sigmoid_f32(v);
+    case kActGelu: return 0.5f * v * erfcf(-0.70710678118654752440f * v);
+    case kActGeluTanh: return v * sigmoid_f32(1.59576912160573071176f * v * (1.f + 0.044715f * v * v));
+    case kActRelu: return v > 0.f ? v : (v != v ? v : 0.f);
+    default: return v;
+  }
+}
+
 // Byte offset of scale (row r, block c) in the GEMM scale layout with G groups.
 __device__ __forceinline__ uint32_t gemm_scale_offset(uint32_t r, uint32_t c, uint32_t G) {
   uint32_t t = c >> 2, kb = c & 3, g = t >> 2, j = t & 3;

@@ -88,6 +88,20 @@ hipError_t launch_preshuffle_strided(const void* w_fp4, int64_t ldw, const void*
                                      int64_t lds, int64_t batch, int64_t N, int64_t K,
                                      void* w_out, void* ws_out, hipStream_t stream);
 
+// The epilogue of mxfp4_linear_act over fp32 rows [M, N] (bias added): the
+// activation, the gate and the residual, rounded once into out.
+struct EpilogueArgs {
+  const float* y;
+  int M, N;  // N: columns of y
+  int act, gated;
+  const uint16_t* residual;  // bf16 [M, N or N / 2] or nullptr
+  int64_t ldr;
+  void* out;
+  int64_t ldo;
+  int out_f32;
+};
+hipError_t launch_epilogue(const EpilogueArgs& p, hipStream_t stream);
+
 // mxfp4_linear's steps behind its C entry points (csrc/api.hip): the host
 // argument checks (everything but the workspace), the activation workspace
 // bytes without the large-M GEMM's split part (0 where the quantisation is

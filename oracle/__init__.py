@@ -37,6 +37,8 @@ Modules:
   per-element tolerance term sum |a_i * b_i|.
 * :mod:`oracle.attention` -- latent attention in fp64 (cache write, absorbed
   attention with and without a shared prefix, prompts).
+* :mod:`oracle.feedforward` -- routing, the experts' products and the linear
+  with an epilogue, in fp64, with the bounds their kernels are held to.
 
 Parity status per function is stated in each module header.  One quantity is
 "parity unpinned": the internal precision of the hardware's scaled FP4 dot
@@ -44,4 +46,4 @@ product, which is not a function of this oracle and is only measured against
 the tolerance.
 """
 
-from . import attention, formats, quant, layout, linalg  # noqa: F401
+from . import attention, feedforward, formats, quant, layout, linalg  # noqa: F401
