@@ -69,6 +69,10 @@ bool prequant_permute(int64_t M, int64_t N, int64_t K) {
 }
 
 hipError_t launch_gemm_path(int path, const GemmArgs& p, hipStream_t s) {
+  if (p.epilogue)
+    return path == 1   ? launch_gemm_decode_act(p, s)
+           : path == 3 ? launch_gemm_decode_rows_act(p, s)
+                       : launch_gemm_prefill(p, s);
   return path == 1 ? launch_gemm_decode(p, s) : path == 3 ? launch_gemm_decode_rows(p, s) : launch_gemm_prefill(p, s);
 }
 
@@ -144,10 +148,9 @@ int linear_check(const void* x, int64_t ldx, const void* w_pre, const void* ws_p
   return MXFP4_OK;
 }
 
-int linear_run(const void* x, int64_t ldx, const void* w_pre, const void* ws_pre, const void* bias,
-               void* out, int64_t ldo, int out_dtype, int64_t M, int64_t N, int64_t K, void* workspace,
-               size_t workspace_bytes, bool split, int cus, hipStream_t s) {
-  GemmArgs p{};
+static int linear_steps(GemmArgs p, const void* x, int64_t ldx, const void* w_pre, const void* ws_pre,
+                        const void* bias, void* out, int64_t ldo, int out_dtype, int64_t M, int64_t N, int64_t K,
+                        void* workspace, size_t workspace_bytes, bool split, int cus, hipStream_t s) {
   p.cus = cus;
   p.w = (const uint8_t*)w_pre;
   p.ws = (const uint8_t*)ws_pre;
@@ -162,18 +165,19 @@ int linear_run(const void* x, int64_t ldx, const void* w_pre, const void* ws_pre
   p.G = (int)cdiv(p.Kt, 4);
   p.Ns = (int)cdiv(N, 16);
   const int64_t x_bytes = ((M - 1) * ldx + K) * 2;
-  if (linear_persist_applies((int)M, (int)K, x_bytes) && linear_persist_pays((int)M, (int)N, (int)K, cus)) {
+  if (!p.gated && linear_persist_applies((int)M, (int)K, x_bytes) &&
+      linear_persist_pays((int)M, (int)N, (int)K, cus)) {
     // quantised inside the persistent form: the workspace stays untouched
     p.x = (const uint16_t*)x;
     p.ldx = (int)ldx;
     p.x_bytes = (uint32_t)x_bytes;
-    return launched(launch_linear_persist(p, s));
+    return launched(p.epilogue ? launch_linear_persist_act(p, s) : launch_linear_persist(p, s));
   }
   if (linear_fused(M, N, K)) {
     p.x = (const uint16_t*)x;
     p.ldx = (int)ldx;
     p.x_bytes = (uint32_t)(((M - 1) * ldx + K) * 2);
-    return launched(launch_linear_decode(p, s));
+    return launched(p.epilogue ? launch_linear_decode_act(p, s) : launch_linear_decode(p, s));
   }
   // Larger M: quantise into the workspace, then the GEMM kernel for that M
   // (the large-M kernel's split schedule in the rest of the workspace, when
@@ -189,6 +193,20 @@ int linear_run(const void* x, int64_t ldx, const void* w_pre, const void* ws_pre
     p.work_bytes = workspace_bytes - act_gemm_offset(M, K);
   }
   return launched(launch_gemm_path(M <= 64 ? 1 : gemm_path(M, N), p, s));
+}
+
+int linear_run(const void* x, int64_t ldx, const void* w_pre, const void* ws_pre, const void* bias,
+               void* out, int64_t ldo, int out_dtype, int64_t M, int64_t N, int64_t K, void* workspace,
+               size_t workspace_bytes, bool split, int cus, hipStream_t s) {
+  return linear_steps(GemmArgs{}, x, ldx, w_pre, ws_pre, bias, out, ldo, out_dtype, M, N, K, workspace,
+                      workspace_bytes, split, cus, s);
+}
+
+int linear_run_act(const GemmArgs& epi, const void* x, int64_t ldx, const void* w_pre, const void* ws_pre,
+                   const void* bias, void* out, int64_t ldo, int out_dtype, int64_t M, int64_t N, int64_t K,
+                   void* workspace, size_t workspace_bytes, int cus, hipStream_t s) {
+  return linear_steps(epi, x, ldx, w_pre, ws_pre, bias, out, ldo, out_dtype, M, N, K, workspace, workspace_bytes,
+                      true, cus, s);
 }
 
 }  // namespace mxfp4

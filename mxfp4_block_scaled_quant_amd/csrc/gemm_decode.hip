@@ -25,15 +25,39 @@
 #include "mxfp4_device.h"
 #include "mxfp4_launch.h"
 
+// This source built again with MXFP4_DECODE_ACT = 1 holds the same kernels with
+// an activation, a gate and a residual in their epilogue.
+#ifndef MXFP4_DECODE_ACT
+#define MXFP4_DECODE_ACT 0
+#endif
+#if MXFP4_DECODE_ACT
+#define gemm_decode_kernel gemm_decode_act_kernel
+#define gemm_decode_persist_kernel gemm_decode_persist_act_kernel
+#define linear_decode_kernel linear_decode_act_kernel
+#define launch_gemm_decode launch_gemm_decode_act
+#define launch_gemm_decode_rows launch_gemm_decode_rows_act
+#define launch_linear_decode launch_linear_decode_act
+#define launch_linear_persist launch_linear_persist_act
+#endif
+
 namespace mxfp4 {
 
 namespace {
 
+constexpr bool kAct = MXFP4_DECODE_ACT != 0;
 constexpr int kAuxNT = 2;  // cache policy bits of a buffer load: non-temporal
 
 template <int SEL>
 __device__ __forceinline__ v4f mfma_sel(const int4& a, const int4& b, uint32_t sa, uint32_t sb, v4f acc) {
   return mfma_fp4<SEL, SEL>(a, b, sa, sb, acc);
+}
+
+// Weight strip j of the workgroup (or step) that begins at strip s0.  With a
+// gate a step is one output strip: strip s0 / 2 of the weight's first half
+// and the one beside it of the second.
+template <bool GATED>
+__device__ __forceinline__ int strip_of(const GemmArgs& p, int s0, int j) {
+  return GATED ? (s0 >> 1) + (j ? p.Ns >> 1 : 0) : s0 + j;
 }
 
 }  // namespace
@@ -56,20 +80,86 @@ __device__ __forceinline__ v4f mfma_sel(const int4& a, const int4& b, uint32_t s
 // launch without bias).  A buffer load, so that no branch guards it (a
 // guarded load gets its wait at the end of the branch, before the weight
 // loads are even issued).
-template <int NS>
+template <int NS, bool GATED = false>
 __device__ __forceinline__ void load_bias(const GemmArgs& p, int s0, uint32_t (&bb)[NS]) {
   const int lane = threadIdx.x & 63;
   const auto rb = make_rsrc(p.bias, p.bias ? (uint32_t)p.N * 2u : 0u);
 #pragma unroll
   for (int j = 0; j < NS; ++j) {
-    const uint32_t n = (uint32_t)((s0 + j) * 16 + (lane & 15));
+    const uint32_t n = (uint32_t)(strip_of<GATED>(p, s0, j) * 16 + (lane & 15));
     bb[j] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rb, n < (uint32_t)p.N ? n * 2u : kOOB, 0, 0);
   }
 }
 
-template <int MT, int NS, int MAXW>
+// reduce_store with an epilogue: a thread has the sums of an output (with a
+// gate, of its gate and of what that multiplies), activates them and adds
+// the residual, which it asked for before the sums (the next output's while
+// it finishes one).
+template <int MT, int NS, int MAXW, bool GATED>
+__device__ __forceinline__ void reduce_store_act(float* red, const v4f (&acc)[MT][NS], const GemmArgs& p, int s0,
+                                                 const uint32_t (&bb)[NS]) {
+  static_assert(!GATED || NS == 2, "a gate and its factor");
+  constexpr int NO = GATED ? 1 : NS;  // output strips
+  const int lane = threadIdx.x & 63;
+  const int wv = threadIdx.x >> 6;
+  const int KW = blockDim.x >> 6;
+  const int cols = GATED ? p.N >> 1 : p.N;
+  const int o0 = GATED ? s0 >> 1 : s0;
+  const auto row_of = [&](int sl) { return (sl >> 2) / NO * 16 + 4 * (lane >> 4) + (sl & 3); };
+  const auto col_of = [&](int sl) { return (o0 + (sl >> 2) % NO) * 16 + (lane & 15); };
+  const auto residual_of = [&](int sl) -> uint16_t {
+    const int m = row_of(sl), n = col_of(sl);
+    return p.res && sl < MT * NO * 4 && m < p.M && n < cols ? p.res[(int64_t)m * p.ldr + n] : (uint16_t)0;
+  };
+  uint16_t next = residual_of(wv);
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) red[(((i * NS + j) * 4 + r) * MAXW + wv) * 64 + lane] = acc[i][j][r];
+  __syncthreads();
+  const auto sum = [&](int tile, int r) {
+    const float* src = red + (tile * 4 + r) * MAXW * 64 + lane;
+    float part[MAXW];
+#pragma unroll
+    for (int w = 0; w < MAXW; ++w) part[w] = src[w * 64];
+    float v = part[0];
+#pragma unroll
+    for (int w = 1; w < MAXW; ++w)
+      if (w < KW) v += part[w];
+    return v;
+  };
+  for (int sl = wv; sl < MT * NO * 4; sl += KW) {
+    const float res = bf16_to_f32(next);
+    next = residual_of(sl + KW);
+    const int i = (sl >> 2) / NO, j = (sl >> 2) % NO, r = sl & 3;
+    const int m = row_of(sl), n = col_of(sl);
+    float v = sum(i * NS + j, r);
+    if (p.bias) v += bf16_to_f32((uint16_t)bb[j]);
+    v = activate(v, p.act);
+    if constexpr (GATED) {
+      float u = sum(i * NS + 1, r);
+      if (p.bias) u += bf16_to_f32((uint16_t)bb[1]);
+      v *= u;
+    }
+    v += res;
+    if (m < p.M && n < cols) {
+      if (p.out_f32)
+        reinterpret_cast<float*>(p.out)[(int64_t)m * p.ldo + n] = v;
+      else
+        reinterpret_cast<uint16_t*>(p.out)[(int64_t)m * p.ldo + n] = f32_to_bf16_rne(v);
+    }
+  }
+}
+
+template <int MT, int NS, int MAXW, bool GATED = false>
 __device__ __forceinline__ void reduce_store(float* red, const v4f (&acc)[MT][NS], const GemmArgs& p, int s0,
                                              const uint32_t (&bb)[NS]) {
+  if constexpr (kAct) {
+    reduce_store_act<MT, NS, MAXW, GATED>(red, acc, p, s0, bb);
+    return;
+  }
   const int lane = threadIdx.x & 63;
   const int wv = threadIdx.x >> 6;
   const int KW = blockDim.x >> 6;
@@ -168,7 +258,7 @@ __device__ __forceinline__ void reduce_store_fp4(v4f* red, const v4f (&acc)[MT][
   }
 }
 
-template <int MT, int NS, int GPR, int MAXW, int ASRC, bool HOLDA>
+template <int MT, int NS, int GPR, int MAXW, int ASRC, bool HOLDA, bool GATED = false>
 __global__ __launch_bounds__(64 * MAXW) void gemm_decode_kernel(GemmArgs p, int gpw) {
   constexpr bool AROW = ASRC == kASrcRow16 || ASRC == kASrcRow8;
   static_assert(ASRC != kASrcBf16, "bf16 activations: the persistent form only");
@@ -204,7 +294,7 @@ __global__ __launch_bounds__(64 * MAXW) void gemm_decode_kernel(GemmArgs p, int 
       const bool tv = (gr + u / 4) < g_end && t < p.Kt;
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
-        const int s = s0 + j;
+        const int s = strip_of<GATED>(p, s0, j);
         const uint32_t off = (tv && s < p.Ns) ? (uint32_t)((s * p.Kt + t) * 1024 + lane * 16) : kOOB;
         bf[u][j] = __builtin_bit_cast(int4, __builtin_amdgcn_raw_buffer_load_b128(rw, off, 0, kAuxNT));
       }
@@ -215,7 +305,7 @@ __global__ __launch_bounds__(64 * MAXW) void gemm_decode_kernel(GemmArgs p, int 
       const bool gv = g < g_end;
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
-        const int s = s0 + j;
+        const int s = strip_of<GATED>(p, s0, j);
         sb[q][j] = buf_load4(rws, (gv && s < p.Ns) ? (uint32_t)((s * p.G + g) * 256 + lane * 4) : kOOB);
       }
 #pragma unroll
@@ -280,7 +370,7 @@ __global__ __launch_bounds__(64 * MAXW) void gemm_decode_kernel(GemmArgs p, int 
     // MFMAs' waits do not include it; row-major operands leave no registers
     // for it (two strips and two groups per round spill), so there it is
     // loaded after the loop
-    if constexpr (!AROW) load_bias<NS>(p, s0, bb);
+    if constexpr (!AROW) load_bias<NS, GATED>(p, s0, bb);
     // Keep every load of the round ahead of the first wait: without this the
     // scheduler interleaves loads and MFMAs to save registers, which turns one
     // memory round trip into several.
@@ -301,14 +391,14 @@ __global__ __launch_bounds__(64 * MAXW) void gemm_decode_kernel(GemmArgs p, int 
         }
   }
 
-  if constexpr (AROW) load_bias<NS>(p, s0, bb);
-  if constexpr (NS == 2) {
+  if constexpr (AROW) load_bias<NS, GATED>(p, s0, bb);
+  if constexpr (NS == 2 && !kAct) {
     if (p.out_fp4) {
       reduce_store_fp4<MT>(red, acc, p, s0, bb);
       return;
     }
   }
-  reduce_store<MT, NS, MAXW>(reinterpret_cast<float*>(red), acc, p, s0, bb);
+  reduce_store<MT, NS, MAXW, GATED>(reinterpret_cast<float*>(red), acc, p, s0, bb);
 }
 
 // Persistent form, for more rows (each workgroup of the form above re-reads
@@ -328,12 +418,12 @@ __global__ __launch_bounds__(64 * MAXW) void gemm_decode_kernel(GemmArgs p, int 
 // strips (one 1x32 block per row), walked the same way, and
 // reduce_store_fp4 reduces it in one area: its second barrier already
 // orders every read of a step before the next step's writes.
-template <int MT, int MAXW, int D, int ASRC, int NS = 1, int GPW = 1>
+template <int MT, int MAXW, int D, int ASRC, int NS = 1, int GPW = 1, bool GATED = false>
 __global__ __launch_bounds__(64 * MAXW) void gemm_decode_persist_kernel(GemmArgs p) {
   constexpr bool AROW = ASRC == kASrcRow16 || ASRC == kASrcRow8;
   static_assert(GPW == 1 || (GPW == 2 && ASRC == kASrcGemm && NS == 1), "two groups per wave: GEMM layout, one strip");
   extern __shared__ v4f red[];
-  constexpr size_t kRedFloats = reduce_lds_bytes<MT, 1, MAXW>() / sizeof(float);
+  constexpr size_t kRedFloats = reduce_lds_bytes<MT, GATED ? 2 : 1, MAXW>() / sizeof(float);
   const int lane = threadIdx.x & 63;
   const int g = (threadIdx.x >> 6) * GPW;  // this wave's (first) scale group
   const bool gv = g < p.G;
@@ -428,7 +518,7 @@ __global__ __launch_bounds__(64 * MAXW) void gemm_decode_persist_kernel(GemmArgs
     for (int j = 0; j < NS; ++j)
 #pragma unroll
       for (int q = 0; q < GPW; ++q) {
-        const int s = s0 + j;
+        const int s = strip_of<GATED>(p, s0, j);
         const bool sv = k < nk && g + q < p.G && s < p.Ns;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -438,7 +528,7 @@ __global__ __launch_bounds__(64 * MAXW) void gemm_decode_persist_kernel(GemmArgs
         }
         sc[j][q] = buf_load4(rws, sv ? (uint32_t)((s * p.G + g + q) * 256 + lane * 4) : kOOB);
       }
-    load_bias<NS>(p, k < nk ? s0 : p.Ns, bias);
+    load_bias<NS, GATED>(p, k < nk ? s0 : p.Ns, bias);
   };
 #pragma unroll
   for (int d = 0; d < D; ++d) issue(d, bf[d], sb[d], bb[d]);
@@ -505,7 +595,9 @@ __global__ __launch_bounds__(64 * MAXW) void gemm_decode_persist_kernel(GemmArgs
       for (int j = 0; j < NS; ++j) bias[j] = bb[d][j];
       issue(k + D, bf[d], sb[d], bb[d]);
       const int s0 = ((int)blockIdx.x + k * (int)gridDim.x) * NS;
-      if constexpr (NS == 2)
+      if constexpr (GATED)
+        reduce_store<MT, NS, MAXW, true>(reinterpret_cast<float*>(red) + (size_t)(k & 1) * kRedFloats, acc, p, s0, bias);
+      else if constexpr (NS == 2)
         reduce_store_fp4<MT>(red, acc, p, s0, bias);
       else
         reduce_store<MT, 1, MAXW>(reinterpret_cast<float*>(red) + (size_t)(k & 1) * kRedFloats, acc, p, s0, bias);
@@ -534,7 +626,7 @@ __device__ __forceinline__ uint32_t lane_permute(uint32_t src_lane, uint32_t v) 
   return (uint32_t)__builtin_amdgcn_ds_bpermute((int)(src_lane * 4u), (int)v);
 }
 
-template <int NS, int GPR, int MAXW>
+template <int NS, int GPR, int MAXW, bool GATED = false>
 __global__ __launch_bounds__(64 * MAXW) void linear_decode_kernel(GemmArgs p, int gpw) {
   extern __shared__ v4f red[];  // reduce_store's partials
   constexpr int STEPS = 4 * GPR;
@@ -562,7 +654,7 @@ __global__ __launch_bounds__(64 * MAXW) void linear_decode_kernel(GemmArgs p, in
 #pragma unroll
   for (int j = 0; j < NS; ++j) acc[0][j] = (v4f){0.f, 0.f, 0.f, 0.f};
   uint32_t bb[NS];
-  load_bias<NS>(p, s0, bb);
+  load_bias<NS, GATED>(p, s0, bb);
 
   const int g_begin = wv * gpw;
   const int g_end = min(g_begin + gpw, p.G);
@@ -584,7 +676,7 @@ __global__ __launch_bounds__(64 * MAXW) void linear_decode_kernel(GemmArgs p, in
       const bool tv = (gr + u / 4) < g_end && t < p.Kt;
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
-        const int s = s0 + j;
+        const int s = strip_of<GATED>(p, s0, j);
         const uint32_t off = (tv && s < p.Ns) ? (uint32_t)((s * p.Kt + t) * 1024 + lane * 16) : kOOB;
         bf[u][j] = __builtin_bit_cast(int4, __builtin_amdgcn_raw_buffer_load_b128(rw, off, 0, kAuxNT));
       }
@@ -594,7 +686,7 @@ __global__ __launch_bounds__(64 * MAXW) void linear_decode_kernel(GemmArgs p, in
       const int g = gr + q;
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
-        const int s = s0 + j;
+        const int s = strip_of<GATED>(p, s0, j);
         sb[q][j] = buf_load4(rws, (g < g_end && s < p.Ns) ? (uint32_t)((s * p.G + g) * 256 + lane * 4) : kOOB);
       }
     }
@@ -634,7 +726,7 @@ __global__ __launch_bounds__(64 * MAXW) void linear_decode_kernel(GemmArgs p, in
       }
   }
 
-  reduce_store<1, NS, MAXW>(reinterpret_cast<float*>(red), acc, p, s0, bb);
+  reduce_store<1, NS, MAXW, GATED>(reinterpret_cast<float*>(red), acc, p, s0, bb);
 }
 
 // HOLDA: row-major activation loads wait for the round's weights (one group
@@ -649,7 +741,17 @@ static hipError_t launch_decode_t(const GemmArgs& p, int kw, int gpw, hipStream_
   // round (launch_decode_mt gives them one: two strips of two groups spill
   // with the 16-byte scale loads), so those forms are not built.
   constexpr bool kRowForms = !(MT == 1 && GPR == 2);
-  if constexpr (kRowForms) {
+  if constexpr (kAct) {
+    // (the epilogue's calls quantise bf16 rows into the GEMM layout)
+    if (p.a_rowmajor || p.out_fp4) return hipErrorInvalidValue;
+    if constexpr (NS == 2) {
+      if (p.gated) {
+        gemm_decode_kernel<MT, NS, GPR, MAXW, kASrcGemm, false, true><<<grid, 64 * kw, lds, stream>>>(p, gpw);
+        return hipGetLastError();
+      }
+    }
+    gemm_decode_kernel<MT, NS, GPR, MAXW, kASrcGemm, false><<<grid, 64 * kw, lds, stream>>>(p, gpw);
+  } else if constexpr (kRowForms) {
     if (p.a_rowmajor && p.scales_vec)
       gemm_decode_kernel<MT, NS, GPR, MAXW, kASrcRow16, HOLDA><<<grid, 64 * kw, lds, stream>>>(p, gpw);
     else if (p.a_rowmajor)
@@ -755,7 +857,11 @@ static hipError_t launch_decode_persist(const GemmArgs& p, int kw, hipStream_t s
   constexpr int D = MT == 4 ? 3 : 4;
   const int grid = p.Ns < p.cus ? p.Ns : p.cus;
   const size_t lds = 2 * reduce_lds_bytes<MT, 1, MAXW>();
-  if (p.a_rowmajor && p.scales_vec)
+  if constexpr (kAct) {
+    if (p.a_rowmajor) return hipErrorInvalidValue;
+    gemm_decode_persist_kernel<MT, MAXW, D, kASrcGemm><<<grid, 64 * kw, lds, stream>>>(p);
+    return hipGetLastError();
+  } else if (p.a_rowmajor && p.scales_vec)
     gemm_decode_persist_kernel<MT, MAXW, D, kASrcRow16><<<grid, 64 * kw, lds, stream>>>(p);
   else if (p.a_rowmajor)
     gemm_decode_persist_kernel<MT, MAXW, D, kASrcRow8><<<grid, 64 * kw, lds, stream>>>(p);
@@ -802,6 +908,7 @@ static hipError_t launch_decode_persist2(const GemmArgs& p, hipStream_t stream) 
   return hipGetLastError();
 }
 
+#if !MXFP4_DECODE_ACT
 // MXFP4 output in the persistent form: steps of two strips (one 1x32
 // block per row), one reduction area (two barriers per step).
 template <int MT>
@@ -814,6 +921,38 @@ static hipError_t launch_decode_persist_fp4(const GemmArgs& p, int kw, hipStream
   return hipGetLastError();
 }
 
+#else
+// A gate in the persistent form: steps of one output strip, two of the
+// weight's.
+template <int MT>
+static hipError_t launch_decode_persist_gated(const GemmArgs& p, int kw, hipStream_t stream) {
+  constexpr int D = 1;  // steps in flight per wave (two strips each)
+  const int Nu = p.Ns / 2;
+  const int grid = Nu < p.cus ? Nu : p.cus;
+  const size_t lds = 2 * reduce_lds_bytes<MT, 2, 12>();
+  gemm_decode_persist_kernel<MT, 12, D, kASrcGemm, 2, 1, true><<<grid, 64 * kw, lds, stream>>>(p);
+  return hipGetLastError();
+}
+#endif
+
+#if MXFP4_DECODE_ACT
+// The launch shape with a gate: a workgroup always holds two strips, and K is
+// split as without one.
+template <int MT>
+static hipError_t launch_decode_gated(const GemmArgs& p, int kw, int gpw, hipStream_t stream) {
+  constexpr int MAXW = MT == 1 ? 16 : MT == 4 ? 12 : 8;
+  const int ov = get_gemm_path_override();
+  {
+    if (p.G <= 12 && (ov == 7 || (ov != 8 && decode_persist_fp4_pays(p.M, p.Ns, p.cus, p.G))))
+      return launch_decode_persist_gated<MT>(p, p.G, stream);
+  }
+  if constexpr (MT == 1) {
+    if (gpw >= 2 && p.Ns < 2 * p.cus) return launch_decode_t<MT, 2, 2, MAXW>(p, kw, gpw, stream);
+  }
+  return launch_decode_t<MT, 2, 1, MAXW, false>(p, kw, gpw, stream);
+}
+#endif
+
 template <int MT>
 static hipError_t launch_decode_mt(const GemmArgs& p, hipStream_t stream) {
   constexpr int MAXW = MT == 1 ? 16 : MT == 4 ? 12 : 8;
@@ -824,6 +963,9 @@ static hipError_t launch_decode_mt(const GemmArgs& p, hipStream_t stream) {
   const bool three = MT == 1 && p.M > 8 && p.G > 28 && p.G <= 32 && p.Ns >= 4 * p.cus;
   const int gpw = three ? (p.G + 11) / 12 : (p.G + MAXW - 1) / MAXW;
   const int kw = (p.G + gpw - 1) / gpw;
+#if MXFP4_DECODE_ACT
+  if (p.gated) return launch_decode_gated<MT>(p, kw, gpw, stream);
+#endif
   // persistent form: one group per wave, bf16 / fp32 output, activations in
   // the GEMM layout or row-major (path 7 of the test hook forces it where it
   // applies, 8 keeps the streaming form); the same K split as the streaming
@@ -843,8 +985,10 @@ static hipError_t launch_decode_mt(const GemmArgs& p, hipStream_t stream) {
   }
   // MXFP4 output (GEMM-layout activations): the same form in steps of two
   // strips
+#if !MXFP4_DECODE_ACT
   if (p.out_fp4 && !p.a_rowmajor && p.G <= 12 && (ov == 7 || (ov != 8 && decode_persist_fp4_pays(p.M, p.Ns, p.cus, p.G))))
     return launch_decode_persist_fp4<MT>(p, p.G, stream);
+#endif
   // one strip per workgroup never with MXFP4 output (a workgroup encodes
   // whole 32-column blocks)
   const bool one_round = p.Ns <= p.cus && !p.out_fp4;
@@ -923,6 +1067,7 @@ hipError_t launch_gemm_decode_rows(const GemmArgs& p0, hipStream_t stream) {
       p.a = p0.a + (size_t)(r0 / 16) * p0.Kt * 1024;
       p.as = p0.as + (size_t)(r0 / 16) * p0.G * 256;
     }
+    if (p0.res) p.res = p0.res + (size_t)r0 * p0.ldr;
     if (p0.out_fp4) {
       p.out = (uint8_t*)p0.out + (size_t)r0 * p0.ldo;
       p.out_scales = p0.out_scales + (size_t)r0 * p0.ldos;
@@ -940,10 +1085,17 @@ template <int NS, int GPR>
 static hipError_t launch_linear_t(const GemmArgs& p, int kw, int gpw, hipStream_t stream) {
   const dim3 grid((unsigned)((p.Ns + NS - 1) / NS));
   const size_t lds = reduce_lds_bytes<1, NS, 16>();
+  if constexpr (kAct && NS == 2) {
+    if (p.gated) {
+      linear_decode_kernel<NS, GPR, 16, true><<<grid, 64 * kw, lds, stream>>>(p, gpw);
+      return hipGetLastError();
+    }
+  }
   linear_decode_kernel<NS, GPR, 16><<<grid, 64 * kw, lds, stream>>>(p, gpw);
   return hipGetLastError();
 }
 
+#if !MXFP4_DECODE_ACT
 bool linear_fused_pays(int M, int N, int K) {
   // Every workgroup re-reads and re-encodes the bf16 rows, so the fused
   // call beats quantisation + GEMM (about 2 us for the extra launch) only
@@ -968,8 +1120,16 @@ bool linear_fused_pays(int M, int N, int K) {
   return K <= 16384 && (M == 2 || N <= 4096);
 }
 
+#endif
+
 hipError_t launch_linear_decode(const GemmArgs& p, hipStream_t stream) {
   if (p.M > kFusedRows) return hipErrorInvalidValue;
+#if MXFP4_DECODE_ACT
+  if (p.gated) {
+    const int gpw = (p.G + 15) / 16;
+    return launch_linear_t<2, 1>(p, (p.G + gpw - 1) / gpw, gpw, stream);
+  }
+#endif
   // Up to 8192-wide K: at most 16 waves of one group each, one strip per
   // workgroup when strips are plentiful or all fit in one round of compute
   // units (N = 4096, K = 5120, M = 1 / 4: 5.01 / 5.56 -> 4.41 / 4.88 us;
@@ -1013,6 +1173,7 @@ hipError_t launch_linear_decode(const GemmArgs& p, hipStream_t stream) {
 // the persistent GEMM, so the same bits.  (Three or four tiles of encoded
 // operands beside the weight ring spill at the 12-wave register budget, so
 // those forms are not built.)
+#if !MXFP4_DECODE_ACT
 bool linear_persist_applies(int M, int K, int64_t x_bytes) {
   const int G = (K / 32 + 15) / 16;
   return M >= 1 && M <= 32 && G <= 12 && x_bytes <= (int64_t)0x7FFFFFFF;  // 31-bit buffer offsets
@@ -1037,6 +1198,8 @@ bool linear_persist_pays(int M, int N, int K, int cus) {
   return M >= 2 && M <= 4 && G >= 10 && Ns >= 6 * cus;
 }
 
+#endif
+
 template <int MT, int D>
 static void launch_linear_persist_mt(const GemmArgs& p, hipStream_t stream) {
   const int grid = p.Ns < p.cus ? p.Ns : p.cus;
@@ -1044,7 +1207,7 @@ static void launch_linear_persist_mt(const GemmArgs& p, hipStream_t stream) {
 }
 
 hipError_t launch_linear_persist(const GemmArgs& p, hipStream_t stream) {
-  if (p.M < 1 || p.M > 32 || p.G > 12) return hipErrorInvalidValue;
+  if (p.M < 1 || p.M > 32 || p.G > 12 || (kAct && p.gated)) return hipErrorInvalidValue;
   // ring depth: as the GEMM-layout form at one row tile; at two, the
   // encoding's registers are live beside the ring, which holds one step
   if (p.M <= 16)

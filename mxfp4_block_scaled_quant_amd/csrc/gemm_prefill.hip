@@ -49,18 +49,35 @@
 //
 // Every register counts: at two waves per SIMD a wave has 256 registers, 128
 // of them accumulators and 64 operand fragments (256 wide).
+#include "moe_launch.h"
 #include "mxfp4_device.h"
 #include "mxfp4_launch.h"
 
 #ifndef MXFP4_PREFILL_BN
 #define MXFP4_PREFILL_BN 256
 #endif
-#if MXFP4_PREFILL_BN == 256
-#define MXFP4_PREFILL_KERNEL gemm_prefill_kernel
-#define MXFP4_PREFILL_TILES launch_prefill_tiles_256
+// What this build of the source is for: 0 = the GEMM, 1 = the GEMM with an
+// activation, a gate and a residual in its epilogue, 2 = the experts'
+// products (row tiles from the list of a plan, each with its expert's weight).
+#ifndef MXFP4_PREFILL_FORM
+#define MXFP4_PREFILL_FORM 0
+#endif
+#define MXFP4_CAT_(a, b, c) a##b##c
+#define MXFP4_CAT(a, b, c) MXFP4_CAT_(a, b, c)
+#if MXFP4_PREFILL_FORM == 0
+#define MXFP4_PREFILL_STEM gemm_prefill
+#define MXFP4_PREFILL_TILES MXFP4_CAT(launch_prefill_tiles_, MXFP4_PREFILL_BN, )
+#elif MXFP4_PREFILL_FORM == 1
+#define MXFP4_PREFILL_STEM gemm_prefill_act
+#define MXFP4_PREFILL_TILES MXFP4_CAT(launch_prefill_act_tiles_, MXFP4_PREFILL_BN, )
 #else
-#define MXFP4_PREFILL_KERNEL gemm_prefill_n128_kernel
-#define MXFP4_PREFILL_TILES launch_prefill_tiles_128
+#define MXFP4_PREFILL_STEM gemm_prefill_experts
+#define MXFP4_PREFILL_TILES MXFP4_CAT(launch_prefill_experts_, MXFP4_PREFILL_BN, )
+#endif
+#if MXFP4_PREFILL_BN == 256
+#define MXFP4_PREFILL_KERNEL MXFP4_CAT(MXFP4_PREFILL_STEM, _kernel, )
+#else
+#define MXFP4_PREFILL_KERNEL MXFP4_CAT(MXFP4_PREFILL_STEM, _n128, _kernel)
 #endif
 
 namespace mxfp4 {
@@ -148,32 +165,67 @@ __device__ __forceinline__ v4f mfma_fp4v(v4i a, v4i b, uint32_t sa, uint32_t sb,
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, acc, 4, 4, SEL, (int)sa, SEL, (int)sb);
 }
 
+// What a kernel's MODE adds to its output mode (0 .. 4, OutMode below):
+//  kModeAct    the activation and the residual in the epilogue
+//  kModeGated  the weight's first half of strips is a gate, the second what it
+//              multiplies: a tile takes both halves of its output columns, so
+//              that a lane holds a gate and its factor (a wave's strips
+//              0 .. kWN/2 - 1 are gates, the others the factors beside them)
+//  kModeGroup  row tiles come from the plan's list, with their experts' weights
+//  kModeRows   (kModeGroup) MXFP4 output in the GEMM layouts
+constexpr int kModeAct = 8, kModeGated = 16, kModeGroup = 32, kModeRows = 64;
+constexpr bool is_act(int mode) { return (mode & kModeAct) != 0; }
+constexpr bool is_gated(int mode) { return (mode & kModeGated) != 0; }
+constexpr bool is_group(int mode) { return (mode & kModeGroup) != 0; }
+constexpr bool is_rows(int mode) { return (mode & kModeRows) != 0; }
+// 16-column output strips of a tile and of a wave.
+template <int MODE>
+constexpr int kOutTilesB = is_gated(MODE) ? kTilesB / 2 : kTilesB;
+template <int MODE>
+constexpr int kOutWN = is_gated(MODE) ? kWN / 2 : kWN;
+
 // One output tile: its first 16-row activation strip and strip count, its
 // first 16-column weight strip and strip count (counts are 0 for an empty
 // tile past the end).  Buffer descriptors are derived from it where a load is
 // issued, after any selection between tiles: a select between descriptors
 // becomes a vector select, which then costs a waterfall loop per load.
 // A work item: the groups [g0, g1) of 4 K-steps of one tile (a slice of a
-// split tile unless that is all G of them).
+// split tile unless that is all G of them).  With a gate s0 and strips count
+// output strips.  kModeGroup: its expert and the end of its rows.
 struct Tile {
   int ms, mstrips, s0, strips;
   int g0, g1;
+  int e, mend;
 };
 
 // Linear tile L (all its groups): tiles run down groups of kGroupM
 // row-tiles, then across columns.
+template <int MODE>
 __device__ __forceinline__ Tile tile_at(const GemmArgs& p, int L, int tiles_m, int tiles_n) {
-  Tile t = {0, 0, 0, 0, 0, 0};
+  Tile t = {0, 0, 0, 0, 0, 0, 0, 0};
   if (L >= tiles_m * tiles_n) return t;
   t.g1 = p.G;
   const int group = L / (kGroupM * tiles_n);
   const int first_m = group * kGroupM;
   const int gm = min(tiles_m - first_m, kGroupM);
   const int r = L % (kGroupM * tiles_n);
-  t.ms = (first_m + r % gm) * kTilesA;
-  t.mstrips = min(kTilesA, ((p.M + 15) >> 4) - t.ms);
-  t.s0 = (r / gm) * kTilesB;
-  t.strips = min(kTilesB, p.Ns - t.s0);
+  if constexpr (is_group(MODE)) {
+    // scalar loads, waited for here: left in flight they would be counted
+    // with the LDS reads of the K loop
+    typedef __attribute__((address_space(4))) const int* words_t;
+    const words_t b = (words_t)(uintptr_t)(p.blocks + (first_m + r % gm));
+    int e = b[0], ms = b[1], rows = b[2];
+    asm volatile("s_waitcnt lgkmcnt(0)" : "+s"(e), "+s"(ms), "+s"(rows));
+    t.e = e;
+    t.ms = ms;
+    t.mstrips = (rows + 15) >> 4;
+    t.mend = ms * 16 + rows;
+  } else {
+    t.ms = (first_m + r % gm) * kTilesA;
+    t.mstrips = min(kTilesA, ((p.M + 15) >> 4) - t.ms);
+  }
+  t.s0 = (r / gm) * kOutTilesB<MODE>;
+  t.strips = min(kOutTilesB<MODE>, (is_gated(MODE) ? p.Ns / 2 : p.Ns) - t.s0);
   return t;
 }
 
@@ -186,16 +238,35 @@ struct Share {
 
 // Groups [g0, g1) of slice j of s: the G groups cut as evenly as whole
 // groups allow.
+template <int MODE>
 __device__ __forceinline__ Tile work_at(const GemmArgs& p, const SkArgs& sk, const Share& s, int i, int tiles_m,
                                         int tiles_n) {
   if (i < s.nsk) {
     const int j = s.slot / sk.r;
-    Tile tl = tile_at(p, s.slot - j * sk.r, tiles_m, tiles_n);
+    Tile tl = tile_at<MODE>(p, s.slot - j * sk.r, tiles_m, tiles_n);
     tl.g0 = j * p.G / sk.s;
     tl.g1 = (j + 1) * p.G / sk.s;
     return tl;
   }
-  return tile_at(p, sk.r + (i - s.nsk) * s.grid + s.slot, tiles_m, tiles_n);
+  return tile_at<MODE>(p, sk.r + (i - s.nsk) * s.grid + s.slot, tiles_m, tiles_n);
+}
+
+// The end of a tile's rows.
+template <int MODE>
+__device__ __forceinline__ int row_end(const GemmArgs& p, const Tile& tl) {
+  return is_group(MODE) ? tl.mend : p.M;
+}
+
+// With a gate, weight unit u of a tile (strip u % kWN of wave column u / kWN)
+// is output strip gate_strip(u) of the tile, in the second half of the
+// weight's strips where u % kWN >= kWN / 2.
+__device__ __forceinline__ int gate_strip(int u) { return u / kWN * (kWN / 2) + u % (kWN / 2); }
+__device__ __forceinline__ int gate_half(int u) { return u % kWN >= kWN / 2 ? 1 : 0; }
+
+// The weight (scales, bias) of a tile's expert.
+template <int MODE, typename T>
+__device__ __forceinline__ const T* expert_of(const T* base, const Tile& tl, int64_t stride) {
+  return is_group(MODE) ? base + tl.e * stride : base;
 }
 
 // This wave's buffer->LDS load of unit q (of its 4) of K-step t of tile
@@ -204,6 +275,7 @@ __device__ __forceinline__ Tile work_at(const GemmArgs& p, const SkArgs& sk, con
 // K-steps); units past the tile's last strip and steps past K get an empty
 // one and load zeros.  The vector offset is the lane's 16 bytes, the step
 // goes in the scalar offset (in range whenever the descriptor is not empty).
+template <int MODE>
 __device__ __forceinline__ void issue_unit(const GemmArgs& p, const Tile& tl, int J, int t, int q, int wv,
                                            uint32_t lane16) {
   // unit gu of the step's kUnits (activation units first): wave wv loads
@@ -213,17 +285,26 @@ __device__ __forceinline__ void issue_unit(const GemmArgs& p, const Tile& tl, in
   const bool is_a = gu < kTilesA;
   const int first = is_a ? tl.ms : tl.s0;
   const int count = t < p.Kt ? (is_a ? tl.mstrips : tl.strips) : 0;
-  const uint8_t* base = is_a ? p.a : p.w;
-  const int u = is_a ? gu : gu - kTilesA;
+  const uint8_t* base = is_a ? p.a : expert_of<MODE>(p.w, tl, p.w_expert);
+  int u = is_a ? gu : gu - kTilesA;
   const uint32_t row_bytes = (uint32_t)p.Kt * 1024u;
-  const __amdgpu_buffer_rsrc_t r = make_rsrc(base + (int64_t)(first + u) * row_bytes, u < count ? row_bytes : 0u);
+  int strip = first + u;
+  if constexpr (is_gated(MODE)) {
+    if (!is_a) {
+      const int half = gate_half(u);
+      u = gate_strip(u);
+      strip = first + u + half * (p.Ns >> 1);
+    }
+  }
+  const __amdgpu_buffer_rsrc_t r = make_rsrc(base + (int64_t)strip * row_bytes, u < count ? row_bytes : 0u);
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds_at((gu * kBufs + J) * 1024), 16, lane16, t << 10, 0, 0);
 }
 
+template <int MODE>
 __device__ __forceinline__ void issue_step(const GemmArgs& p, const Tile& tl, int J, int t, int wv,
                                            uint32_t lane16) {
 #pragma unroll
-  for (int q = 0; q < kLoadsPerWave; ++q) issue_unit(p, tl, J, t, q, wv, lane16);
+  for (int q = 0; q < kLoadsPerWave; ++q) issue_unit<MODE>(p, tl, J, t, q, wv, lane16);
 }
 
 // This wave's one buffer->LDS load of the scales of group g of tile `tl`:
@@ -234,6 +315,7 @@ __device__ __forceinline__ void issue_step(const GemmArgs& p, const Tile& tl, in
 // group goes in the scalar offset) and, at 128 wide, waves 6-7, whose zeros
 // land in a dummy area: every wave issues the load, so the waits count the
 // same operations in every wave.
+template <int MODE>
 __device__ __forceinline__ void issue_scales(const GemmArgs& p, const Tile& tl, int g, int wv) {
   const int gt = wv * 4;
   const bool is_a = gt < kTilesA;
@@ -242,11 +324,25 @@ __device__ __forceinline__ void issue_scales(const GemmArgs& p, const Tile& tl, 
   const int count = none ? 0 : is_a ? tl.mstrips : tl.strips;
   const int rt0 = is_a ? gt : gt - kTilesA;
   const int G = p.G;
-  const int left = __builtin_amdgcn_readfirstlane(max(0, count - rt0));
-  const __amdgpu_buffer_rsrc_t r =
-      make_rsrc((is_a ? p.as : p.ws) + (int64_t)(first + rt0) * G * 256, g < G ? (uint32_t)(left * G * 256) : 0u);
+  const uint8_t* sbase = is_a ? p.as : expert_of<MODE>(p.ws, tl, p.ws_expert);
   const uint32_t lds = none ? (uint32_t)kDummyLds : (uint32_t)(kScaleLds + gt * 256);
   const uint32_t l = lane_here();
+  if constexpr (is_gated(MODE)) {
+    // weight strips of both halves: a window from the first to the weight's
+    // end, the lanes past the tile's strips outside it
+    const int all = is_a ? count : p.Ns - first;
+    const __amdgpu_buffer_rsrc_t r =
+        make_rsrc(sbase + (int64_t)first * G * 256, (g < G && count > 0) ? (uint32_t)(all * G) * 256u : 0u);
+    const int u = rt0 + (int)(l >> 4);
+    const int at = is_a ? u : gate_strip(u);
+    const uint32_t strip = (uint32_t)(is_a ? u : at + gate_half(u) * (p.Ns >> 1));
+    const uint32_t svoff = at < count ? strip * (uint32_t)(G * 256) + (l & 15) * 16 : kOOB;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds_at(lds), 16, svoff, g << 8, 0, 0);
+    return;
+  }
+  const int left = __builtin_amdgcn_readfirstlane(max(0, count - rt0));
+  const __amdgpu_buffer_rsrc_t r =
+      make_rsrc(sbase + (int64_t)(first + rt0) * G * 256, g < G ? (uint32_t)(left * G * 256) : 0u);
   const uint32_t svoff = (l >> 4) * (uint32_t)(G * 256) + (l & 15) * 16;
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds_at(lds), 16, svoff, g << 8, 0, 0);
 }
@@ -255,12 +351,26 @@ __device__ __forceinline__ void issue_scales(const GemmArgs& p, const Tile& tl, 
 // tile `tl` (lanes 0 .. 8 kWN - 1 one bf16 pair each; N is a multiple of 4
 // here, so the window ends on a whole pair; no bias: an empty window,
 // zeros).
+// With a gate the wave's columns are those of its strips in both halves (N / 2
+// is a multiple of 16, so every strip is whole).
+template <int MODE>
 __device__ __forceinline__ void issue_bias(const GemmArgs& p, const Tile& tl, int wv, int wn) {
   const uint32_t lane = lane_here();
+  const uint16_t* bias = expert_of<MODE>(p.bias, tl, (int64_t)p.N);
+  if constexpr (is_gated(MODE)) {
+    const int u = wn * kWN + (int)(lane >> 3);
+    const int at = gate_strip(u);
+    const __amdgpu_buffer_rsrc_t r =
+        make_rsrc(p.bias ? (const void*)bias : (const void*)p.a, p.bias ? (uint32_t)p.N * 2u : 0u);
+    const uint32_t off = (uint32_t)(tl.s0 + at + gate_half(u) * (p.Ns >> 1)) * 32u + (lane & 7) * 4u;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds_at(kBiasLds + wv * 256), 4,
+                                             lane < 8 * kWN && at < tl.strips ? off : kOOB, 0, 0, 0);
+    return;
+  }
   const int col0 = (tl.s0 + wn * kWN) * 16;
   const int cols = __builtin_amdgcn_readfirstlane(p.bias ? max(0, min(16 * kWN, p.N - col0)) : 0);
   const __amdgpu_buffer_rsrc_t r =
-      make_rsrc(p.bias ? (const void*)(p.bias + col0) : (const void*)p.a, (uint32_t)(cols * 2));
+      make_rsrc(p.bias ? (const void*)(bias + col0) : (const void*)p.a, (uint32_t)(cols * 2));
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds_at(kBiasLds + wv * 256), 4, lane < 8 * kWN ? lane * 4 : kOOB, 0,
                                            0, 0);
 }
@@ -296,6 +406,13 @@ __device__ __forceinline__ void ds_write4(uint32_t addr, uint32_t v) {
 template <int N>
 __device__ __forceinline__ void wait_lgkm(v4i& a, v4i& b, v4i& c, v4i& d) {
   asm volatile("s_waitcnt lgkmcnt(%4)" : "+v"(a), "+v"(b), "+v"(c), "+v"(d) : "i"(N));
+}
+template <int N>
+__device__ __forceinline__ void wait_weights(v4i (&b)[kWN]) {
+  if constexpr (kWN == 4)
+    asm volatile("s_waitcnt lgkmcnt(%4)" : "+v"(b[0]), "+v"(b[1]), "+v"(b[2]), "+v"(b[3]) : "i"(N));
+  else
+    asm volatile("s_waitcnt lgkmcnt(%2)" : "+v"(b[0]), "+v"(b[1]) : "i"(N));
 }
 template <int N>
 __device__ __forceinline__ void wait_lgkm_scales(uint32_t (&sa)[kWM], uint32_t (&sb)[kWN]) {
@@ -455,16 +572,20 @@ struct Pipe {
 // loads plus, for J = 1 and 2, the scale and bias loads issued at J = 0,
 // plus, in a tile's first group (`first`), the kStores output stores of the
 // previous tile's epilogue (or the prologue's dropped stores).
-template <int J, int kStores, bool kBias>
+template <int J, int MODE, int kStores, bool kBias>
 __device__ __forceinline__ void main_step(const GemmArgs& p, Pipe& P, v4i (&bf_cur)[kWN], v4i (&bf_nxt)[kWN],
                                           const Tile& dt, const Tile& ct, int td, int first, int wv, int wm,
                                           int wn, const ReadAddr& ra, uint32_t lane16) {
   constexpr int kNext = (J + 1) & 3;
   constexpr int kAfter = 2 * kLoadsPerWave + ((J == 1 || J == 2) ? 1 + (kBias ? 1 : 0) : 0);
+  // An expert's last row tile is rarely whole: its empty quarters of rows
+  // are not multiplied.
+  const bool lo = !is_group(MODE) || ct.mstrips > wm * kWM;
+  const bool hi = !is_group(MODE) || ct.mstrips > wm * kWM + kWM / 2;
   wait_lgkm<4>(P.af[0], P.af[1], P.af[2], P.af[3]);
-  wait_lgkm<4>(bf_cur[0], bf_cur[1], bf_cur[2], bf_cur[3]);
+  wait_weights<4>(bf_cur);
   if (J == 0) wait_lgkm_scales<4>(P.sa, P.sb);
-  mfma_rows<J, 0>(P.acc, P.af, bf_cur, P.sa, P.sb);
+  if (lo) mfma_rows<J, 0>(P.acc, P.af, bf_cur, P.sa, P.sb);
   __builtin_amdgcn_sched_barrier(0);
   wait_lgkm<0>(P.af[4], P.af[5], P.af[6], P.af[7]);
   wait_vm_sel<kAfter, kAfter + (J < 3 ? kStores : 0)>(first);
@@ -473,20 +594,20 @@ __device__ __forceinline__ void main_step(const GemmArgs& p, Pipe& P, v4i (&bf_c
   // Rows 4-7 with this wave's buffer->LDS loads spread between them: issued
   // back to back by all waves right after the barrier, they would queue up
   // in the address unit and stall instruction issue (and the MFMAs behind).
-  if (J == 0) issue_scales(p, dt, td >> 2, wv);
-  if (J == 0 && kBias) issue_bias(p, ct, wv, wn);
+  if (J == 0) issue_scales<MODE>(p, dt, td >> 2, wv);
+  if (J == 0 && kBias) issue_bias<MODE>(p, ct, wv, wn);
   __builtin_amdgcn_sched_barrier(0);
-  mfma_row<J, 4>(P.acc, P.af, bf_cur, P.sa, P.sb);
-  issue_unit(p, dt, J, td, 0, wv, lane16);
+  if (hi) mfma_row<J, 4>(P.acc, P.af, bf_cur, P.sa, P.sb);
+  issue_unit<MODE>(p, dt, J, td, 0, wv, lane16);
   __builtin_amdgcn_sched_barrier(0);
-  mfma_row<J, 5>(P.acc, P.af, bf_cur, P.sa, P.sb);
-  issue_unit(p, dt, J, td, 1, wv, lane16);
+  if (hi) mfma_row<J, 5>(P.acc, P.af, bf_cur, P.sa, P.sb);
+  issue_unit<MODE>(p, dt, J, td, 1, wv, lane16);
   __builtin_amdgcn_sched_barrier(0);
-  mfma_row<J, 6>(P.acc, P.af, bf_cur, P.sa, P.sb);
-  issue_unit(p, dt, J, td, 2, wv, lane16);
+  if (hi) mfma_row<J, 6>(P.acc, P.af, bf_cur, P.sa, P.sb);
+  issue_unit<MODE>(p, dt, J, td, 2, wv, lane16);
   __builtin_amdgcn_sched_barrier(0);
-  mfma_row<J, 7>(P.acc, P.af, bf_cur, P.sa, P.sb);
-  if constexpr (kLoadsPerWave == 4) issue_unit(p, dt, J, td, 3, wv, lane16);
+  if (hi) mfma_row<J, 7>(P.acc, P.af, bf_cur, P.sa, P.sb);
+  if constexpr (kLoadsPerWave == 4) issue_unit<MODE>(p, dt, J, td, 3, wv, lane16);
   __builtin_amdgcn_sched_barrier(0);
   if (J == 3) read_scales(P.sa, P.sb, wm, wn);
   read_second_half<kNext>(P.af, ra);
@@ -504,15 +625,22 @@ __device__ __forceinline__ void main_step(const GemmArgs& p, Pipe& P, v4i (&bf_c
 // counted by its waits (vmcnt retires loads and stores in issue order); the
 // 128 of an element mode would exceed the counter's range (63), so that
 // epilogue waits for them instead.
+// (With a gate the wave's output is half as wide, and so are the counts: the
+// staged forms then store one piece a lane.)
 template <int MODE>
 struct OutMode {
-  static constexpr bool kF32 = MODE == 2 || MODE == 3;
-  static constexpr bool kFp4 = MODE == 4;
-  static constexpr bool kStaged = MODE == 0 || MODE == 4;
-  static constexpr bool kVec = MODE == 2;
+  static constexpr int kOut = MODE & 7;
+  static constexpr bool kF32 = kOut == 2 || kOut == 3;
+  static constexpr bool kFp4 = kOut == 4;
+  static constexpr bool kStaged = kOut == 0 || kOut == 4;
+  static constexpr bool kVec = kOut == 2;
   // per 16-row block: kWN / 2 row-piece stores (bf16), or as many code and
   // as many scale stores (MXFP4)
-  static constexpr int kStores = MODE == 0 ? kWN / 2 * kWM : kFp4 ? kWN * kWM : kVec ? kWM * kWN : 4 * kWM * kWN;
+  static constexpr int kPieces = is_gated(MODE) ? 1 : kWN / 2;
+  static constexpr int kStores = kOut == 0 ? kPieces * kWM
+                                 : kFp4    ? 2 * kPieces * kWM
+                                 : kVec    ? kWM * kOutWN<MODE>
+                                           : 4 * kWM * kOutWN<MODE>;
   static constexpr bool kDrain = !kStaged && !kVec;
   static constexpr int kInFlight = kDrain ? 0 : kStores;  // stores the next tile's waits count
   static constexpr bool kBiasLds = !kDrain;  // bias staged in LDS (whole pairs: N % 4 == 0)
@@ -530,6 +658,208 @@ __device__ __forceinline__ void read_bias(v2i (&bl)[kWN], int wv, int lane) {
     asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(bl[0]), "+v"(bl[1]), "+v"(bl[2]), "+v"(bl[3]));
   } else {
     asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(bl[0]), "+v"(bl[1]));
+  }
+}
+
+// Four bias values from the two dwords read_bias gives for a strip.
+__device__ __forceinline__ void bias_floats(const v2i& b, float (&v)[4]) {
+  v[0] = __uint_as_float((uint32_t)b.x << 16), v[1] = __uint_as_float((uint32_t)b.x & 0xFFFF0000u);
+  v[2] = __uint_as_float((uint32_t)b.y << 16), v[3] = __uint_as_float((uint32_t)b.y & 0xFFFF0000u);
+}
+
+// Raw bf16 bits of the `left` elements (4 at most) at byte offset off, one by
+// one; zeros past them.
+__device__ __forceinline__ void load_elements(__amdgpu_buffer_rsrc_t src, uint32_t off, int left, v2i& bits) {
+  uint32_t h[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    h[r] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(src, r < left ? off + 2 * r : kOOB, 0, 0);
+  bits.x = (int)(h[0] | h[1] << 16);
+  bits.y = (int)(h[2] | h[3] << 16);
+}
+
+// Raw bf16 bits of the residual at this lane's row (lane % 16) of the 16-row
+// block at rb and columns n .. n + 3, 0 outside the output or without a
+// residual: one 8-byte load where its rows allow it (p.res_vec, the same for
+// the whole launch), else, and with output by elements, one by one.
+template <bool kElements>
+__device__ __forceinline__ void load_residual_bits(const GemmArgs& p, int rb, int nrows, int n, int ncols, int lane,
+                                                   v2i& bits) {
+  const __amdgpu_buffer_rsrc_t rr =
+      make_rsrc(p.res ? (const void*)(p.res + (int64_t)rb * p.ldr) : (const void*)p.a,
+                p.res && nrows > 0 ? (uint32_t)((nrows - 1) * p.ldr + ncols) * 2u : 0u);
+  const bool in = (lane & 15) < nrows;
+  const uint32_t off = (uint32_t)((lane & 15) * p.ldr + n) * 2u;
+  if (!kElements && p.res_vec)
+    bits = __builtin_bit_cast(v2i, __builtin_amdgcn_raw_buffer_load_b64(rr, in && n < ncols ? off : kOOB, 0, 0));
+  else
+    load_elements(rr, off, in ? ncols - n : 0, bits);
+}
+template <bool kElements>
+__device__ __forceinline__ void load_residual(const GemmArgs& p, int rb, int nrows, int n, int ncols, int lane,
+                                              float (&v)[4]) {
+  v2i bits;
+  load_residual_bits<kElements>(p, rb, nrows, n, ncols, lane, bits);
+  bias_floats(bits, v);
+}
+
+// The epilogue's values of strip j of block i: bias, and with an activation
+// act(v) (times the gate's factor) + residual bits.
+template <int MODE, int CLASS>
+__device__ __forceinline__ void finish(const GemmArgs& p, const v4f (&acc)[kWN], const v2i (&bl)[kWN], int j,
+                                       const v2i& res, float (&v)[4]) {
+  float b[4];
+  bias_floats(bl[j], b);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) v[r] = acc[j][r] + b[r];
+  if constexpr (is_act(MODE)) {
+    float add[4];
+    bias_floats(res, add);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = activate_as<CLASS>(v[r], p.act);
+    if constexpr (is_gated(MODE)) {
+      bias_floats(bl[j + kWN / 2], b);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] *= acc[j + kWN / 2][r] + b[r];
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] += add[r];
+  }
+}
+
+// The staged epilogue with an activation (mode 0, kModeAct): as
+// epilogue_staged, with the residual of the next 16-row block loaded while
+// one is finished.  With a gate a row of the wave is 8 kWN columns: kWN
+// lanes of 16 bytes, and at 128-wide tiles only the first half of the lanes
+// has a piece.
+template <int MODE, int CLASS>
+__device__ __forceinline__ void epilogue_staged_act(const GemmArgs& p, const Tile& tl, v4f (&acc)[kWM][kWN], int wv,
+                                                    int wm, int wn) {
+  constexpr int kJ = kOutWN<MODE>;
+  constexpr int kLanes = 2 * kJ;                             // lanes of a row
+  constexpr int kRows = 64 / kLanes < 16 ? 64 / kLanes : 16;  // rows a store takes
+  constexpr int kPieces = OutMode<MODE>::kPieces;
+  static_assert(kPieces * kRows == 16, "pieces cover the block's rows");
+  const int lane = (int)lane_here();
+  const int row0 = tl.ms * 16 + wm * 128;
+  const int ncols = is_gated(MODE) ? p.N >> 1 : p.N;
+  const int n = (tl.s0 + wn * kJ) * 16 + (lane % kLanes) * 8;
+  const int nd = (tl.s0 + wn * kJ) * 16 + 4 * (lane >> 4);  // this lane's computed columns of strip 0
+  v2i bl[kWN];
+  read_bias(bl, wv, lane);
+  const uint32_t wst = kEpiLds + (uint32_t)wv * 16 * kEpiRowB;
+  const uint32_t waddr = wst + (uint32_t)(lane & 15) * kEpiRowB + (uint32_t)(lane >> 4) * 8;
+  const int prow = lane / kLanes;
+  const uint32_t raddr = wst + (uint32_t)(prow & 15) * kEpiRowB + (uint32_t)(lane % kLanes) * 16;
+  const uint32_t voff = n < ncols && prow < 16 ? (uint32_t)(prow * p.ldo + n) * 2 : kOOB;
+  uint8_t* const out = reinterpret_cast<uint8_t*>(p.out);
+  v2i res[2][kJ];
+  auto fetch = [&](int i, v2i (&r)[kJ]) {
+    const int rb = row0 + i * 16;
+    const int nrows = __builtin_amdgcn_readfirstlane(max(0, min(16, row_end<MODE>(p, tl) - rb)));
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) load_residual_bits<false>(p, rb, nrows, nd + j * 16, ncols, lane, r[j]);
+  };
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) res[0][j] = res[1][j] = (v2i){0, 0};
+  if (p.res) fetch(0, res[0]);
+#pragma unroll
+  for (int i = 0; i < kWM; ++i) {
+    if (p.res && i + 1 < kWM) fetch(i + 1, res[(i + 1) & 1]);
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      float v[4];
+      finish<MODE, CLASS>(p, acc[i], bl, j, res[i & 1][j], v);
+      const v2i d = {(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])};
+      if (j == 0) ds_write8<0>(waddr, d);
+      if (j == 1) ds_write8<32>(waddr, d);
+      if (j == 2) ds_write8<64>(waddr, d);
+      if (j == 3) ds_write8<96>(waddr, d);
+    }
+    v4i r0, r1;
+    ds_read16<0>(r0, raddr);
+    if constexpr (kPieces == 2) {
+      ds_read16<kRows * kEpiRowB>(r1, raddr);
+      asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(r0), "+v"(r1));
+    } else {
+      asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(r0));
+    }
+    const int rb = row0 + i * 16;
+    // (uniform: see epilogue_staged)
+    const int nrows = __builtin_amdgcn_readfirstlane(max(0, min(16, row_end<MODE>(p, tl) - rb)));
+    const __amdgpu_buffer_rsrc_t ro = make_rsrc(out + (int64_t)rb * p.ldo * 2, (uint32_t)(nrows * p.ldo * 2));
+    // (whole 128-byte lines only without a gate, 256 wide: see kStagedStoreAux)
+    constexpr int kAux = is_gated(MODE) ? 0 : kStagedStoreAux;
+    __builtin_amdgcn_raw_buffer_store_b128(r0, ro, voff, 0, kAux);
+    if constexpr (kPieces == 2)
+      __builtin_amdgcn_raw_buffer_store_b128(r1, ro, n < ncols ? voff + (uint32_t)(kRows * p.ldo) * 2 : kOOB, 0, kAux);
+  }
+}
+
+// Rows of the experts' first product (mode 4, kModeGroup | kModeRows): the
+// bf16 values, staged as in epilogue_staged, encoded per 1x32 block and stored
+// in the GEMM layouts of the second, whose strips are the same: a quad of
+// lanes holds a row's block, its 16 code bytes are one slot of the strip's
+// unit, and the 16 rows' slots are consecutive.
+template <int MODE, int CLASS>
+__device__ __forceinline__ void epilogue_rows(const GemmArgs& p, const Tile& tl, v4f (&acc)[kWM][kWN], int wv, int wm,
+                                              int wn) {
+  constexpr int kJ = kOutWN<MODE>;
+  static_assert(kJ % 2 == 0, "a wave holds whole 1x32 blocks");
+  constexpr int kLanes = 2 * kJ;
+  constexpr int kRows = 64 / kLanes;
+  constexpr int kPieces = OutMode<MODE>::kPieces;
+  static_assert(kPieces * kRows == 16, "pieces cover the block's rows");
+  const int lane = (int)lane_here();
+  const int ncols = is_gated(MODE) ? p.N >> 1 : p.N;
+  const int n = (tl.s0 + wn * kJ) * 16 + (lane % kLanes) * 8;
+  const int c = n >> 5;  // 1x32 block of the row
+  v2i bl[kWN];
+  read_bias(bl, wv, lane);
+  const uint32_t wst = kEpiLds + (uint32_t)wv * 16 * kEpiRowB;
+  const uint32_t waddr = wst + (uint32_t)(lane & 15) * kEpiRowB + (uint32_t)(lane >> 4) * 8;
+  const int prow = lane / kLanes;
+  const uint32_t raddr = wst + (uint32_t)prow * kEpiRowB + (uint32_t)(lane % kLanes) * 16;
+  const uint32_t doff =
+      n < ncols ? (uint32_t)(c >> 2) * 1024u + (uint32_t)((c & 3) * 16 + prow) * 16u + (uint32_t)(lane & 3) * 4u : kOOB;
+  const uint32_t soff = (n < ncols && (lane & 3) == 0)
+                            ? (uint32_t)(c >> 4) * 256u + (uint32_t)((c & 3) * 16 + prow) * 4u + (uint32_t)((c >> 2) & 3)
+                            : kOOB;
+#pragma unroll
+  for (int i = 0; i < kWM; ++i) {
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      float v[4];
+      finish<MODE, CLASS>(p, acc[i], bl, j, (v2i){0, 0}, v);
+      const v2i d = {(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])};
+      if (j == 0) ds_write8<0>(waddr, d);
+      if (j == 1) ds_write8<32>(waddr, d);
+      if (j == 2) ds_write8<64>(waddr, d);
+      if (j == 3) ds_write8<96>(waddr, d);
+    }
+    v4i rv[2];
+    ds_read16<0>(rv[0], raddr);
+    if constexpr (kPieces == 2) {
+      ds_read16<kRows * kEpiRowB>(rv[1], raddr);
+      asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(rv[0]), "+v"(rv[1]));
+    } else {
+      asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(rv[0]));
+    }
+    const int strip = tl.ms + wm * kWM + i;
+    const bool there = wm * kWM + i < tl.mstrips;  // a strip past the tile's belongs to another
+    const __amdgpu_buffer_rsrc_t rd =
+        make_rsrc(p.rows_out + (int64_t)strip * p.rows_kt * 1024, there ? (uint32_t)p.rows_kt * 1024u : 0u);
+    const __amdgpu_buffer_rsrc_t rs =
+        make_rsrc(p.rows_scales + (int64_t)strip * p.rows_g * 256, there ? (uint32_t)p.rows_g * 256u : 0u);
+#pragma unroll
+    for (int q = 0; q < kPieces; ++q) {
+      const uint32_t w0 = (uint32_t)rv[q].x, w1 = (uint32_t)rv[q].y, w2 = (uint32_t)rv[q].z, w3 = (uint32_t)rv[q].w;
+      const uint32_t b = e8m0_of_amax_bits(quad_amax_bits(w0, w1, w2, w3));
+      const uint32_t code = e2m1_pack8(w0, w1, w2, w3, e8m0_value(b));
+      __builtin_amdgcn_raw_buffer_store_b32(code, rd, n < ncols ? doff + (uint32_t)(q * kRows) * 16u : kOOB, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b8((uint8_t)b, rs, soff != kOOB ? soff + (uint32_t)(q * kRows) * 4u : kOOB, 0,
+                                           0);
+    }
   }
 }
 
@@ -656,31 +986,45 @@ __device__ __forceinline__ void epilogue_fp4(const GemmArgs& p, const Tile& tl, 
 // size ends at the last valid row; columns past N get an out-of-range
 // offset.  Each store instruction is issued unconditionally, so the count of
 // memory operations the K loop's waits rely on is exact.
-template <int MODE>
+template <int MODE, int CLASS>
 __device__ __forceinline__ void epilogue(const GemmArgs& p, const Tile& tl, v4f (&acc)[kWM][kWN], int wv, int wm,
                                          int wn) {
   using OM = OutMode<MODE>;
+  constexpr int kJ = kOutWN<MODE>;
   const int lane = (int)lane_here();
   constexpr int esz = OM::kF32 ? 4 : 2;
   const int row0 = tl.ms * 16 + wm * 128;  // wave's first output row
-  const int ncol0 = (tl.s0 + wn * kWN) * 16 + 4 * (lane >> 4);
+  const int ncol0 = (tl.s0 + wn * kJ) * 16 + 4 * (lane >> 4);
+  const int ncols = is_gated(MODE) ? p.N >> 1 : p.N;
   const uint32_t lrow = (uint32_t)((lane & 15) * p.ldo) * esz;
   uint8_t* const out = reinterpret_cast<uint8_t*>(p.out);
+  const uint16_t* const bsrc = expert_of<MODE>(p.bias, tl, (int64_t)p.N);
   // Bias staged in LDS by this wave (mode 2): 4 columns per j.
   v2i bl[kWN];
-  if (OM::kBiasLds) read_bias(bl, wv, lane);
+  if constexpr (OM::kBiasLds) {
+    read_bias(bl, wv, lane);
+  } else if constexpr (is_act(MODE)) {
 #pragma unroll
-  for (int j = 0; j < kWN; ++j) {
+    for (int j = 0; j < kWN; ++j) {
+      const bool second = is_gated(MODE) && j >= kJ;
+      load_elements(make_rsrc(p.bias ? (const void*)bsrc : (const void*)p.a, p.bias ? (uint32_t)p.N * 2u : 0u),
+                    (uint32_t)(ncol0 + (second ? ncols + (j - kJ) * 16 : j * 16)) * 2u,
+                    ncols - (ncol0 + (second ? j - kJ : j) * 16), bl[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) {
     const int n = ncol0 + j * 16;
-    float bias[4];
-    if (OM::kBiasLds) {
-      bias[0] = __uint_as_float((uint32_t)bl[j].x << 16);
-      bias[1] = __uint_as_float((uint32_t)bl[j].x & 0xFFFF0000u);
-      bias[2] = __uint_as_float((uint32_t)bl[j].y << 16);
-      bias[3] = __uint_as_float((uint32_t)bl[j].y & 0xFFFF0000u);
+    float bias[4], ubias[4];
+    if (OM::kBiasLds || is_act(MODE)) {
+      bias_floats(bl[j], bias);
+      if (is_gated(MODE)) bias_floats(bl[j + kWN - kJ], ubias);
     } else {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) bias[r] = (p.bias && n + r < p.N) ? bf16_to_f32(p.bias[n + r]) : 0.f;
+      for (int r = 0; r < 4; ++r) {
+        bias[r] = (p.bias && n + r < ncols) ? bf16_to_f32(bsrc[n + r]) : 0.f;
+        if (is_gated(MODE)) ubias[r] = (p.bias && n + r < ncols) ? bf16_to_f32(bsrc[ncols + n + r]) : 0.f;
+      }
     }
     const uint32_t voff = lrow + (uint32_t)n * esz;
 #pragma unroll
@@ -688,13 +1032,23 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Tile& tl, v4f 
       const int rb = row0 + i * 16;
       // (uniform, but max/min would be computed in a vector register, which
       // would turn every store into a waterfall loop over the descriptor)
-      const int nrows = __builtin_amdgcn_readfirstlane(max(0, min(16, p.M - rb)));
+      const int nrows = __builtin_amdgcn_readfirstlane(max(0, min(16, row_end<MODE>(p, tl) - rb)));
       const __amdgpu_buffer_rsrc_t ro = make_rsrc(out + (int64_t)rb * p.ldo * esz, (uint32_t)(nrows * p.ldo * esz));
       float v[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) v[r] = acc[i][j][r] + bias[r];
+      if constexpr (is_act(MODE)) {
+        float res[4];
+        load_residual<OM::kDrain>(p, rb, nrows, n, ncols, lane, res);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          v[r] = activate_as<CLASS>(v[r], p.act);
+          if constexpr (is_gated(MODE)) v[r] *= acc[i][j + kWN - kJ][r] + ubias[r];
+          v[r] += res[r];
+        }
+      }
       if (OM::kVec) {
-        const uint32_t off = n < p.N ? voff : kOOB;
+        const uint32_t off = n < ncols ? voff : kOOB;
         if (OM::kF32) {
           __builtin_amdgcn_raw_buffer_store_b128(
               (v4i){(int)__float_as_uint(v[0]), (int)__float_as_uint(v[1]), (int)__float_as_uint(v[2]),
@@ -704,7 +1058,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Tile& tl, v4f 
       } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const uint32_t off = n + r < p.N ? voff + r * esz : kOOB;
+          const uint32_t off = n + r < ncols ? voff + r * esz : kOOB;
           if (OM::kF32)
             __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[r]), ro, off, 0, 0);
           else
@@ -716,9 +1070,20 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Tile& tl, v4f 
   if (OM::kDrain) wait_vm<0>();
 }
 
+template <int MODE, int CLASS>
+__device__ __forceinline__ void epilogue_act(const GemmArgs& p, const Tile& tl, v4f (&acc)[kWM][kWN], int wv, int wm,
+                                             int wn) {
+  if constexpr (is_rows(MODE))
+    epilogue_rows<MODE, CLASS>(p, tl, acc, wv, wm, wn);
+  else if constexpr (OutMode<MODE>::kStaged)
+    epilogue_staged_act<MODE, CLASS>(p, tl, acc, wv, wm, wn);
+  else
+    epilogue<MODE, CLASS>(p, tl, acc, wv, wm, wn);
+}
+
 // The four K-steps of group g of work item c, loading four steps on (from
 // item cn when g is c's last group).
-template <int kStores, bool kBias>
+template <int MODE, int kStores, bool kBias>
 __device__ __forceinline__ void group_body(const GemmArgs& p, Pipe& P, const Tile& c, const Tile& cn, int g,
                                            int wv, int wm, int wn, const ReadAddr& ra, uint32_t lane16) {
   const bool last = g + 1 == c.g1;
@@ -727,16 +1092,17 @@ __device__ __forceinline__ void group_body(const GemmArgs& p, Pipe& P, const Til
   dt.mstrips = last ? cn.mstrips : c.mstrips;
   dt.s0 = last ? cn.s0 : c.s0;
   dt.strips = last ? cn.strips : c.strips;
+  dt.e = last ? cn.e : c.e;
   const int t4 = last ? 4 * cn.g0 : 4 * (g + 1);
   // 1 in the item's first group, from a scalar instruction the compiler
   // cannot see through (it would peel the first group to fold the test,
   // which costs register copies around the loop).
   int first;
   asm volatile("s_cmp_eq_u32 %1, %2\n\ts_cselect_b32 %0, 1, 0" : "=s"(first) : "s"(g), "s"(c.g0) : "scc");
-  main_step<0, kStores, kBias>(p, P, P.b0, P.b1, dt, c, t4 + 0, first, wv, wm, wn, ra, lane16);
-  main_step<1, kStores, kBias>(p, P, P.b1, P.b0, dt, c, t4 + 1, first, wv, wm, wn, ra, lane16);
-  main_step<2, kStores, kBias>(p, P, P.b0, P.b1, dt, c, t4 + 2, first, wv, wm, wn, ra, lane16);
-  main_step<3, kStores, kBias>(p, P, P.b1, P.b0, dt, c, t4 + 3, first, wv, wm, wn, ra, lane16);
+  main_step<0, MODE, kStores, kBias>(p, P, P.b0, P.b1, dt, c, t4 + 0, first, wv, wm, wn, ra, lane16);
+  main_step<1, MODE, kStores, kBias>(p, P, P.b1, P.b0, dt, c, t4 + 1, first, wv, wm, wn, ra, lane16);
+  main_step<2, MODE, kStores, kBias>(p, P, P.b0, P.b1, dt, c, t4 + 2, first, wv, wm, wn, ra, lane16);
+  main_step<3, MODE, kStores, kBias>(p, P, P.b1, P.b0, dt, c, t4 + 3, first, wv, wm, wn, ra, lane16);
 }
 
 // kStores stores that write nothing (no records in the descriptor), as
@@ -873,6 +1239,7 @@ __global__ __launch_bounds__(512, 1) void MXFP4_PREFILL_KERNEL(GemmArgs p, int t
   // multiple of 8, slot numbers are remapped so each XCD's workgroups hold
   // consecutive slots (and so consecutive tiles, or slices of consecutive
   // tiles).
+  if constexpr (is_group(MODE)) tiles_m = __builtin_amdgcn_readfirstlane(p.head->blocks);
   const int ntiles = tiles_m * tiles_n;
   Share s;
   s.grid = gridDim.x;
@@ -882,6 +1249,8 @@ __global__ __launch_bounds__(512, 1) void MXFP4_PREFILL_KERNEL(GemmArgs p, int t
     const int rest = ntiles - sk.r;
     s.n = s.nsk + (rest > s.slot ? (rest - s.slot + s.grid - 1) / s.grid : 0);
   }
+  // (the grid is of the most tiles that a plan can list)
+  if (is_group(MODE) && s.n == 0) return;
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)&lds_raw[0];
   const uint32_t lane16 = lane * 16;
@@ -892,19 +1261,19 @@ __global__ __launch_bounds__(512, 1) void MXFP4_PREFILL_KERNEL(GemmArgs p, int t
   Pipe P;
   zero_acc(P.acc);
 
-  Tile c = work_at(p, sk, s, 0, tiles_m, tiles_n);
-  Tile cn = work_at(p, sk, s, 1, tiles_m, tiles_n);
+  Tile c = work_at<MODE>(p, sk, s, 0, tiles_m, tiles_n);
+  Tile cn = work_at<MODE>(p, sk, s, 1, tiles_m, tiles_n);
 
   // Prologue: scales of the first item's first group and its first 4 steps
   // in flight; then as many dropped stores as an epilogue leaves in flight,
   // so every item's first group counts the same operations.  Once the
   // scales and the first step have landed everywhere, read them in the
   // order the loop expects.
-  issue_scales(p, c, c.g0, wv);
-  issue_step(p, c, 0, 4 * c.g0 + 0, wv, lane16);
-  issue_step(p, c, 1, 4 * c.g0 + 1, wv, lane16);
-  issue_step(p, c, 2, 4 * c.g0 + 2, wv, lane16);
-  issue_step(p, c, 3, 4 * c.g0 + 3, wv, lane16);
+  issue_scales<MODE>(p, c, c.g0, wv);
+  issue_step<MODE>(p, c, 0, 4 * c.g0 + 0, wv, lane16);
+  issue_step<MODE>(p, c, 1, 4 * c.g0 + 1, wv, lane16);
+  issue_step<MODE>(p, c, 2, 4 * c.g0 + 2, wv, lane16);
+  issue_step<MODE>(p, c, 3, 4 * c.g0 + 3, wv, lane16);
   drop_stores<kStores>();
   wait_vm<3 * kLoadsPerWave + kStores>();
   barrier_nofence();
@@ -913,15 +1282,22 @@ __global__ __launch_bounds__(512, 1) void MXFP4_PREFILL_KERNEL(GemmArgs p, int t
   read_second_half<0>(P.af, ra);
 
   for (int k = 0;;) {
-    for (int g = c.g0; g < c.g1; ++g) group_body<kStores, kBiasLds>(p, P, c, cn, g, wv, wm, wn, ra, lane16);
-    const bool out = k >= s.nsk || sk_combine<kStores>(sk, s, P, wv);
+    for (int g = c.g0; g < c.g1; ++g) group_body<MODE, kStores, kBiasLds>(p, P, c, cn, g, wv, wm, wn, ra, lane16);
+    bool out = true;
+    if constexpr (!is_group(MODE)) out = k >= s.nsk || sk_combine<kStores>(sk, s, P, wv);
     if (out) {
-      if (OutMode<MODE>::kFp4)
+      if constexpr (is_act(MODE)) {
+        switch (act_class(p.act)) {
+          case 0: epilogue_act<MODE, 0>(p, c, P.acc, wv, wm, wn); break;
+          case 1: epilogue_act<MODE, 1>(p, c, P.acc, wv, wm, wn); break;
+          default: epilogue_act<MODE, 2>(p, c, P.acc, wv, wm, wn); break;
+        }
+      } else if (OutMode<MODE>::kFp4)
         epilogue_fp4(p, c, P.acc, wv, wm, wn);
       else if (OutMode<MODE>::kStaged)
         epilogue_staged(p, c, P.acc, wv, wm, wn);
       else
-        epilogue<MODE>(p, c, P.acc, wv, wm, wn);
+        epilogue<MODE, 0>(p, c, P.acc, wv, wm, wn);
     }
     if (++k == s.n) break;
     // The next item's first fragments and scales, already read in the last
@@ -933,7 +1309,7 @@ __global__ __launch_bounds__(512, 1) void MXFP4_PREFILL_KERNEL(GemmArgs p, int t
     read_second_half<0>(P.af, ra);
     zero_acc(P.acc);
     c = cn;
-    cn = work_at(p, sk, s, k + 1, tiles_m, tiles_n);
+    cn = work_at<MODE>(p, sk, s, k + 1, tiles_m, tiles_n);
   }
   // The loads issued past the last item (empty descriptors) still write
   // zeros to LDS: let them and the LDS reads finish before the workgroup
@@ -942,6 +1318,27 @@ __global__ __launch_bounds__(512, 1) void MXFP4_PREFILL_KERNEL(GemmArgs p, int t
   wait_vm<0>();
 }
 
+#if MXFP4_PREFILL_FORM == 2
+// The experts' products on `grid` workgroups: rows for the second product
+// (rows_out), or fp32 rows (out).
+hipError_t MXFP4_PREFILL_TILES(const GemmArgs& p, int grid, hipStream_t stream) {
+  const SkArgs none = {0, 1, nullptr, nullptr, nullptr, nullptr};
+  const int out_strips = p.gated ? p.Ns / 2 : p.Ns;
+  const dim3 g((unsigned)grid), b(64 * kWaves);
+  constexpr int kUp = 4 | kModeAct | kModeGroup | kModeRows;
+  if (p.rows_out && p.gated) {
+    if constexpr (kBN == 256)
+      MXFP4_PREFILL_KERNEL<kUp | kModeGated><<<g, b, 0, stream>>>(p, 0, (out_strips + kTilesB / 2 - 1) / (kTilesB / 2), none);
+    else
+      return hipErrorInvalidValue;  // a wave's gated output would be half a 1x32 block
+  } else if (p.rows_out) {
+    MXFP4_PREFILL_KERNEL<kUp><<<g, b, 0, stream>>>(p, 0, (out_strips + kTilesB - 1) / kTilesB, none);
+  } else {
+    MXFP4_PREFILL_KERNEL<2 | kModeGroup><<<g, b, 0, stream>>>(p, 0, (out_strips + kTilesB - 1) / kTilesB, none);
+  }
+  return hipGetLastError();
+}
+#else
 // This tile width's launch on `grid` workgroups: the split schedule's
 // counters cleared first (a kernel, not a memset: the launch may be
 // captured into a graph), then the GEMM in the output mode the call needs.
@@ -950,21 +1347,39 @@ hipError_t MXFP4_PREFILL_TILES(const GemmArgs& p, int grid, const PrefillSplit& 
   const int tiles_n = (p.Ns * 16 + kBN - 1) / kBN;
   if (sk.r) sk_clear_kernel<<<1, 256, 0, stream>>>(sk.err, 1 + sk.r + grid);
   const bool a16 = ((uintptr_t)p.out & 15) == 0;
+  const int cols = p.gated ? p.N / 2 : p.N;
   const int mode = p.out_fp4 ? 4
-                 : p.out_f32 ? ((p.N % 4 == 0 && p.ldo % 4 == 0 && a16) ? 2 : 3)
-                             : ((p.N % 8 == 0 && p.ldo % 8 == 0 && a16) ? 0 : 1);
+                 : p.out_f32 ? ((cols % 4 == 0 && p.ldo % 4 == 0 && a16) ? 2 : 3)
+                             : ((cols % 8 == 0 && p.ldo % 8 == 0 && a16) ? 0 : 1);
   const dim3 g((unsigned)grid), b(64 * kWaves);
+#if MXFP4_PREFILL_FORM == 0
+#define MXFP4_RUN(M) MXFP4_PREFILL_KERNEL<M><<<g, b, 0, stream>>>(p, tiles_m, tiles_n, sk)
   switch (mode) {
-    case 0: MXFP4_PREFILL_KERNEL<0><<<g, b, 0, stream>>>(p, tiles_m, tiles_n, sk); break;
-    case 1: MXFP4_PREFILL_KERNEL<1><<<g, b, 0, stream>>>(p, tiles_m, tiles_n, sk); break;
-    case 2: MXFP4_PREFILL_KERNEL<2><<<g, b, 0, stream>>>(p, tiles_m, tiles_n, sk); break;
-    case 4: MXFP4_PREFILL_KERNEL<4><<<g, b, 0, stream>>>(p, tiles_m, tiles_n, sk); break;
-    default: MXFP4_PREFILL_KERNEL<3><<<g, b, 0, stream>>>(p, tiles_m, tiles_n, sk); break;
+    case 0: MXFP4_RUN(0); break;
+    case 1: MXFP4_RUN(1); break;
+    case 2: MXFP4_RUN(2); break;
+    case 4: MXFP4_RUN(4); break;
+    default: MXFP4_RUN(3); break;
   }
+#else
+#define MXFP4_RUN(M)                                                                                       \
+  if (p.gated)                                                                                              \
+    MXFP4_PREFILL_KERNEL<(M) | kModeAct | kModeGated><<<g, b, 0, stream>>>(p, tiles_m, tiles_n, sk);        \
+  else                                                                                                      \
+    MXFP4_PREFILL_KERNEL<(M) | kModeAct><<<g, b, 0, stream>>>(p, tiles_m, tiles_n, sk)
+  switch (mode) {
+    case 0: MXFP4_RUN(0); break;
+    case 1: MXFP4_RUN(1); break;
+    case 2: MXFP4_RUN(2); break;
+    default: MXFP4_RUN(3); break;
+  }
+#endif
+#undef MXFP4_RUN
   return hipGetLastError();
 }
+#endif
 
-#if MXFP4_PREFILL_BN == 256
+#if MXFP4_PREFILL_BN == 256 && MXFP4_PREFILL_FORM == 0
 namespace {
 
 constexpr int kMaxSkGrid = 256;  // the split schedule's workgroups (and workspace) at most
@@ -1057,6 +1472,9 @@ hipError_t launch_gemm_prefill(const GemmArgs& p, hipStream_t stream) {
     sk.flags = sk.ctrl + pl.r;
     sk.part = p.work + sk_words_bytes(pl.r, pl.grid);
   }
+  if (p.epilogue)
+    return pl.bn == 128 ? launch_prefill_act_tiles_128(p, pl.grid, sk, stream)
+                        : launch_prefill_act_tiles_256(p, pl.grid, sk, stream);
   return pl.bn == 128 ? launch_prefill_tiles_128(p, pl.grid, sk, stream)
                       : launch_prefill_tiles_256(p, pl.grid, sk, stream);
 }

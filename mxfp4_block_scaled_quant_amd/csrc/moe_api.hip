@@ -149,8 +149,7 @@ int mxfp4_moe(const void* x, int64_t ldx, const void* ids, int64_t ldi, const vo
 }
 
 size_t mxfp4_linear_act_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (M <= 0 || N <= 0 || K <= 0 || K % 32) return 0;
-  return (size_t)cdiv(M * N * 4, 256) * 256 + mxfp4_linear_workspace_bytes(M, N, K);
+  return mxfp4_linear_workspace_bytes(M, N, K);
 }
 
 int mxfp4_linear_act(const void* x, int64_t ldx, const void* w_pre, const void* ws_pre, const void* bias,
@@ -164,31 +163,26 @@ int mxfp4_linear_act(const void* x, int64_t ldx, const void* w_pre, const void* 
   // 256 rows (one tile of the large-M kernel) stay addressable by 32-bit offsets
   if (M > 1 && (ldo > kMaxInt / 256 / (out_dtype == MXFP4_OUT_F32 ? 4 : 2) || (residual && ldr > kMaxInt / 256 / 2)))
     return MXFP4_ERR_SHAPE;
-  int st = linear_check(x, used(ldx, M) ? ldx : K, w_pre, ws_pre, bias, out, N, out_dtype, M, N, K);
+  int st = linear_check(x, M > 1 ? ldx : K, w_pre, ws_pre, bias, out, N, out_dtype, M, N, K);
   if (st) return st;
   if (workspace_bytes < mxfp4_linear_act_workspace_bytes(M, N, K)) return MXFP4_ERR_WORKSPACE;
   if (M == 0) return MXFP4_OK;
-  if (!workspace) return MXFP4_ERR_NULL;
-  if (!aligned(workspace, 256) || !aligned(residual, 2)) return MXFP4_ERR_ALIGN;
+  const size_t need = mxfp4_linear_act_workspace_bytes(M, N, K);
+  if (need && !workspace) return MXFP4_ERR_NULL;
+  if ((need && !aligned(workspace, 256)) || !aligned(residual, 2)) return MXFP4_ERR_ALIGN;
   int cus = 0;
   st = device_cus(&cus);
   if (st) return st;
-  const size_t rows = (size_t)cdiv(M * N * 4, 256) * 256;
-  st = linear_run(x, ldx, w_pre, ws_pre, bias, workspace, N, MXFP4_OUT_F32, M, N, K, (uint8_t*)workspace + rows,
-                  workspace_bytes - rows, true, cus, (hipStream_t)stream);
-  if (st) return st;
-  EpilogueArgs e{};
-  e.y = (const float*)workspace;
-  e.M = (int)M;
-  e.N = (int)N;
+  GemmArgs e{};
+  // (a call without anything to add is mxfp4_linear's)
+  e.epilogue = activation != MXFP4_ACT_NONE || gated || residual;
   e.act = activation;
   e.gated = gated != 0;
-  e.residual = (const uint16_t*)residual;
+  e.res = (const uint16_t*)residual;
   e.ldr = used(ldr, M);
-  e.out = out;
-  e.ldo = used(ldo, M);
-  e.out_f32 = out_dtype == MXFP4_OUT_F32;
-  return launched(launch_epilogue(e, (hipStream_t)stream));
+  e.res_vec = aligned(residual, 8) && e.ldr % 4 == 0 && cols % 4 == 0;
+  return linear_run_act(e, x, M > 1 ? ldx : K, w_pre, ws_pre, bias, out, M > 1 ? ldo : cols, out_dtype, M, N, K,
+                        workspace, workspace_bytes, cus, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -16,6 +16,7 @@
 //  * combine: a token's rows, weighted and added.
 #include "moe_launch.h"
 #include "mxfp4_device.h"
+#include "mxfp4_launch.h"
 
 namespace mxfp4 {
 
@@ -32,10 +33,6 @@ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 struct MoeLayout {
   int64_t strips, max_blocks;
   size_t head, blocks, pos, src, a, as, h, hs, part, total;
-};
-
-struct MoeHead {
-  int blocks, strips;
 };
 
 MoeLayout moe_layout(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, int64_t inner) {
@@ -125,9 +122,13 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(const int32_t* ids, int6
 // quant_1x32_gemm_kernel, a 256-thread workgroup per 1 KiB unit (16 rows x
 // one K-step), whose rows come from the pairs' tokens.  A strip's padding
 // rows become zeros with scale 1.
+// The first workgroup of a strip also writes the padding of its rows in
+// the second product's input (K2 values in Kt2 K-steps): zeros with scale 1
+// past K2.
 __global__ __launch_bounds__(256) void moe_gather_kernel(const uint16_t* x, int64_t ldx, const MoeHead* head,
                                                          const int32_t* src, int top_k, int K, int Kt, int G,
-                                                         uint8_t* q, uint8_t* scales) {
+                                                         uint8_t* q, uint8_t* scales, int K2, int Kt2, int G2,
+                                                         uint8_t* h, uint8_t* hs) {
   const int L = threadIdx.x;
   const int r = L >> 4, kb = (L >> 2) & 3, sub = L & 3;
   const int s = (int)(blockIdx.x / (unsigned)(4 * G)), tq = (int)(blockIdx.x % (unsigned)(4 * G));
@@ -147,6 +148,12 @@ __global__ __launch_bounds__(256) void moe_gather_kernel(const uint16_t* x, int6
     *reinterpret_cast<uint32_t*>(q + ((int64_t)s * Kt + tq) * 1024 + (kb * 16 + r) * 16 + sub * 4) = packed;
   }
   if (sub == 0) scales[((int64_t)s * G + (tq >> 2)) * 256 + (kb * 16 + r) * 4 + (tq & 3)] = (uint8_t)b;
+  if (tq == 0)
+    for (int c2 = (K2 >> 5) + (L & 15); c2 < G2 * 16; c2 += 16) {
+      const int t2 = c2 >> 2, k2 = c2 & 3;
+      if (t2 < Kt2) *reinterpret_cast<int4*>(h + ((int64_t)s * Kt2 + t2) * 1024 + (k2 * 16 + r) * 16) = (int4){0, 0, 0, 0};
+      hs[((int64_t)s * G2 + (t2 >> 2)) * 256 + (k2 * 16 + r) * 4 + (t2 & 3)] = (uint8_t)kE8M0One;
+    }
 }
 
 // -------------------------------------------------------------- the products
@@ -286,13 +293,6 @@ __global__ __launch_bounds__(64 * stream_waves(MT)) void moe_stream_kernel(Produ
         const int r = m & 15, t = c >> 2, kb = c & 3;
         *reinterpret_cast<uint32_t*>(p.h + (s * Kt2 + t) * 1024 + (kb * 16 + r) * 16 + piece * 4) = code;
         if (piece == 0) p.hs[(s * G2 + (t >> 2)) * 256 + (kb * 16 + r) * 4 + (t & 3)] = (uint8_t)b;
-        // the row's padding to whole K-steps and scale groups
-        if (c == p.cols - 1)
-          for (int c2 = p.cols + piece; c2 < G2 * 16; c2 += 4) {
-            const int t2 = c2 >> 2, k2 = c2 & 3;
-            if (t2 < Kt2) *reinterpret_cast<int4*>(p.h + (s * Kt2 + t2) * 1024 + (k2 * 16 + r) * 16) = (int4){0, 0, 0, 0};
-            p.hs[(s * G2 + (t2 >> 2)) * 256 + (k2 * 16 + r) * 4 + (t2 & 3)] = (uint8_t)kE8M0One;
-          }
       }
     }
   } else {
@@ -318,6 +318,18 @@ hipError_t launch_stream(const ProductArgs& p, int64_t max_blocks, hipStream_t s
 template <int MT>
 hipError_t launch_up(const ProductArgs& p, bool gated, int64_t max_blocks, hipStream_t stream) {
   return gated ? launch_stream<MT, 4, true>(p, max_blocks, stream) : launch_stream<MT, 2, true>(p, max_blocks, stream);
+}
+
+// Mean rows of an expert up to which its weights are streamed once per block
+// of up to 64 rows; with more the products run on tiles of 256 rows.
+constexpr int64_t kStreamRows = 48;
+
+// The large-M kernel over the plan's row tiles.
+hipError_t launch_tiles(const GemmArgs& p, int64_t max_blocks, hipStream_t stream) {
+  const int out_strips = p.gated ? p.Ns / 2 : p.Ns;
+  const int wide = p.gated ? 8 : 16;
+  const int64_t tiles = max_blocks * cdiv(out_strips, wide);
+  return launch_prefill_experts_256(p, (int)(tiles < p.cus ? tiles : p.cus), stream);
 }
 
 // --------------------------------------------------------------- the combine
@@ -364,36 +376,61 @@ hipError_t launch_moe(const MoeArgs& p, hipStream_t stream) {
   int32_t* pos = reinterpret_cast<int32_t*>(p.work + l.pos);
   int32_t* src = reinterpret_cast<int32_t*>(p.work + l.src);
   const int64_t mean = pairs / p.experts;
+  const bool tiles = mean > kStreamRows;
   const int mt = mean <= 10 ? 1 : mean <= 24 ? 2 : 4;
-  moe_plan_kernel<<<1, 1024, 0, stream>>>(p.ids, p.ldi, pairs, p.top_k, p.experts, mt, head, blocks, pos, src);
+  const int block_strips = tiles ? 16 : mt;
+  moe_plan_kernel<<<1, 1024, 0, stream>>>(p.ids, p.ldi, pairs, p.top_k, p.experts, block_strips, head, blocks, pos, src);
   const int kt1 = (int)cdiv(p.hidden, 128), g1 = (int)cdiv(kt1, 4);
   const int kt2 = (int)cdiv(p.inner, 128), g2 = (int)cdiv(kt2, 4);
   moe_gather_kernel<<<dim3((unsigned)(l.strips * 4 * g1)), 256, 0, stream>>>(
-      p.x, p.ldx, head, src, p.top_k, p.hidden, kt1, g1, p.work + l.a, p.work + l.as);
+      p.x, p.ldx, head, src, p.top_k, p.hidden, kt1, g1, p.work + l.a, p.work + l.as, p.inner, kt2, g2, p.work + l.h,
+      p.work + l.hs);
   // at most one block per strip, one part block per expert met
   const int64_t met = pairs < p.experts ? pairs : p.experts;
-  int64_t max_blocks = l.strips / mt + met;
+  int64_t max_blocks = l.strips / block_strips + met;
   if (max_blocks > l.strips) max_blocks = l.strips;
-  ProductArgs u{};
-  u.head = head, u.blocks = blocks;
-  u.a = p.work + l.a, u.as = p.work + l.as, u.w = p.up, u.ws = p.up_scales, u.bias = p.up_bias;
-  u.Kt = kt1, u.G = g1, u.Ns = p.inner * (p.gated ? 2 : 1) / 16, u.cols = p.inner / 32;
-  u.act = p.act, u.inner = p.inner, u.h = p.work + l.h, u.hs = p.work + l.hs;
-  hipError_t e = mt == 1 ? launch_up<1>(u, p.gated, max_blocks, stream)
-                 : mt == 2 ? launch_up<2>(u, p.gated, max_blocks, stream)
-                           : launch_up<4>(u, p.gated, max_blocks, stream);
-  if (e != hipSuccess) return e;
-  ProductArgs d{};
-  d.head = head, d.blocks = blocks;
-  d.a = p.work + l.h, d.as = p.work + l.hs, d.w = p.down, d.ws = p.down_scales, d.bias = p.down_bias;
-  d.Kt = kt2, d.G = g2, d.Ns = p.hidden / 16, d.cols = p.hidden / 32;
-  d.part = reinterpret_cast<float*>(p.work + l.part), d.hidden = p.hidden;
-  e = mt == 1 ? launch_stream<1, 2, false>(d, max_blocks, stream)
-      : mt == 2 ? launch_stream<2, 2, false>(d, max_blocks, stream)
-                : launch_stream<4, 2, false>(d, max_blocks, stream);
-  if (e != hipSuccess) return e;
+  float* part = reinterpret_cast<float*>(p.work + l.part);
+  hipError_t e;
+  if (tiles) {
+    GemmArgs u{};
+    u.cus = p.cus, u.head = head, u.blocks = blocks;
+    u.a = p.work + l.a, u.as = p.work + l.as, u.w = p.up, u.ws = p.up_scales, u.bias = p.up_bias;
+    u.N = p.inner * (p.gated ? 2 : 1), u.K = p.hidden, u.Kt = kt1, u.G = g1, u.Ns = u.N / 16;
+    u.w_expert = (int64_t)u.Ns * kt1 * 1024, u.ws_expert = (int64_t)u.Ns * g1 * 256;
+    u.epilogue = 1, u.act = p.act, u.gated = p.gated;
+    u.rows_out = p.work + l.h, u.rows_scales = p.work + l.hs, u.rows_kt = kt2, u.rows_g = g2;
+    e = launch_tiles(u, max_blocks, stream);
+    if (e != hipSuccess) return e;
+    GemmArgs d{};
+    d.cus = p.cus, d.head = head, d.blocks = blocks;
+    d.a = p.work + l.h, d.as = p.work + l.hs, d.w = p.down, d.ws = p.down_scales, d.bias = p.down_bias;
+    d.N = p.hidden, d.K = p.inner, d.Kt = kt2, d.G = g2, d.Ns = p.hidden / 16;
+    d.w_expert = (int64_t)d.Ns * kt2 * 1024, d.ws_expert = (int64_t)d.Ns * g2 * 256;
+    d.out = part, d.ldo = p.hidden, d.out_f32 = 1;
+    e = launch_tiles(d, max_blocks, stream);
+    if (e != hipSuccess) return e;
+  } else {
+    ProductArgs u{};
+    u.head = head, u.blocks = blocks;
+    u.a = p.work + l.a, u.as = p.work + l.as, u.w = p.up, u.ws = p.up_scales, u.bias = p.up_bias;
+    u.Kt = kt1, u.G = g1, u.Ns = p.inner * (p.gated ? 2 : 1) / 16, u.cols = p.inner / 32;
+    u.act = p.act, u.inner = p.inner, u.h = p.work + l.h, u.hs = p.work + l.hs;
+    e = mt == 1 ? launch_up<1>(u, p.gated, max_blocks, stream)
+        : mt == 2 ? launch_up<2>(u, p.gated, max_blocks, stream)
+                  : launch_up<4>(u, p.gated, max_blocks, stream);
+    if (e != hipSuccess) return e;
+    ProductArgs d{};
+    d.head = head, d.blocks = blocks;
+    d.a = p.work + l.h, d.as = p.work + l.hs, d.w = p.down, d.ws = p.down_scales, d.bias = p.down_bias;
+    d.Kt = kt2, d.G = g2, d.Ns = p.hidden / 16, d.cols = p.hidden / 32;
+    d.part = part, d.hidden = p.hidden;
+    e = mt == 1 ? launch_stream<1, 2, false>(d, max_blocks, stream)
+        : mt == 2 ? launch_stream<2, 2, false>(d, max_blocks, stream)
+                  : launch_stream<4, 2, false>(d, max_blocks, stream);
+    if (e != hipSuccess) return e;
+  }
   const int64_t n = p.tokens * (p.hidden / 4);
-  moe_combine_kernel<<<dim3((unsigned)cdiv(n, 256)), 256, 0, stream>>>(p, pos, d.part);
+  moe_combine_kernel<<<dim3((unsigned)cdiv(n, 256)), 256, 0, stream>>>(p, pos, part);
   return hipGetLastError();
 }
 

@@ -29,6 +29,11 @@ struct RouteArgs {
 
 hipError_t launch_moe_route(const RouteArgs& p, bool f32, bool sigmoid, hipStream_t stream);
 
+// What a plan found: blocks in its list, 16-row strips in all.
+struct MoeHead {
+  int blocks, strips;
+};
+
 // A run of one expert's rows that one workgroup (or row of tiles) takes:
 // `rows` rows from the first of 16-row strip `strip` on.
 struct MoeBlock {

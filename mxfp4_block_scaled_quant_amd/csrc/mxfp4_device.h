@@ -135,20 +135,53 @@ __device__ __forceinline__ int4 quant_block32(const int4 (&v)[4], uint32_t& b) {
   return c;
 }
 
-// The activations of an epilogue (MXFP4_ACT_* of the C ABI), in fp32.  The
-// sigmoid forms divide through the power and reciprocal instructions (an ulp
-// each); gelu's tail is taken from erfc, which keeps its relative precision.
+// The activations of an epilogue (MXFP4_ACT_* of the C ABI), in fp32, in three
+// classes, so that an unrolled epilogue is built once per class and not once
+// per activation:
+//  0  v, or max(v, 0)
+//  1  v times the sigmoid of a v (1 + b v^2): silu (1, 0) and gelu's tanh form
+//     (2 sqrt(2 / pi), 0.044715), through the power and reciprocal
+//     instructions (an ulp each)
+//  2  gelu: v/2 erfc(-v / sqrt 2), with erfc(z) = t exp(-z^2 + P(t)),
+//     t = 1 / (1 + z/2), z >= 0.  P, of degree 9, is a least-maximum fit of
+//     ln(exp(z^2) erfc(z) / t) over 0 <= z <= 23 in 64 bits (off by 7.2e-8),
+//     its coefficients here times log2(e).  The exponent's own rounding
+//     leaves 2.5e-6 relative at |v| = 5 and 7e-6 at 8.
 enum { kActNone = 0, kActSilu = 1, kActGelu = 2, kActGeluTanh = 3, kActRelu = 4 };
-__device__ __forceinline__ float sigmoid_f32(float v) {
-  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * v));
+__host__ __device__ __forceinline__ constexpr int act_class(int act) {
+  return act == kActGelu ? 2 : act == kActSilu || act == kActGeluTanh ? 1 : 0;
+}
+template <int CLASS>
+__device__ __forceinline__ float activate_as(float v, int act) {
+  constexpr float kLog2e = 1.44269504088896340736f;
+  if constexpr (CLASS == 0) {
+    return !(v <= 0.f) || act == kActNone ? v : 0.f;
+  } else if constexpr (CLASS == 1) {
+    const float a = act == kActSilu ? -kLog2e : -1.59576912160573071176f * kLog2e;
+    const float ab = act == kActSilu ? 0.f : -0.044715f * 1.59576912160573071176f * kLog2e;
+    return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * fmaf(ab, v * v, a)));
+  } else {
+    const float z = fabsf(v) * 0.70710678118654752440f;
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.5f, z, 1.f));
+    float q = 0.248002207f;
+    q = fmaf(q, t, -1.19127223f);
+    q = fmaf(q, t, 2.15287108f);
+    q = fmaf(q, t, -1.63642387f);
+    q = fmaf(q, t, 0.394838415f);
+    q = fmaf(q, t, -0.26192416f);
+    q = fmaf(q, t, 0.136590191f);
+    q = fmaf(q, t, 0.540417214f);
+    q = fmaf(q, t, 1.44264585f);
+    q = fmaf(q, t, -1.8257446f);
+    const float h = 0.5f * t * __builtin_amdgcn_exp2f(fmaf(-kLog2e * z, z, q));
+    return v < 0.f ? v * h : fmaf(-v, h, v);
+  }
 }
 __device__ __forceinline__ float activate(float v, int act) {
-  switch (act) {
-    case kActSilu: return v * sigmoid_f32(v);
-    case kActGelu: return 0.5f * v * erfcf(-0.70710678118654752440f * v);
-    case kActGeluTanh: return v * sigmoid_f32(1.59576912160573071176f * v * (1.f + 0.044715f * v * v));
-    case kActRelu: return v > 0.f ? v : (v != v ? v : 0.f);
-    default: return v;
+  switch (act_class(act)) {
+    case 0: return activate_as<0>(v, act);
+    case 1: return activate_as<1>(v, act);
+    default: return activate_as<2>(v, act);
   }
 }
 

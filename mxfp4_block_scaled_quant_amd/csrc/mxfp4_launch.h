@@ -39,6 +39,22 @@ struct GemmArgs {
   // tiles when this is smaller than gemm_prefill_workspace_bytes asks).
   uint8_t* work;
   size_t work_bytes;
+  // An epilogue after the bias (epilogue != 0): act(v), gated: act(v of the
+  // weight's first half of rows) * v of the second, plus the residual (bf16,
+  // row stride ldr elements, or nullptr; res_vec: whole 8-byte groups of its
+  // columns are aligned).
+  int epilogue, act, gated;
+  const uint16_t* res;
+  int64_t ldr;
+  int res_vec;
+  // The experts' products (large-M kernel): the plan's row tiles, the bytes
+  // from one expert's weight and scales to the next one's, and where the
+  // first product's rows go (GEMM layouts with rows_kt K-steps).
+  const struct MoeHead* head;
+  const struct MoeBlock* blocks;
+  int64_t w_expert, ws_expert;
+  uint8_t *rows_out, *rows_scales;
+  int rows_kt, rows_g;
 };
 
 hipError_t launch_gemm_decode(const GemmArgs& p, hipStream_t stream);
@@ -46,6 +62,11 @@ hipError_t launch_gemm_decode(const GemmArgs& p, hipStream_t stream);
 // of the activations and the output), each as launch_gemm_decode of those
 // rows alone.
 hipError_t launch_gemm_decode_rows(const GemmArgs& p, hipStream_t stream);
+// The same with an epilogue.
+hipError_t launch_gemm_decode_act(const GemmArgs& p, hipStream_t stream);
+hipError_t launch_gemm_decode_rows_act(const GemmArgs& p, hipStream_t stream);
+hipError_t launch_linear_decode_act(const GemmArgs& p, hipStream_t stream);
+hipError_t launch_linear_persist_act(const GemmArgs& p, hipStream_t stream);
 hipError_t launch_gemm_prefill(const GemmArgs& p, hipStream_t stream);
 // The large-M kernel's split (split-K) schedule of one launch: tiles [0, r)
 // cut into s K slices (r = 0: whole tiles); in the workspace, in this order:
@@ -63,6 +84,11 @@ struct PrefillSplit {
 // The large-M kernel at output-tile width 256 / 128 on `grid` workgroups.
 hipError_t launch_prefill_tiles_256(const GemmArgs& p, int grid, const PrefillSplit& sk, hipStream_t stream);
 hipError_t launch_prefill_tiles_128(const GemmArgs& p, int grid, const PrefillSplit& sk, hipStream_t stream);
+// The same with an epilogue, and over a plan's row tiles.
+hipError_t launch_prefill_act_tiles_256(const GemmArgs& p, int grid, const PrefillSplit& sk, hipStream_t stream);
+hipError_t launch_prefill_act_tiles_128(const GemmArgs& p, int grid, const PrefillSplit& sk, hipStream_t stream);
+hipError_t launch_prefill_experts_256(const GemmArgs& p, int grid, hipStream_t stream);
+hipError_t launch_prefill_experts_128(const GemmArgs& p, int grid, hipStream_t stream);
 // Workspace the large-M kernel's split schedule takes for this shape on up
 // to 256 compute units (0: whole tiles only).
 size_t gemm_prefill_workspace_bytes(int64_t M, int64_t N, int64_t K);
@@ -88,20 +114,6 @@ hipError_t launch_preshuffle_strided(const void* w_fp4, int64_t ldw, const void*
                                      int64_t lds, int64_t batch, int64_t N, int64_t K,
                                      void* w_out, void* ws_out, hipStream_t stream);
 
-// The epilogue of mxfp4_linear_act over fp32 rows [M, N] (bias added): the
-// activation, the gate and the residual, rounded once into out.
-struct EpilogueArgs {
-  const float* y;
-  int M, N;  // N: columns of y
-  int act, gated;
-  const uint16_t* residual;  // bf16 [M, N or N / 2] or nullptr
-  int64_t ldr;
-  void* out;
-  int64_t ldo;
-  int out_f32;
-};
-hipError_t launch_epilogue(const EpilogueArgs& p, hipStream_t stream);
-
 // mxfp4_linear's steps behind its C entry points (csrc/api.hip): the host
 // argument checks (everything but the workspace), the activation workspace
 // bytes without the large-M GEMM's split part (0 where the quantisation is
@@ -113,6 +125,11 @@ size_t linear_act_bytes(int64_t M, int64_t N, int64_t K);
 int linear_run(const void* x, int64_t ldx, const void* w_pre, const void* ws_pre, const void* bias,
                void* out, int64_t ldo, int out_dtype, int64_t M, int64_t N, int64_t K, void* workspace,
                size_t workspace_bytes, bool split, int cus, hipStream_t s);
+// mxfp4_linear_act's: the same with p.epilogue, act, gated, res, ldr and
+// res_vec of `epi`.
+int linear_run_act(const GemmArgs& epi, const void* x, int64_t ldx, const void* w_pre, const void* ws_pre,
+                   const void* bias, void* out, int64_t ldo, int out_dtype, int64_t M, int64_t N, int64_t K,
+                   void* workspace, size_t workspace_bytes, int cus, hipStream_t s);
 // The current device's compute units if it is a gfx950 (MXFP4_OK), else MXFP4_ERR_DEVICE.
 int device_cus(int* cus);
 
