@@ -22,6 +22,8 @@
 // bits.
 #include <float.h>
 
+#include <type_traits>
+
 #include "moe_launch.h"
 #include "mxfp4_device.h"
 
@@ -260,15 +262,134 @@ __device__ __forceinline__ int choose(const Choice& p, const float (&x)[V], cons
   return id;
 }
 
-template <int L, int V, bool SIGMOID, bool F32>
-__global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs p, int lanes2) {
-  constexpr float kLow = -__builtin_huge_valf();
-  const int lane = threadIdx.x & (L - 1);
-  const int64_t token = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
-  const bool live = token < p.tokens;
-  const int64_t row = (live ? token : p.tokens - 1) * p.ld;
+// fp32 values as integers of the same order (0 and -0 equal), and back.
+constexpr int kNone = (int)0x807FFFFFu;  // -inf
+__device__ __forceinline__ int order_of(float v) {
+  const int i = __builtin_bit_cast(int, v + 0.f);
+  return i ^ ((i >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float value_of(int i) {
+  return __builtin_bit_cast(float, i ^ ((i >> 31) & 0x7FFFFFFF));
+}
 
-  float x[V], b[V];
+// The largest integer of a wave, in a scalar register: shifts within rows of
+// 16 lanes, then row 0 into row 1 and 2 into 3, then the lower half into the
+// upper, one instruction each.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int max_step(int v) {
+  return max(v, __builtin_amdgcn_update_dpp((int)0x80000000u, v, CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ int wave_max(int v) {
+  v = max_step<0x111, 0xF>(v);
+  v = max_step<0x112, 0xF>(v);
+  v = max_step<0x114, 0xF>(v);
+  v = max_step<0x118, 0xF>(v);
+  v = max_step<0x142, 0xA>(v);
+  v = max_step<0x143, 0xC>(v);
+  return __builtin_amdgcn_readlane(v, 63);
+}
+
+// choose() in fp32 for a token that has a wave of its own (and whose groups,
+// if any, fill whole lanes): a round's largest value is in a scalar register,
+// so that one comparison and vote per register finds the lanes that hold it,
+// and the rest of the round is scalar.  Lane j gets round j's
+// expert.
+template <int V, bool SIGMOID>
+__device__ __forceinline__ int choose_wave(const Choice& p, const float (&x)[V], const float (&b)[V], int lane,
+                                           bool& unsure) {
+  constexpr float kLow = -__builtin_huge_valf();
+  constexpr float kBase = SIGMOID ? kMarginSigmoid : kMarginSoftmax;
+  float key[V];
+  const bool grouped = p.groups > 1;
+  if (!p.by_logit || grouped) {
+    if constexpr (SIGMOID) {
+#pragma unroll
+      for (int r = 0; r < V; ++r) key[r] = quotient(1.f, 1.f + exp_of(-x[r]));
+    } else {
+      float m = x[0];
+#pragma unroll
+      for (int r = 1; r < V; ++r) m = fmaxf(m, x[r]);
+      m = value_of(wave_max(order_of(m)));
+      float z = 0.f;
+#pragma unroll
+      for (int r = 0; r < V; ++r) {
+        key[r] = x[r] > kLow ? exp_of(x[r] - m) : 0.f;
+        z += key[r];
+      }
+      const float inv = quotient(1.f, all_sum<64>(z));
+#pragma unroll
+      for (int r = 0; r < V; ++r) key[r] *= inv;
+    }
+#pragma unroll
+    for (int r = 0; r < V; ++r) key[r] = x[r] > kLow ? key[r] + b[r] : kLow;
+  } else {
+#pragma unroll
+    for (int r = 0; r < V; ++r) key[r] = x[r];
+  }
+  if (grouped) {
+    float a = kLow, c = kLow;
+#pragma unroll
+    for (int r = 0; r < V; ++r) {
+      c = fmaxf(c, fminf(a, key[r]));
+      a = fmaxf(a, key[r]);
+    }
+    merge_lanes<64>(a, c, p.lanes2);
+    const float mine = (p.group_top == 2 && c > kLow) ? a + c : a;
+    // groups ahead of this lane's: for certain, and at most (its own among
+    // them); between the two fp32 cannot tell
+    const float margin = 2 * kBase + 2 * kMarginRel * fabsf(mine);
+    int certain = 0, most = 0;
+    for (int g = 0; g < p.groups; ++g) {
+      const float other =
+          __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine), g << p.lanes2));
+      certain += other > mine + margin ? 1 : 0;
+      most += !(other < mine - margin) ? 1 : 0;  // (true for inf - inf)
+    }
+    const bool in = (lane >> p.lanes2) < p.groups && mine > kLow;
+    const bool stays = in && most - 1 < p.kept;
+    unsure = unsure || (in && !stays && certain < p.kept);
+#pragma unroll
+    for (int r = 0; r < V; ++r) key[r] = stays ? (p.by_logit ? x[r] : key[r]) : kLow;
+  }
+  int left[V], got = kNone;
+#pragma unroll
+  for (int r = 0; r < V; ++r) left[r] = order_of(key[r]);
+  int id = -1;
+  const int rounds = p.by_logit ? p.top_k : min(p.top_k + 1, 64);  // the one after the last shows how sure it is
+  for (int j = 0; j < rounds; ++j) {
+    int best = left[0];
+#pragma unroll
+    for (int r = 1; r < V; ++r) best = max(best, left[r]);
+    best = wave_max(best);
+    if (best <= kNone) break;
+    uint64_t held[V], any = 0;
+#pragma unroll
+    for (int r = 0; r < V; ++r) any |= held[r] = __ballot(left[r] == best);
+    const int at = __builtin_ctzll(any);
+    int reg = 0;
+#pragma unroll
+    for (int r = V - 1; r >= 0; --r) reg = (held[r] >> at & 1) ? r : reg;
+    id = lane == j ? at * V + reg : id;
+    got = lane == j ? best : got;
+#pragma unroll
+    for (int r = 0; r < V; ++r) left[r] = (lane == at && reg == r) ? kNone : left[r];
+  }
+  const float value = value_of(got);
+  if (!p.by_logit) {
+    // round j and the next one closer than fp32 can tell
+    const float next = __shfl_down(value, 1);
+    if (lane < p.top_k && lane < 63 && next > kLow && !(value - next > kBase + kMarginRel * fabsf(next))) unsure = true;
+    if (p.top_k == 64) unsure = true;  // (lane 64, the first that is not chosen, does not exist)
+  }
+  return id;
+}
+
+// One token's logits and biases in registers, V consecutive ones a lane; -inf
+// for an expert that is not available.  Returns whether all biases are the
+// same.
+template <int L, int V, bool F32>
+__device__ __forceinline__ bool load_row(const RouteArgs& p, int64_t row, int lane, float (&x)[V], float (&b)[V]) {
+  constexpr float kLow = -__builtin_huge_valf();
   float lo = -kLow, hi = kLow;
 #pragma unroll
   for (int r = 0; r < V; ++r) {
@@ -277,26 +398,26 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs p, int lanes2)
     x[r] = F32 ? static_cast<const float*>(p.logits)[row + at]
                : bf16_to_f32(static_cast<const uint16_t*>(p.logits)[row + at]);
     b[r] = p.bias ? p.bias[at] : 0.f;
+  }
+#pragma unroll
+  for (int r = 0; r < V; ++r) {
+    const int e = lane * V + r;
     lo = fminf(lo, b[r]);
     hi = fmaxf(hi, b[r]);
     // false for a NaN
     const bool open = e < p.experts && x[r] > kLow && b[r] > kLow;
     x[r] = open ? fminf(x[r], FLT_MAX) : kLow;
   }
-  Choice c;
-  c.experts = p.experts, c.top_k = p.top_k, c.groups = p.groups, c.kept = p.kept, c.group_top = p.group_top;
-  c.size = p.experts / p.groups;
-  c.lanes2 = lanes2;
-  // (every lane reads the last expert's bias at least, so lo <= hi)
-  c.by_logit = !p.bias || all_min<64>(lo) == all_max<64>(hi);
+  // (every lane reads the last expert's bias at least, so lo <= hi; a NaN
+  // leaves both as they are, and is the same as -inf to the choice)
+  return !p.bias || !__any(lo != hi || lo != __shfl(lo, 0));
+}
 
-  bool unsure = false;
-  int id = choose<L, V, SIGMOID, float>(c, x, b, lane, unsure);
-  if (__any(unsure)) {
-    bool never = false;
-    id = choose<L, V, SIGMOID, double>(c, x, b, lane, never);
-  }
-
+// The weights of the chosen experts, one a lane: s, or s over their sum.
+template <int L, int V, bool SIGMOID, bool F32>
+__device__ __forceinline__ void store_choice(const RouteArgs& p, int64_t token, int64_t row, bool live, int lane,
+                                             int id, const float (&x)[V]) {
+  constexpr float kLow = -__builtin_huge_valf();
   const bool mine = lane < p.top_k && id >= 0;
   float xi = kLow;
   if (mine)
@@ -337,22 +458,85 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs p, int lanes2)
   }
 }
 
+__device__ __forceinline__ Choice choice_of(const RouteArgs& p, int lanes2, bool by_logit) {
+  Choice c;
+  c.experts = p.experts, c.top_k = p.top_k, c.groups = p.groups, c.kept = p.kept, c.group_top = p.group_top;
+  c.size = p.experts / p.groups;
+  c.lanes2 = lanes2;
+  c.by_logit = by_logit;
+  return c;
+}
+
+// A wave per token.
+template <int V, bool SIGMOID, bool F32>
+__global__ __launch_bounds__(256) void moe_route_wave_kernel(RouteArgs p, int lanes2) {
+  const int lane = threadIdx.x & 63;
+  const int64_t token = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (token >= p.tokens) return;
+  const int64_t row = token * p.ld;
+  float x[V], b[V];
+  const bool same = load_row<64, V, F32>(p, row, lane, x, b);
+  const Choice c = choice_of(p, lanes2, same);
+  bool unsure = false;
+  int id = choose_wave<V, SIGMOID>(c, x, b, lane, unsure);
+  if (__any(unsure)) {
+    bool never = false;
+    id = choose<64, V, SIGMOID, double>(c, x, b, lane, never);
+  }
+  store_choice<64, V, SIGMOID, F32>(p, token, row, true, lane, id, x);
+}
+
+template <int L, int V, bool SIGMOID, bool F32>
+__global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs p, int lanes2) {
+  const int lane = threadIdx.x & (L - 1);
+  const int64_t token = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  const bool live = token < p.tokens;
+  const int64_t row = (live ? token : p.tokens - 1) * p.ld;
+
+  float x[V], b[V];
+  const bool same = load_row<L, V, F32>(p, row, lane, x, b);
+  const Choice c = choice_of(p, lanes2, same);
+  bool unsure = false;
+  int id = choose<L, V, SIGMOID, float>(c, x, b, lane, unsure);
+  if (__any(unsure)) {
+    bool never = false;
+    id = choose<L, V, SIGMOID, double>(c, x, b, lane, never);
+  }
+  store_choice<L, V, SIGMOID, F32>(p, token, row, live, lane, id, x);
+}
+
+#define MOE_ROUTE(KERNEL, GRID, ...)                                              \
+  if (sigmoid && f32)                                                               \
+    KERNEL<__VA_ARGS__, true, true><<<GRID, 256, 0, stream>>>(p, lanes2);           \
+  else if (sigmoid)                                                                 \
+    KERNEL<__VA_ARGS__, true, false><<<GRID, 256, 0, stream>>>(p, lanes2);          \
+  else if (f32)                                                                     \
+    KERNEL<__VA_ARGS__, false, true><<<GRID, 256, 0, stream>>>(p, lanes2);          \
+  else                                                                              \
+    KERNEL<__VA_ARGS__, false, false><<<GRID, 256, 0, stream>>>(p, lanes2)
+
+// log2 of the lanes that a group of `size` experts fills, -1 if it does not
+// fill whole lanes, a power of two of them.
+int group_lanes(int size, int V, int L) {
+  for (int n = 0; (1 << n) <= L; ++n)
+    if (size == V << n) return n;
+  return -1;
+}
+
 template <int L, int V>
-hipError_t launch_lv(const RouteArgs& p, bool f32, bool sigmoid, hipStream_t stream) {
-  const int size = p.experts / p.groups;
-  int lanes2 = -1;
-  if (size % V == 0)
-    for (int n = 0; (1 << n) <= L; ++n)
-      if (size == V << n) lanes2 = n;
+hipError_t launch_parts(const RouteArgs& p, bool f32, bool sigmoid, hipStream_t stream) {
+  const int lanes2 = group_lanes(p.experts / p.groups, V, L);
   const dim3 grid((unsigned)((p.tokens + 256 / L - 1) / (256 / L)));
-  if (sigmoid && f32)
-    moe_route_kernel<L, V, true, true><<<grid, 256, 0, stream>>>(p, lanes2);
-  else if (sigmoid)
-    moe_route_kernel<L, V, true, false><<<grid, 256, 0, stream>>>(p, lanes2);
-  else if (f32)
-    moe_route_kernel<L, V, false, true><<<grid, 256, 0, stream>>>(p, lanes2);
-  else
-    moe_route_kernel<L, V, false, false><<<grid, 256, 0, stream>>>(p, lanes2);
+  MOE_ROUTE(moe_route_kernel, grid, L, V);
+  return hipGetLastError();
+}
+
+template <int V>
+hipError_t launch_wave(const RouteArgs& p, bool f32, bool sigmoid, hipStream_t stream) {
+  const int lanes2 = group_lanes(p.experts / p.groups, V, 64);
+  if (p.groups > 1 && lanes2 < 0) return launch_parts<64, V>(p, f32, sigmoid, stream);
+  const dim3 grid((unsigned)((p.tokens + 3) / 4));
+  MOE_ROUTE(moe_route_wave_kernel, grid, V);
   return hipGetLastError();
 }
 
@@ -362,11 +546,12 @@ hipError_t launch_moe_route(const RouteArgs& p, bool f32, bool sigmoid, hipStrea
   // Lane j keeps round j's expert and lane g group g's score, so a token has
   // at least as many lanes as either.
   const int need = p.top_k > p.groups ? p.top_k : p.groups;
-  if (need <= 16 && p.experts <= 64) return launch_lv<16, 4>(p, f32, sigmoid, stream);
-  if (need <= 16 && p.experts <= 128) return launch_lv<16, 8>(p, f32, sigmoid, stream);
-  if (need <= 16 && p.experts <= 256) return launch_lv<16, 16>(p, f32, sigmoid, stream);
-  if (p.experts <= 256) return launch_lv<64, 4>(p, f32, sigmoid, stream);
-  return launch_lv<64, 16>(p, f32, sigmoid, stream);
+  if (need <= 16 && p.experts <= 64) return launch_parts<16, 4>(p, f32, sigmoid, stream);
+  if (p.experts <= 64) return launch_wave<1>(p, f32, sigmoid, stream);
+  if (p.experts <= 128) return launch_wave<2>(p, f32, sigmoid, stream);
+  if (p.experts <= 256) return launch_wave<4>(p, f32, sigmoid, stream);
+  if (p.experts <= 512) return launch_wave<8>(p, f32, sigmoid, stream);
+  return launch_wave<16>(p, f32, sigmoid, stream);
 }
 
 }  // namespace mxfp4

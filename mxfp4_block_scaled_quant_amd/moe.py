@@ -29,7 +29,7 @@ def _code(table: dict, name: str, value: str) -> int:
 
 def _elsewhere(device: torch.device) -> bool:
     """Whether tensors on `device` need it made the current one first."""
-    return device.index != torch.cuda.current_device()
+    return device.index != torch._C._cuda_getDevice()
 
 
 def moe_route(logits: torch.Tensor, top_k: int, bias: Optional[torch.Tensor] = None, scoring: str = "softmax",
@@ -56,18 +56,21 @@ def moe_route(logits: torch.Tensor, top_k: int, bias: Optional[torch.Tensor] = N
     kind = logits.dtype
     if kind is not _F32 and kind is not _BF16:
         raise ValueError(f"logits must be torch.float32 or torch.bfloat16, got {kind}")
-    ld = _require(logits, "logits", kind, (-1, -1), dev)[0]
+    if logits.dim() != 2 or logits.stride(1) != 1:
+        _require(logits, "logits", kind, (-1, -1), dev)
     T, E = logits.shape
     if bias is not None:
         _require(bias, "bias", _F32, (E,), dev)
     if weights is None:
-        weights = torch.empty((T, top_k), dtype=_F32, device=dev)
+        weights, ldw = torch.empty_strided((T, top_k), (top_k, 1), dtype=_F32, device=dev), top_k
+    else:
+        ldw = _require(weights, "weights", _F32, (T, top_k), dev)[0]
     if ids is None:
-        ids = torch.empty((T, top_k), dtype=_I32, device=dev)
-    ldw = _require(weights, "weights", _F32, (T, top_k), dev)[0]
-    ldi = _require(ids, "ids", _I32, (T, top_k), dev)[0]
+        ids, ldi = torch.empty_strided((T, top_k), (top_k, 1), dtype=_I32, device=dev), top_k
+    else:
+        ldi = _require(ids, "ids", _I32, (T, top_k), dev)[0]
     status = lib().moe_route(
-        logits.data_ptr(), ld, 1 if kind is _F32 else 0, _addr(bias), T, E, top_k,
+        logits.data_ptr(), logits.stride(0), 1 if kind is _F32 else 0, _addr(bias), T, E, top_k,
         _code(SCORINGS, "scoring", scoring), groups, top_groups, group_top, 1 if renormalize else 0, scale,
         weights.data_ptr(), ldw, ids.data_ptr(), ldi, _raw_stream(dev))
     if status:
