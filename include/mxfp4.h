@@ -518,7 +518,7 @@ int moe_route(const void* logits, int64_t ld, int logits_dtype, const void* bias
  *             this call
  *   tokens >= 0 (0 enqueues nothing), tokens * top_k <= 2^24, top_k <= 64,
  *   experts <= 1024, hidden and inner multiples of 32 up to 2^20; an expert's
- *   weight stays below 2 GiB.
+ *   weight and x in MXFP4 (tokens * hidden / 2 bytes) stay below 2 GiB each.
  */
 size_t mxfp4_moe_workspace_bytes(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden,
                                  int64_t inner);

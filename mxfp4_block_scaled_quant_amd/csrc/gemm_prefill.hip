@@ -72,7 +72,7 @@
 #define MXFP4_PREFILL_TILES MXFP4_CAT(launch_prefill_act_tiles_, MXFP4_PREFILL_BN, )
 #else
 #define MXFP4_PREFILL_STEM gemm_prefill_experts
-#define MXFP4_PREFILL_TILES MXFP4_CAT(launch_prefill_experts_, MXFP4_PREFILL_BN, )
+#define MXFP4_PREFILL_TILES launch_prefill_experts
 #endif
 #if MXFP4_PREFILL_BN == 256
 #define MXFP4_PREFILL_KERNEL MXFP4_CAT(MXFP4_PREFILL_STEM, _kernel, )
@@ -172,7 +172,8 @@ __device__ __forceinline__ v4f mfma_fp4v(v4i a, v4i b, uint32_t sa, uint32_t sb,
 //              that a lane holds a gate and its factor (a wave's strips
 //              0 .. kWN/2 - 1 are gates, the others the factors beside them)
 //  kModeGroup  row tiles come from the plan's list, with their experts' weights
-//  kModeRows   (kModeGroup) MXFP4 output in the GEMM layouts
+//  kModeRows   (kModeGroup) rows gathered from tokens that are quantised row
+//              by row, MXFP4 output in the GEMM layouts
 constexpr int kModeAct = 8, kModeGated = 16, kModeGroup = 32, kModeRows = 64;
 constexpr bool is_act(int mode) { return (mode & kModeAct) != 0; }
 constexpr bool is_gated(int mode) { return (mode & kModeGated) != 0; }
@@ -269,6 +270,47 @@ __device__ __forceinline__ const T* expert_of(const T* base, const Tile& tl, int
   return is_group(MODE) ? base + tl.e * stride : base;
 }
 
+// kModeRows: where this lane finds its part of the wave's activation units of
+// a tile: byte offsets of its row (and block) in the quantised tokens, for
+// its four units and for the scales, out of range for a row of padding.  The
+// unit's LDS slots hold its rows one after the other, four 16-byte blocks
+// each (so that four lanes read 64 consecutive bytes), block b of row r in
+// slot 4 r + (b ^ (r / 4 % 4)): the exclusive or spreads the 16 rows that a
+// fragment read takes of one block over all LDS banks.
+struct Rows {
+  uint32_t unit[kLoadsPerWave], scale;
+};
+template <int MODE>
+__device__ __forceinline__ Rows rows_of(const GemmArgs& p, const Tile& tl, int wv) {
+  Rows o;
+  if constexpr (is_rows(MODE)) {
+    const int l = (int)lane_here();
+    const uint32_t block = (uint32_t)((l & 3) ^ (l >> 4));
+#pragma unroll
+    for (int q = 0; q < kLoadsPerWave; ++q) {
+      const int unit = wv * kLoadsPerWave + q;  // (weight units: not used)
+      const int tok = unit < tl.mstrips ? p.row_tokens[(tl.ms + unit) * 16 + (l >> 2)] : -1;
+      o.unit[q] = tok >= 0 ? (uint32_t)tok * (uint32_t)p.Kt * 64u + block * 16u : kOOB;
+    }
+    const int unit = wv * 4 + (l >> 4);
+    const int tok = unit < tl.mstrips ? p.row_tokens[(tl.ms + unit) * 16 + (l & 15)] : -1;
+    o.scale = tok >= 0 ? (uint32_t)tok * (uint32_t)p.G * 16u : kOOB;
+  } else {
+#pragma unroll
+    for (int q = 0; q < kLoadsPerWave; ++q) o.unit[q] = 0;
+    o.scale = 0;
+  }
+  return o;
+}
+template <int MODE>
+__device__ __forceinline__ Rows select_rows(bool second, const Rows& a, const Rows& b) {
+  Rows o;
+#pragma unroll
+  for (int q = 0; q < kLoadsPerWave; ++q) o.unit[q] = second ? b.unit[q] : a.unit[q];
+  o.scale = second ? b.scale : a.scale;
+  return o;
+}
+
 // This wave's buffer->LDS load of unit q (of its 4) of K-step t of tile
 // `tl` into stage J.  Waves 0-3 fetch the 16 activation units, waves 4-7 the
 // 16 weight units.  Each unit has its own descriptor (the unit's row of
@@ -276,13 +318,20 @@ __device__ __forceinline__ const T* expert_of(const T* base, const Tile& tl, int
 // one and load zeros.  The vector offset is the lane's 16 bytes, the step
 // goes in the scalar offset (in range whenever the descriptor is not empty).
 template <int MODE>
-__device__ __forceinline__ void issue_unit(const GemmArgs& p, const Tile& tl, int J, int t, int q, int wv,
-                                           uint32_t lane16) {
+__device__ __forceinline__ void issue_unit(const GemmArgs& p, const Tile& tl, const Rows& rows, int J, int t, int q,
+                                           int wv, uint32_t lane16) {
   // unit gu of the step's kUnits (activation units first): wave wv loads
   // units wv * kLoadsPerWave + q (all activation units in waves 0-3 at
   // 256 wide; at 128 wide wave 5 loads one of each kind)
   const int gu = wv * kLoadsPerWave + q;
   const bool is_a = gu < kTilesA;
+  if constexpr (is_rows(MODE)) {
+    if (is_a) {
+      const __amdgpu_buffer_rsrc_t r = make_rsrc(p.a, t < p.Kt ? p.a_bytes : 0u);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds_at((gu * kBufs + J) * 1024), 16, rows.unit[q], t << 6, 0, 0);
+      return;
+    }
+  }
   const int first = is_a ? tl.ms : tl.s0;
   const int count = t < p.Kt ? (is_a ? tl.mstrips : tl.strips) : 0;
   const uint8_t* base = is_a ? p.a : expert_of<MODE>(p.w, tl, p.w_expert);
@@ -301,10 +350,10 @@ __device__ __forceinline__ void issue_unit(const GemmArgs& p, const Tile& tl, in
 }
 
 template <int MODE>
-__device__ __forceinline__ void issue_step(const GemmArgs& p, const Tile& tl, int J, int t, int wv,
+__device__ __forceinline__ void issue_step(const GemmArgs& p, const Tile& tl, const Rows& rows, int J, int t, int wv,
                                            uint32_t lane16) {
 #pragma unroll
-  for (int q = 0; q < kLoadsPerWave; ++q) issue_unit<MODE>(p, tl, J, t, q, wv, lane16);
+  for (int q = 0; q < kLoadsPerWave; ++q) issue_unit<MODE>(p, tl, rows, J, t, q, wv, lane16);
 }
 
 // This wave's one buffer->LDS load of the scales of group g of tile `tl`:
@@ -316,9 +365,17 @@ __device__ __forceinline__ void issue_step(const GemmArgs& p, const Tile& tl, in
 // land in a dummy area: every wave issues the load, so the waits count the
 // same operations in every wave.
 template <int MODE>
-__device__ __forceinline__ void issue_scales(const GemmArgs& p, const Tile& tl, int g, int wv) {
+__device__ __forceinline__ void issue_scales(const GemmArgs& p, const Tile& tl, const Rows& rows, int g, int wv) {
   const int gt = wv * 4;
   const bool is_a = gt < kTilesA;
+  if constexpr (is_rows(MODE)) {
+    // a lane's row: the group's 16 scales, one word per block
+    if (is_a) {
+      const __amdgpu_buffer_rsrc_t r = make_rsrc(p.as, g < p.G ? p.as_bytes : 0u);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds_at(kScaleLds + gt * 256), 16, rows.scale, g << 4, 0, 0);
+      return;
+    }
+  }
   const bool none = gt >= kUnits;
   const int first = is_a ? tl.ms : tl.s0;
   const int count = none ? 0 : is_a ? tl.mstrips : tl.strips;
@@ -494,9 +551,12 @@ __device__ __forceinline__ void read_second_half(v4i (&af)[kWM], const ReadAddr&
   ds_read16<7 * 4096 + BUF * 1024>(af[7], ra.a);
 }
 // The 12 scale dwords of the group in LDS.
+template <int MODE>
 __device__ __forceinline__ void read_scales(uint32_t (&sa)[kWM], uint32_t (&sb)[kWN], int wm, int wn) {
-  const uint32_t l4 = lane_here() * 4;
-  const uint32_t a = l4 + (uint32_t)(kScaleLds + wm * kWM * 256);
+  const uint32_t l = lane_here();
+  const uint32_t l4 = l * 4;
+  // (kModeRows: row l % 16, word l / 16)
+  const uint32_t a = (is_rows(MODE) ? (l & 15) * 16 + (l >> 4) * 4 : l4) + (uint32_t)(kScaleLds + wm * kWM * 256);
   const uint32_t b = l4 + (uint32_t)(kScaleLds + (kTilesA + wn * kWN) * 256);
   ds_read4<0 * 256>(sa[0], a);
   ds_read4<1 * 256>(sa[1], a);
@@ -574,8 +634,8 @@ struct Pipe {
 // previous tile's epilogue (or the prologue's dropped stores).
 template <int J, int MODE, int kStores, bool kBias>
 __device__ __forceinline__ void main_step(const GemmArgs& p, Pipe& P, v4i (&bf_cur)[kWN], v4i (&bf_nxt)[kWN],
-                                          const Tile& dt, const Tile& ct, int td, int first, int wv, int wm,
-                                          int wn, const ReadAddr& ra, uint32_t lane16) {
+                                          const Tile& dt, const Rows& rows, const Tile& ct, int td, int first, int wv,
+                                          int wm, int wn, const ReadAddr& ra, uint32_t lane16) {
   constexpr int kNext = (J + 1) & 3;
   constexpr int kAfter = 2 * kLoadsPerWave + ((J == 1 || J == 2) ? 1 + (kBias ? 1 : 0) : 0);
   // An expert's last row tile is rarely whole: its empty quarters of rows
@@ -594,22 +654,22 @@ __device__ __forceinline__ void main_step(const GemmArgs& p, Pipe& P, v4i (&bf_c
   // Rows 4-7 with this wave's buffer->LDS loads spread between them: issued
   // back to back by all waves right after the barrier, they would queue up
   // in the address unit and stall instruction issue (and the MFMAs behind).
-  if (J == 0) issue_scales<MODE>(p, dt, td >> 2, wv);
+  if (J == 0) issue_scales<MODE>(p, dt, rows, td >> 2, wv);
   if (J == 0 && kBias) issue_bias<MODE>(p, ct, wv, wn);
   __builtin_amdgcn_sched_barrier(0);
   if (hi) mfma_row<J, 4>(P.acc, P.af, bf_cur, P.sa, P.sb);
-  issue_unit<MODE>(p, dt, J, td, 0, wv, lane16);
+  issue_unit<MODE>(p, dt, rows, J, td, 0, wv, lane16);
   __builtin_amdgcn_sched_barrier(0);
   if (hi) mfma_row<J, 5>(P.acc, P.af, bf_cur, P.sa, P.sb);
-  issue_unit<MODE>(p, dt, J, td, 1, wv, lane16);
+  issue_unit<MODE>(p, dt, rows, J, td, 1, wv, lane16);
   __builtin_amdgcn_sched_barrier(0);
   if (hi) mfma_row<J, 6>(P.acc, P.af, bf_cur, P.sa, P.sb);
-  issue_unit<MODE>(p, dt, J, td, 2, wv, lane16);
+  issue_unit<MODE>(p, dt, rows, J, td, 2, wv, lane16);
   __builtin_amdgcn_sched_barrier(0);
   if (hi) mfma_row<J, 7>(P.acc, P.af, bf_cur, P.sa, P.sb);
-  if constexpr (kLoadsPerWave == 4) issue_unit<MODE>(p, dt, J, td, 3, wv, lane16);
+  if constexpr (kLoadsPerWave == 4) issue_unit<MODE>(p, dt, rows, J, td, 3, wv, lane16);
   __builtin_amdgcn_sched_barrier(0);
-  if (J == 3) read_scales(P.sa, P.sb, wm, wn);
+  if (J == 3) read_scales<MODE>(P.sa, P.sb, wm, wn);
   read_second_half<kNext>(P.af, ra);
 }
 
@@ -851,6 +911,20 @@ __device__ __forceinline__ void epilogue_rows(const GemmArgs& p, const Tile& tl,
         make_rsrc(p.rows_out + (int64_t)strip * p.rows_kt * 1024, there ? (uint32_t)p.rows_kt * 1024u : 0u);
     const __amdgpu_buffer_rsrc_t rs =
         make_rsrc(p.rows_scales + (int64_t)strip * p.rows_g * 256, there ? (uint32_t)p.rows_g * 256u : 0u);
+    // the wave of the last block also pads the strip's rows to whole K-steps and
+    // scale groups: zeros with scale 1 (stores that no wait counts, which only
+    // makes the waits longer)
+    const int nblk = ncols >> 5, c0 = ((tl.s0 + wn * kJ) * 16) >> 5;
+    if (there && c0 < nblk && c0 + kJ / 2 >= nblk) {
+      const uint32_t pr = (uint32_t)(lane & 15);
+      for (int c2 = nblk + (lane >> 4); c2 < p.rows_g * 16; c2 += 4) {
+        const uint32_t t2 = (uint32_t)c2 >> 2, k2 = (uint32_t)c2 & 3;
+        __builtin_amdgcn_raw_buffer_store_b128((v4i){0, 0, 0, 0}, rd,
+                                               (int)t2 < p.rows_kt ? t2 * 1024u + (k2 * 16u + pr) * 16u : kOOB, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b8((uint8_t)kE8M0One, rs, (t2 >> 2) * 256u + (k2 * 16u + pr) * 4u + (t2 & 3), 0,
+                                             0);
+      }
+    }
 #pragma unroll
     for (int q = 0; q < kPieces; ++q) {
       const uint32_t w0 = (uint32_t)rv[q].x, w1 = (uint32_t)rv[q].y, w2 = (uint32_t)rv[q].z, w3 = (uint32_t)rv[q].w;
@@ -1084,8 +1158,8 @@ __device__ __forceinline__ void epilogue_act(const GemmArgs& p, const Tile& tl, 
 // The four K-steps of group g of work item c, loading four steps on (from
 // item cn when g is c's last group).
 template <int MODE, int kStores, bool kBias>
-__device__ __forceinline__ void group_body(const GemmArgs& p, Pipe& P, const Tile& c, const Tile& cn, int g,
-                                           int wv, int wm, int wn, const ReadAddr& ra, uint32_t lane16) {
+__device__ __forceinline__ void group_body(const GemmArgs& p, Pipe& P, const Tile& c, const Tile& cn, const Rows& rc,
+                                           const Rows& rn, int g, int wv, int wm, int wn, const ReadAddr& ra, uint32_t lane16) {
   const bool last = g + 1 == c.g1;
   Tile dt;
   dt.ms = last ? cn.ms : c.ms;
@@ -1093,16 +1167,17 @@ __device__ __forceinline__ void group_body(const GemmArgs& p, Pipe& P, const Til
   dt.s0 = last ? cn.s0 : c.s0;
   dt.strips = last ? cn.strips : c.strips;
   dt.e = last ? cn.e : c.e;
+  const Rows rows = select_rows<MODE>(last, rc, rn);
   const int t4 = last ? 4 * cn.g0 : 4 * (g + 1);
   // 1 in the item's first group, from a scalar instruction the compiler
   // cannot see through (it would peel the first group to fold the test,
   // which costs register copies around the loop).
   int first;
   asm volatile("s_cmp_eq_u32 %1, %2\n\ts_cselect_b32 %0, 1, 0" : "=s"(first) : "s"(g), "s"(c.g0) : "scc");
-  main_step<0, MODE, kStores, kBias>(p, P, P.b0, P.b1, dt, c, t4 + 0, first, wv, wm, wn, ra, lane16);
-  main_step<1, MODE, kStores, kBias>(p, P, P.b1, P.b0, dt, c, t4 + 1, first, wv, wm, wn, ra, lane16);
-  main_step<2, MODE, kStores, kBias>(p, P, P.b0, P.b1, dt, c, t4 + 2, first, wv, wm, wn, ra, lane16);
-  main_step<3, MODE, kStores, kBias>(p, P, P.b1, P.b0, dt, c, t4 + 3, first, wv, wm, wn, ra, lane16);
+  main_step<0, MODE, kStores, kBias>(p, P, P.b0, P.b1, dt, rows, c, t4 + 0, first, wv, wm, wn, ra, lane16);
+  main_step<1, MODE, kStores, kBias>(p, P, P.b1, P.b0, dt, rows, c, t4 + 1, first, wv, wm, wn, ra, lane16);
+  main_step<2, MODE, kStores, kBias>(p, P, P.b0, P.b1, dt, rows, c, t4 + 2, first, wv, wm, wn, ra, lane16);
+  main_step<3, MODE, kStores, kBias>(p, P, P.b1, P.b0, dt, rows, c, t4 + 3, first, wv, wm, wn, ra, lane16);
 }
 
 // kStores stores that write nothing (no records in the descriptor), as
@@ -1255,7 +1330,8 @@ __global__ __launch_bounds__(512, 1) void MXFP4_PREFILL_KERNEL(GemmArgs p, int t
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)&lds_raw[0];
   const uint32_t lane16 = lane * 16;
   ReadAddr ra;
-  ra.a = lds0 + wm * kWM * 4096 + lane16;
+  ra.a = lds0 + wm * kWM * 4096 +
+         (is_rows(MODE) ? (uint32_t)((lane & 15) * 4 + ((lane >> 4) ^ ((lane >> 2) & 3))) * 16u : lane16);
   ra.b = lds0 + (kTilesA + wn * kWN) * 4096 + lane16;
 
   Pipe P;
@@ -1269,20 +1345,21 @@ __global__ __launch_bounds__(512, 1) void MXFP4_PREFILL_KERNEL(GemmArgs p, int t
   // so every item's first group counts the same operations.  Once the
   // scales and the first step have landed everywhere, read them in the
   // order the loop expects.
-  issue_scales<MODE>(p, c, c.g0, wv);
-  issue_step<MODE>(p, c, 0, 4 * c.g0 + 0, wv, lane16);
-  issue_step<MODE>(p, c, 1, 4 * c.g0 + 1, wv, lane16);
-  issue_step<MODE>(p, c, 2, 4 * c.g0 + 2, wv, lane16);
-  issue_step<MODE>(p, c, 3, 4 * c.g0 + 3, wv, lane16);
+  Rows rc = rows_of<MODE>(p, c, wv), rn = rows_of<MODE>(p, cn, wv);
+  issue_scales<MODE>(p, c, rc, c.g0, wv);
+  issue_step<MODE>(p, c, rc, 0, 4 * c.g0 + 0, wv, lane16);
+  issue_step<MODE>(p, c, rc, 1, 4 * c.g0 + 1, wv, lane16);
+  issue_step<MODE>(p, c, rc, 2, 4 * c.g0 + 2, wv, lane16);
+  issue_step<MODE>(p, c, rc, 3, 4 * c.g0 + 3, wv, lane16);
   drop_stores<kStores>();
   wait_vm<3 * kLoadsPerWave + kStores>();
   barrier_nofence();
-  read_scales(P.sa, P.sb, wm, wn);
+  read_scales<MODE>(P.sa, P.sb, wm, wn);
   read_first_half<0>(P.af, P.b0, ra);
   read_second_half<0>(P.af, ra);
 
   for (int k = 0;;) {
-    for (int g = c.g0; g < c.g1; ++g) group_body<MODE, kStores, kBiasLds>(p, P, c, cn, g, wv, wm, wn, ra, lane16);
+    for (int g = c.g0; g < c.g1; ++g) group_body<MODE, kStores, kBiasLds>(p, P, c, cn, rc, rn, g, wv, wm, wn, ra, lane16);
     bool out = true;
     if constexpr (!is_group(MODE)) out = k >= s.nsk || sk_combine<kStores>(sk, s, P, wv);
     if (out) {
@@ -1304,12 +1381,14 @@ __global__ __launch_bounds__(512, 1) void MXFP4_PREFILL_KERNEL(GemmArgs p, int t
     // group, are read again from LDS (they stay there until the next
     // group's first barrier): so their registers are free across the
     // epilogue and the combine.
-    read_scales(P.sa, P.sb, wm, wn);
+    read_scales<MODE>(P.sa, P.sb, wm, wn);
     read_first_half<0>(P.af, P.b0, ra);
     read_second_half<0>(P.af, ra);
     zero_acc(P.acc);
     c = cn;
     cn = work_at<MODE>(p, sk, s, k + 1, tiles_m, tiles_n);
+    rc = rn;
+    rn = rows_of<MODE>(p, cn, wv);
   }
   // The loads issued past the last item (empty descriptors) still write
   // zeros to LDS: let them and the LDS reads finish before the workgroup
@@ -1327,10 +1406,7 @@ hipError_t MXFP4_PREFILL_TILES(const GemmArgs& p, int grid, hipStream_t stream) 
   const dim3 g((unsigned)grid), b(64 * kWaves);
   constexpr int kUp = 4 | kModeAct | kModeGroup | kModeRows;
   if (p.rows_out && p.gated) {
-    if constexpr (kBN == 256)
-      MXFP4_PREFILL_KERNEL<kUp | kModeGated><<<g, b, 0, stream>>>(p, 0, (out_strips + kTilesB / 2 - 1) / (kTilesB / 2), none);
-    else
-      return hipErrorInvalidValue;  // a wave's gated output would be half a 1x32 block
+    MXFP4_PREFILL_KERNEL<kUp | kModeGated><<<g, b, 0, stream>>>(p, 0, (out_strips + kTilesB / 2 - 1) / (kTilesB / 2), none);
   } else if (p.rows_out) {
     MXFP4_PREFILL_KERNEL<kUp><<<g, b, 0, stream>>>(p, 0, (out_strips + kTilesB - 1) / kTilesB, none);
   } else {

@@ -36,6 +36,8 @@ int moe_shape(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, in
   if (tokens > kMaxPairs / top_k) return MXFP4_ERR_SHAPE;
   if (one_weight(inner * (gated ? 2 : 1), hidden) > kMaxInt || one_weight(hidden, inner) > kMaxInt)
     return MXFP4_ERR_SHAPE;
+  // x in MXFP4 through 32-bit buffer offsets
+  if (tokens * cdiv(hidden, 128) * 64 > kMaxInt) return MXFP4_ERR_SHAPE;
   // workgroups of a launch: 16-row strips times 32-column blocks or K-steps
   const int64_t strips = (tokens * top_k + 15 * experts) / 16;
   const int64_t widest = (hidden > inner ? hidden : inner) / 32 + 16;

@@ -47,11 +47,15 @@ struct GemmArgs {
   const uint16_t* res;
   int64_t ldr;
   int res_vec;
-  // The experts' products (large-M kernel): the plan's row tiles, the bytes
+  // The experts' products (large-M kernel): the plan's row tiles (the first
+  // product's rows with their tokens, a and as then row by row, a_bytes and
+  // as_bytes long), the bytes
   // from one expert's weight and scales to the next one's, and where the
   // first product's rows go (GEMM layouts with rows_kt K-steps).
   const struct MoeHead* head;
   const struct MoeBlock* blocks;
+  const int32_t* row_tokens;
+  uint32_t a_bytes, as_bytes;
   int64_t w_expert, ws_expert;
   uint8_t *rows_out, *rows_scales;
   int rows_kt, rows_g;
@@ -87,8 +91,7 @@ hipError_t launch_prefill_tiles_128(const GemmArgs& p, int grid, const PrefillSp
 // The same with an epilogue, and over a plan's row tiles.
 hipError_t launch_prefill_act_tiles_256(const GemmArgs& p, int grid, const PrefillSplit& sk, hipStream_t stream);
 hipError_t launch_prefill_act_tiles_128(const GemmArgs& p, int grid, const PrefillSplit& sk, hipStream_t stream);
-hipError_t launch_prefill_experts_256(const GemmArgs& p, int grid, hipStream_t stream);
-hipError_t launch_prefill_experts_128(const GemmArgs& p, int grid, hipStream_t stream);
+hipError_t launch_prefill_experts(const GemmArgs& p, int grid, hipStream_t stream);
 // Workspace the large-M kernel's split schedule takes for this shape on up
 // to 256 compute units (0: whole tiles only).
 size_t gemm_prefill_workspace_bytes(int64_t M, int64_t N, int64_t K);
