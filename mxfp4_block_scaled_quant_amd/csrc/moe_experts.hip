@@ -33,11 +33,16 @@ constexpr int kChunk = 1024;  // pairs that one workgroup counts
 
 // ------------------------------------------------------------ the workspace
 
+// Mean rows of an expert up to which its weights are streamed once per block
+// of up to 64 rows; with more the products run on tiles of 256 rows.
+constexpr int64_t kStreamRows = 48;
+inline bool moe_tiles(int64_t pairs, int64_t experts) { return pairs / experts > kStreamRows; }
+
 // Where things are in the workspace (byte offsets).  rows: 16 per strip, at
 // most as many strips as pairs, and 15 rows of padding per expert met.
 struct MoeLayout {
   int64_t strips, max_blocks;
-  size_t head, blocks, counts, pos, src, tok, a, as, h, hs, part, total;
+  size_t head, blocks, counts, pos, src, tok, a, as, h, hs, part, exps, total;
 };
 
 MoeLayout moe_layout(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, int64_t inner) {
@@ -63,7 +68,8 @@ MoeLayout moe_layout(int64_t tokens, int64_t top_k, int64_t experts, int64_t hid
   l.as = take(tokens * cdiv(kt1, 4) * 16);
   l.h = take(l.strips * kt2 * 1024);
   l.hs = take(l.strips * cdiv(kt2, 4) * 256);
-  l.part = take(l.strips * 16 * hidden * 4);
+  l.part = take(l.strips * 16 * hidden * (moe_tiles(pairs, experts) ? 2 : 4));
+  l.exps = take(moe_tiles(pairs, experts) ? l.strips * 16 * cdiv(hidden, 64) : 0);
   l.total = at;
   return l;
 }
@@ -820,10 +826,6 @@ hipError_t launch_down_sum(const MoeArgs& p, const MoeLayout& l, bool few, int64
   return hipGetLastError();
 }
 
-// Mean rows of an expert up to which its weights are streamed once per block
-// of up to 64 rows; with more the products run on tiles of 256 rows.
-constexpr int64_t kStreamRows = 48;
-
 // The large-M kernel over the plan's row tiles.
 hipError_t launch_tiles(const GemmArgs& p, int64_t max_blocks, hipStream_t stream) {
   const int out_strips = p.gated ? p.Ns / 2 : p.Ns;
@@ -834,32 +836,69 @@ hipError_t launch_tiles(const GemmArgs& p, int64_t max_blocks, hipStream_t strea
 
 // --------------------------------------------------------------- the combine
 
-// A token's rows, weighted and added in the order of its choices: four
-// columns a thread.
-__global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs p, const int32_t* pos, const float* part) {
-  const int64_t quads = p.hidden / 4;
+// A token's rows, weighted and added in the order of its choices: 16 bytes of
+// each a thread (four fp32 columns, or eight of fp16 with an exponent per 64,
+// epilogue_part's), the rows of up to eight choices under way together.
+template <bool HALF>
+__global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs p, const int32_t* pos, const void* part,
+                                                          const uint8_t* exps) {
+  constexpr int kCols = HALF ? 8 : 4;
+  const int64_t pieces = p.hidden / kCols;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= p.tokens * quads) return;
-  const int64_t t = i / quads;
-  const int n = (int)(i % quads) * 4;
-  v4f v = {0.f, 0.f, 0.f, 0.f};
+  if (i >= p.tokens * pieces) return;
+  const int64_t t = i / pieces;
+  const int n = (int)(i % pieces) * kCols;
+  float v[kCols];
   if (p.residual) {
-    const uint2 r = *reinterpret_cast<const uint2*>(p.residual + t * p.ldr + n);
-    v = (v4f){__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
-              __uint_as_float(r.y & 0xFFFF0000u)};
-  }
-  for (int j = 0; j < p.top_k; ++j) {
-    const int row = pos[t * p.top_k + j];
-    if (row < 0) continue;
-    const float w = p.weights[t * p.ldw + j];
-    const v4f y = *reinterpret_cast<const v4f*>(part + (int64_t)row * p.hidden + n);
+    uint32_t r[kCols / 2];
+    __builtin_memcpy(r, __builtin_assume_aligned(p.residual + t * p.ldr + n, 8), kCols * 2);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] += w * y[q];
+    for (int q = 0; q < kCols / 2; ++q)
+      v[2 * q] = __uint_as_float(r[q] << 16), v[2 * q + 1] = __uint_as_float(r[q] & 0xFFFF0000u);
+  } else {
+#pragma unroll
+    for (int q = 0; q < kCols; ++q) v[q] = 0.f;
   }
-  uint2 o;
-  o.x = pack_bf16x2(v[0], v[1]);
-  o.y = pack_bf16x2(v[2], v[3]);
-  *reinterpret_cast<uint2*>(p.out + t * p.ldo + n) = o;
+  const int ldx = (p.hidden + 63) >> 6;
+  for (int j0 = 0; j0 < p.top_k; j0 += 8) {
+    int row[8];
+    float w[8];
+    int4 y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool in = j0 + j < p.top_k;
+      row[j] = in ? pos[t * p.top_k + j0 + j] : -1;
+      w[j] = in ? p.weights[t * p.ldw + j0 + j] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (row[j] >= 0) {
+        y[j] = *reinterpret_cast<const int4*>(static_cast<const uint8_t*>(part) +
+                                              ((int64_t)row[j] * p.hidden + n) * (HALF ? 2 : 4));
+        if constexpr (HALF) w[j] *= __uint_as_float(((uint32_t)exps[(int64_t)row[j] * ldx + (n >> 6)] - 14u) << 23);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (row[j] < 0) continue;
+      const int word[4] = {y[j].x, y[j].y, y[j].z, y[j].w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if constexpr (HALF) {
+          typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+          const v2h h = __builtin_bit_cast(v2h, word[q]);
+          v[2 * q] = fmaf(w[j], (float)h[0], v[2 * q]);
+          v[2 * q + 1] = fmaf(w[j], (float)h[1], v[2 * q + 1]);
+        } else {
+          v[q] = fmaf(w[j], __uint_as_float((uint32_t)word[q]), v[q]);
+        }
+      }
+    }
+  }
+  uint32_t o[kCols / 2];
+#pragma unroll
+  for (int q = 0; q < kCols / 2; ++q) o[q] = pack_bf16x2(v[2 * q], v[2 * q + 1]);
+  __builtin_memcpy(__builtin_assume_aligned(p.out + t * p.ldo + n, 8), o, kCols * 2);
 }
 
 }  // namespace
@@ -881,7 +920,7 @@ hipError_t launch_moe(const MoeArgs& p, hipStream_t stream) {
   plan.src = reinterpret_cast<int32_t*>(p.work + l.src);
   plan.tok = reinterpret_cast<int32_t*>(p.work + l.tok);
   const int64_t mean = pairs / p.experts;
-  const bool tiles = mean > kStreamRows;
+  const bool tiles = moe_tiles(pairs, p.experts);
   const int mt = mean <= 10 ? 1 : mean <= 24 ? 2 : 4;
   const int block_strips = tiles ? 16 : mt;
   const int kt1 = (int)cdiv(p.hidden, 128), g1 = (int)cdiv(kt1, 4);
@@ -938,7 +977,7 @@ hipError_t launch_moe(const MoeArgs& p, hipStream_t stream) {
     d.a = p.work + l.h, d.as = p.work + l.hs, d.w = p.down, d.ws = p.down_scales, d.bias = p.down_bias;
     d.N = p.hidden, d.K = p.inner, d.Kt = kt2, d.G = g2, d.Ns = p.hidden / 16;
     d.w_expert = (int64_t)d.Ns * kt2 * 1024, d.ws_expert = (int64_t)d.Ns * g2 * 256;
-    d.out = part, d.ldo = p.hidden, d.out_f32 = 1;
+    d.out = part, d.out_scales = p.work + l.exps;
     e = launch_tiles(d, max_blocks, stream);
     if (e != hipSuccess) return e;
   } else {
@@ -956,8 +995,12 @@ hipError_t launch_moe(const MoeArgs& p, hipStream_t stream) {
                   : launch_stream<4, 2, false>(d, max_blocks, stream);
     if (e != hipSuccess) return e;
   }
-  const int64_t n = p.tokens * (p.hidden / 4);
-  moe_combine_kernel<<<dim3((unsigned)cdiv(n, 256)), 256, 0, stream>>>(p, plan.pos, part);
+  if (tiles)
+    moe_combine_kernel<true><<<dim3((unsigned)cdiv(p.tokens * (p.hidden / 8), 256)), 256, 0, stream>>>(
+        p, plan.pos, part, p.work + l.exps);
+  else
+    moe_combine_kernel<false><<<dim3((unsigned)cdiv(p.tokens * (p.hidden / 4), 256)), 256, 0, stream>>>(
+        p, plan.pos, part, nullptr);
   return hipGetLastError();
 }
 

@@ -143,8 +143,15 @@ def requantised(v, err):
     return ref.reshape(v.shape), dev.reshape(v.shape)
 
 
-def moe(x_bf16, ids, weights, up, down, up_bias=None, down_bias=None, act="silu", gated=True, residual_bf16=None):
-    """up, down: (qw [E, N, K/2], sw [E, N, K/32]); weights fp64.  (out fp64, bound before the cast)."""
+def moe(x_bf16, ids, weights, up, down, up_bias=None, down_bias=None, act="silu", gated=True, residual_bf16=None,
+        half=False):
+    """up, down: (qw [E, N, K/2], sw [E, N, K/32]); weights fp64.  (out fp64, bound before the cast).
+
+    half: a choice's row may be held in fp16 with one exponent per 64 columns
+    before it is weighted, its largest magnitude scaled into [2^14, 2^15):
+    fp16 keeps 11 bits, so a value is half a step off, 2^-11 of itself, down to
+    fp16's smallest normal number 2^-14, which is 2^-28 of the largest at
+    least; below that half a step is 2^-25, 2^-39 of the largest."""
     x = dequantised(x_bf16)
     T, k = ids.shape
     E = up[0].shape[0]
@@ -165,9 +172,11 @@ def moe(x_bf16, ids, weights, up, down, up_bias=None, down_bias=None, act="silu"
         if down_bias is not None:
             d = F.bf16_to_f64(down_bias[e])
             y, bound = y + d, bound + TOL * np.abs(d)
+        if half:
+            bound = bound + 2.0 ** -11 * (np.abs(y) + bound) + 2.0 ** -39 * np.abs(y).max(1, keepdims=True)
         for n, (t, j) in enumerate(at):
             out[t] += weights[t, j] * y[n]
             err[t] += abs(weights[t, j]) * bound[n]
             size[t] += np.abs(weights[t, j] * y[n])
-    # a product and a sum per choice, in fp32 (a term may be held with 2^-20 of itself less)
-    return out, err + (2 * k * EPS + 2.0 ** -20) * size
+    # a product and a sum per choice, in fp32, and the weight's product with the row's exponent
+    return out, err + (2 * k + 1) * EPS * size
