@@ -278,8 +278,11 @@ __device__ __forceinline__ const T* expert_of(const T* base, const Tile& tl, int
 // its four units and for the scales, out of range for a row of padding.  The
 // unit's LDS slots hold its rows one after the other, four 16-byte blocks
 // each (so that four lanes read 64 consecutive bytes), block b of row r in
-// slot 4 r + (b ^ (r / 4 % 4)): the exclusive or spreads the 16 rows that a
-// fragment read takes of one block over all LDS banks.
+// slot 4 r + (b ^ (-(r / 4) % 4)): a fragment read then finds each of its
+// 16-lane groups (lanes 0-3, 12-15 and 20-27; 4-11, 16-19 and 28-31; and so on)
+// in 16 different slots of the 256 bytes that the banks span.  (With r / 4 in
+// place of -(r / 4) two lanes of a group met in every bank: 4 cycles more a
+// read.)
 struct Rows {
   uint32_t unit[kLoadsPerWave], scale;
 };
@@ -288,7 +291,7 @@ __device__ __forceinline__ Rows rows_of(const GemmArgs& p, const Tile& tl, int w
   Rows o;
   if constexpr (is_rows(MODE)) {
     const int l = (int)lane_here();
-    const uint32_t block = (uint32_t)((l & 3) ^ (l >> 4));
+    const uint32_t block = (uint32_t)((l & 3) ^ (-(l >> 4) & 3));
 #pragma unroll
     for (int q = 0; q < kLoadsPerWave; ++q) {
       const int unit = wv * kLoadsPerWave + q;  // (weight units: not used)
@@ -1184,18 +1187,18 @@ __device__ __forceinline__ void epilogue_part(const GemmArgs& p, const Tile& tl,
 #pragma unroll
   for (int i = 0; i < kWM; ++i) {
     float v[kWN][4];
-    uint32_t top = 0;
+    float top = 0.f;
 #pragma unroll
     for (int j = 0; j < kWN; ++j) {
       float b[4];
       bias_floats(bl[j], b);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        v[j][r] = acc[i][j][r] + b[r];
-        top = max(top, __float_as_uint(v[j][r]) & 0x7FFFFFFFu);
-      }
+      for (int r = 0; r < 4; ++r) v[j][r] = acc[i][j][r] + b[r];
+      // (one three-way maximum of magnitudes per pair)
+      top = fmaxf(fmaxf(top, fabsf(v[j][0])), fabsf(v[j][1]));
+      top = fmaxf(fmaxf(top, fabsf(v[j][2])), fabsf(v[j][3]));
     }
-    const uint32_t e = max(row_max(top) >> 23, 15u);
+    const uint32_t e = max(row_max(__float_as_uint(top)) >> 23, 15u);
     const float f = __uint_as_float((268u - e) << 23);
 #pragma unroll
     for (int j = 0; j < kWN; ++j) {
@@ -1217,8 +1220,10 @@ __device__ __forceinline__ void epilogue_part(const GemmArgs& p, const Tile& tl,
     const int nrows = __builtin_amdgcn_readfirstlane(max(0, min(16, row_end<MODE>(p, tl) - rb)));
     const __amdgpu_buffer_rsrc_t ro = make_rsrc(out + (int64_t)rb * p.N * 2, (uint32_t)(nrows * p.N * 2));
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.out_scales + (int64_t)rb * ldx, (uint32_t)nrows * ldx);
-    __builtin_amdgcn_raw_buffer_store_b128(r0, ro, voff, 0, 0);
-    __builtin_amdgcn_raw_buffer_store_b128(r1, ro, n < p.N ? voff + (uint32_t)(8 * p.N) * 2u : kOOB, 0, 0);
+    // (whole lines, non-temporal: the rows of a long prompt outgrow every cache)
+    __builtin_amdgcn_raw_buffer_store_b128(r0, ro, voff, 0, kStagedStoreAux);
+    __builtin_amdgcn_raw_buffer_store_b128(r1, ro, n < p.N ? voff + (uint32_t)(8 * p.N) * 2u : kOOB, 0,
+                                           kStagedStoreAux);
     __builtin_amdgcn_raw_buffer_store_b8((uint8_t)e, rx, xoff, 0, 0);
   }
 }
@@ -1410,7 +1415,7 @@ __global__ __launch_bounds__(512, 1) void MXFP4_PREFILL_KERNEL(GemmArgs p, int t
   const uint32_t lane16 = lane * 16;
   ReadAddr ra;
   ra.a = lds0 + wm * kWM * 4096 +
-         (is_rows(MODE) ? (uint32_t)((lane & 15) * 4 + ((lane >> 4) ^ ((lane >> 2) & 3))) * 16u : lane16);
+         (is_rows(MODE) ? (uint32_t)((lane & 15) * 4 + ((lane >> 4) ^ (-((lane & 15) >> 2) & 3))) * 16u : lane16);
   ra.b = lds0 + (kTilesA + wn * kWN) * 4096 + lane16;
 
   Pipe P;
