@@ -33,9 +33,13 @@ constexpr int kChunk = 1024;  // pairs that one workgroup counts
 
 // ------------------------------------------------------------ the workspace
 
-// Mean rows of an expert up to which its weights are streamed once per block
-// of up to 64 rows; with more the products run on tiles of 256 rows.
-constexpr int64_t kStreamRows = 48;
+// Mean rows of an expert up to which its weights are streamed into registers,
+// once per block of one or two 16-row tiles; with more the products run on
+// tiles of 256 rows.  Measured (us, streamed / tiles; experts, choices, hidden,
+// inner): 64, 8, 5120, 1024 with mean 12.5 133 / 153, 20 159 / 161, 25 (four
+// row tiles) 195 / 164; 128, 8, 2048, 768 with mean 16 89 / 117, 24 99 / 121,
+// 32 193 / 123; 32, 4, 5120, 1504 with mean 20 121 / 135, 25 154 / 137.
+constexpr int64_t kStreamRows = 24;
 inline bool moe_tiles(int64_t pairs, int64_t experts) { return pairs / experts > kStreamRows; }
 
 // Where things are in the workspace (byte offsets).  rows: 16 per strip, at
@@ -435,7 +439,7 @@ __device__ __forceinline__ void finish_rows(const ProductArgs& p, float* red, co
 // half; else two), its KW waves the groups of 4 K-steps in turn.  All of a
 // group's loads go out before its first product.  The waves' partial sums
 // meet in LDS and are added in wave order.
-constexpr int stream_waves(int mt) { return mt == 1 ? 12 : mt == 2 ? 8 : 4; }
+constexpr int stream_waves(int mt) { return mt == 1 ? 12 : 8; }
 
 template <int MT, int NS, bool UP>
 __global__ __launch_bounds__(64 * stream_waves(MT)) void moe_stream_kernel(ProductArgs p) {
@@ -921,7 +925,7 @@ hipError_t launch_moe(const MoeArgs& p, hipStream_t stream) {
   plan.tok = reinterpret_cast<int32_t*>(p.work + l.tok);
   const int64_t mean = pairs / p.experts;
   const bool tiles = moe_tiles(pairs, p.experts);
-  const int mt = mean <= 10 ? 1 : mean <= 24 ? 2 : 4;
+  const int mt = mean <= 10 ? 1 : 2;
   const int block_strips = tiles ? 16 : mt;
   const int kt1 = (int)cdiv(p.hidden, 128), g1 = (int)cdiv(kt1, 4);
   const int kt2 = (int)cdiv(p.inner, 128), g2 = (int)cdiv(kt2, 4);
@@ -981,18 +985,14 @@ hipError_t launch_moe(const MoeArgs& p, hipStream_t stream) {
     e = launch_tiles(d, max_blocks, stream);
     if (e != hipSuccess) return e;
   } else {
-    e = mt == 1 ? launch_up<1>(u, p.gated, max_blocks, stream)
-        : mt == 2 ? launch_up<2>(u, p.gated, max_blocks, stream)
-                  : launch_up<4>(u, p.gated, max_blocks, stream);
+    e = mt == 1 ? launch_up<1>(u, p.gated, max_blocks, stream) : launch_up<2>(u, p.gated, max_blocks, stream);
     if (e != hipSuccess) return e;
     ProductArgs d{};
     d.head = plan.head, d.blocks = plan.blocks;
     d.a = p.work + l.h, d.as = p.work + l.hs, d.w = p.down, d.ws = p.down_scales, d.bias = p.down_bias;
     d.Kt = kt2, d.G = g2, d.Ns = p.hidden / 16, d.cols = p.hidden / 32;
     d.part = part, d.hidden = p.hidden;
-    e = mt == 1 ? launch_stream<1, 2, false>(d, max_blocks, stream)
-        : mt == 2 ? launch_stream<2, 2, false>(d, max_blocks, stream)
-                  : launch_stream<4, 2, false>(d, max_blocks, stream);
+    e = mt == 1 ? launch_stream<1, 2, false>(d, max_blocks, stream) : launch_stream<2, 2, false>(d, max_blocks, stream);
     if (e != hipSuccess) return e;
   }
   if (tiles)

@@ -48,8 +48,8 @@ def device(p):
 def check(p, out, act="silu", gated=True):
     ref, err = D.moe(p["x"], p["ids"], p["weights"].astype(np.float64), p["up"], p["down"], p["up_bias"],
                      p["down_bias"], act, gated, p["residual"],
-                     # (experts of more than 48 rows on average: the tiled kernels)
-                     half=p["ids"].size // p["up"][0].shape[0] > 48)
+                     # (experts of more than 24 rows on average: the tiled kernels)
+                     half=p["ids"].size // p["up"][0].shape[0] > 24)
     got = F.bf16_to_f64(host_bf16_bits(out))
     assert np.isfinite(got).all()
     # the last rounding: half a step of bf16, of a value that may be err off
