@@ -9,11 +9,12 @@ stream of the tensors' device.
 
 from __future__ import annotations
 
+from functools import lru_cache
 from typing import Optional, Tuple
 
 import torch
 
-from . import MXFP4Weight, _check, _require_bytes, _require_cuda, _require_weight, lib
+from . import MXFP4Weight, _check, _require_bytes, _require_cuda, _require_weight, lib, weight_bytes, weight_scale_bytes
 from .mla import _BF16, _F32, _I32, _addr, _raw_stream, _require
 
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
@@ -78,6 +79,23 @@ def moe_route(logits: torch.Tensor, top_k: int, bias: Optional[torch.Tensor] = N
     return weights, ids
 
 
+# Sizes are functions of the shapes alone and asked for once per shape (a call
+# through ctypes costs a microsecond).
+_weight_bytes = lru_cache(maxsize=256)(lambda batch, N, K: (weight_bytes(batch, N, K), weight_scale_bytes(batch, N, K)))
+_moe_bytes = lru_cache(maxsize=1024)(lambda *shape: int(lib().mxfp4_moe_workspace_bytes(*shape)))
+_U8 = torch.uint8
+
+
+def _weight_ok(w: torch.Tensor, ws: torch.Tensor, batch: int, N: int, K: int, dev: torch.device) -> bool:
+    data, scales = _weight_bytes(batch, N, K)
+    return (w.dtype is _U8 and w.device == dev and w.is_contiguous() and w.numel() >= data > 0
+            and ws.dtype is _U8 and ws.device == dev and ws.is_contiguous() and ws.numel() >= scales)
+
+
+def _rows_ok(t: torch.Tensor, dtype: torch.dtype, T: int, n: int, dev: torch.device) -> bool:
+    return t.dtype is dtype and t.device == dev and t.shape == (T, n) and (t.stride(1) == 1 or n == 1)
+
+
 def mxfp4_moe_workspace_bytes(T: int, top_k: int, experts: int, hidden: int, inner: int) -> int:
     return int(lib().mxfp4_moe_workspace_bytes(T, top_k, experts, hidden, inner))
 
@@ -85,7 +103,7 @@ def mxfp4_moe_workspace_bytes(T: int, top_k: int, experts: int, hidden: int, inn
 def _workspace(workspace: Optional[torch.Tensor], need: int, dev: torch.device):
     """(tensor to keep alive, its address, its bytes)"""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        workspace = torch.empty_strided((need,), (1,), dtype=_U8, device=dev) if need else None
     else:
         _require_bytes(workspace, "workspace", need, dev)
     return workspace, _addr(workspace), 0 if workspace is None else workspace.numel()
@@ -117,13 +135,16 @@ def mxfp4_moe(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, up: MXF
     if down.batch != E or down.N != H or up.N != (2 * I if gated else I):
         raise ValueError(f"up [{E}, {up.N}, {H}] and down [{down.batch}, {down.N}, {I}] are not the two weights of "
                          f"{'gated ' if gated else ''}experts")
-    ldx = _require(x, "x", _BF16, (-1, H), dev)[0]
     T = x.shape[0]
-    ldi = _require(ids, "ids", _I32, (T, -1), dev)[0]
-    k = ids.shape[1]
-    ldw = _require(weights, "weights", _F32, (T, k), dev)[0]
-    _require_weight(up.w_pre, up.ws_pre, up.N, H, dev, batch=E)
-    _require_weight(down.w_pre, down.ws_pre, H, I, dev, batch=E)
+    k = ids.shape[1] if ids.dim() == 2 else -1
+    if not (_rows_ok(x, _BF16, T, H, dev) and _rows_ok(ids, _I32, T, k, dev) and _rows_ok(weights, _F32, T, k, dev)
+            and _weight_ok(up.w_pre, up.ws_pre, E, up.N, H, dev) and _weight_ok(down.w_pre, down.ws_pre, E, H, I, dev)):
+        _require(x, "x", _BF16, (-1, H), dev)
+        _require(ids, "ids", _I32, (T, -1), dev)
+        _require(weights, "weights", _F32, (T, k), dev)
+        _require_weight(up.w_pre, up.ws_pre, up.N, H, dev, batch=E)
+        _require_weight(down.w_pre, down.ws_pre, H, I, dev, batch=E)
+    ldx, ldi, ldw = x.stride(0), ids.stride(0), weights.stride(0)
     for bias, name, n in ((up_bias, "up_bias", up.N), (down_bias, "down_bias", H)):
         if bias is not None:
             _require(bias, name, _BF16, (E, n), dev)
@@ -131,10 +152,11 @@ def mxfp4_moe(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, up: MXF
                 raise ValueError(f"{name} must be contiguous")
     ldr = 0 if residual is None else _require(residual, "residual", _BF16, (T, H), dev)[0]
     if out is None:
-        out = torch.empty((T, H), dtype=_BF16, device=dev)
-    ldo = _require(out, "out", _BF16, (T, H), dev)[0]
+        out, ldo = torch.empty_strided((T, H), (H, 1), dtype=_BF16, device=dev), H
+    else:
+        ldo = _require(out, "out", _BF16, (T, H), dev)[0]
     code = _code(ACTIVATIONS, "activation", activation)
-    need = int(lib().mxfp4_moe_workspace_bytes(T, k, E, H, I))
+    need = _moe_bytes(T, k, E, H, I)
     workspace, work, size = _workspace(workspace, need, dev)
     status = lib().mxfp4_moe(
         x.data_ptr(), ldx, ids.data_ptr(), ldi, weights.data_ptr(), ldw, up.w_pre.data_ptr(), up.ws_pre.data_ptr(),
@@ -170,15 +192,17 @@ def mxfp4_linear_act(x: torch.Tensor, w_pre: torch.Tensor, ws_pre: torch.Tensor,
     if gated and N % 32:
         raise ValueError(f"a gated weight has a multiple of 32 rows, got {N}")
     cols = N // 2 if gated else N
-    _require_weight(w_pre, ws_pre, N, K, dev)
+    if not _weight_ok(w_pre, ws_pre, 1, N, K, dev):
+        _require_weight(w_pre, ws_pre, N, K, dev)
     if bias is not None:
         _require(bias, "bias", _BF16, (N,), dev)
     ldr = 0 if residual is None else _require(residual, "residual", _BF16, (M, cols), dev)[0]
     if out_dtype is not _BF16 and out_dtype is not _F32:
         raise ValueError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
     if out is None:
-        out = torch.empty((M, cols), dtype=out_dtype, device=dev)
-    ldo = _require(out, "out", out_dtype, (M, cols), dev)[0]
+        out, ldo = torch.empty_strided((M, cols), (cols, 1), dtype=out_dtype, device=dev), cols
+    else:
+        ldo = _require(out, "out", out_dtype, (M, cols), dev)[0]
     code = _code(ACTIVATIONS, "activation", activation)
     need = int(lib().mxfp4_linear_act_workspace_bytes(M, N, K))
     workspace, work, size = _workspace(workspace, need, dev)
