@@ -929,7 +929,8 @@ static hipError_t launch_decode_persist_gated(const GemmArgs& p, int kw, hipStre
   constexpr int D = 1;  // steps in flight per wave (two strips each)
   const int Nu = p.Ns / 2;
   const int grid = Nu < p.cus ? Nu : p.cus;
-  const size_t lds = 2 * reduce_lds_bytes<MT, 2, 12>();
+  constexpr size_t lds = 2 * reduce_lds_bytes<MT, 2, 12>();
+  static_assert(lds <= 160 * 1024, "LDS per workgroup");
   gemm_decode_persist_kernel<MT, 12, D, kASrcGemm, 2, 1, true><<<grid, 64 * kw, lds, stream>>>(p);
   return hipGetLastError();
 }
@@ -942,14 +943,20 @@ template <int MT>
 static hipError_t launch_decode_gated(const GemmArgs& p, int kw, int gpw, hipStream_t stream) {
   constexpr int MAXW = MT == 1 ? 16 : MT == 4 ? 12 : 8;
   const int ov = get_gemm_path_override();
-  {
+  // (four row tiles' two reduction areas would not fit the LDS; with one and a
+  // second barrier a step, N = 34816, K = 5120, M = 64 took 47.1 us against 37.4)
+  if constexpr (MT <= 3) {
     if (p.G <= 12 && (ov == 7 || (ov != 8 && decode_persist_fp4_pays(p.M, p.Ns, p.cus, p.G))))
       return launch_decode_persist_gated<MT>(p, p.G, stream);
   }
   if constexpr (MT == 1) {
     if (gpw >= 2 && p.Ns < 2 * p.cus) return launch_decode_t<MT, 2, 2, MAXW>(p, kw, gpw, stream);
+    // (at most 8 waves, as above: N = 34816, K = 5120, M = 8 / 16: 22.4 / 23.6 ->
+    // 21.8 / 23.0 us)
+    const int g8 = (p.G + 7) / 8;
+    return launch_decode_t<MT, 2, 1, 8, false>(p, (p.G + g8 - 1) / g8, g8, stream);
   }
-  return launch_decode_t<MT, 2, 1, MAXW, false>(p, kw, gpw, stream);
+  if constexpr (MT > 1) return launch_decode_t<MT, 2, 1, MAXW, false>(p, kw, gpw, stream);
 }
 #endif
 
@@ -1085,12 +1092,6 @@ template <int NS, int GPR>
 static hipError_t launch_linear_t(const GemmArgs& p, int kw, int gpw, hipStream_t stream) {
   const dim3 grid((unsigned)((p.Ns + NS - 1) / NS));
   const size_t lds = reduce_lds_bytes<1, NS, 16>();
-  if constexpr (kAct && NS == 2) {
-    if (p.gated) {
-      linear_decode_kernel<NS, GPR, 16, true><<<grid, 64 * kw, lds, stream>>>(p, gpw);
-      return hipGetLastError();
-    }
-  }
   linear_decode_kernel<NS, GPR, 16><<<grid, 64 * kw, lds, stream>>>(p, gpw);
   return hipGetLastError();
 }
@@ -1126,8 +1127,13 @@ hipError_t launch_linear_decode(const GemmArgs& p, hipStream_t stream) {
   if (p.M > kFusedRows) return hipErrorInvalidValue;
 #if MXFP4_DECODE_ACT
   if (p.gated) {
-    const int gpw = (p.G + 15) / 16;
-    return launch_linear_t<2, 1>(p, (p.G + gpw - 1) / gpw, gpw, stream);
+    // at most 8 waves (N = 34816, K = 5120, M = 1 / 2: 10 waves of one group
+    // 21.3 / 22.2, 5 of two 18.9 / 20.0, 4 of three 18.9 / 20.2 us)
+    const int gpw = (p.G + 7) / 8;
+    const int kw = (p.G + gpw - 1) / gpw;
+    linear_decode_kernel<2, 1, 8, true>
+        <<<dim3((unsigned)(p.Ns / 2)), 64 * kw, reduce_lds_bytes<1, 2, 8>(), stream>>>(p, gpw);
+    return hipGetLastError();
   }
 #endif
   // Up to 8192-wide K: at most 16 waves of one group each, one strip per

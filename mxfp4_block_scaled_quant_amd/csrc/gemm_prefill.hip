@@ -795,8 +795,9 @@ __device__ __forceinline__ void finish(const GemmArgs& p, const v4f (&acc)[kWN],
 }
 
 // The staged epilogue with an activation (mode 0, kModeAct): as
-// epilogue_staged, with the residual of the next 16-row block loaded while
-// one is finished.  With a gate a row of the wave is 8 kWN columns: kWN
+// epilogue_staged, with the residual of the next kAhead 16-row blocks under
+// way while one is finished (in the fragments' registers, which are free
+// here).  With a gate a row of the wave is 8 kWN columns: kWN
 // lanes of 16 bytes, and at 128-wide tiles only the first half of the lanes
 // has a piece.
 template <int MODE, int CLASS>
@@ -820,7 +821,8 @@ __device__ __forceinline__ void epilogue_staged_act(const GemmArgs& p, const Til
   const uint32_t raddr = wst + (uint32_t)(prow & 15) * kEpiRowB + (uint32_t)(lane % kLanes) * 16;
   const uint32_t voff = n < ncols && prow < 16 ? (uint32_t)(prow * p.ldo + n) * 2 : kOOB;
   uint8_t* const out = reinterpret_cast<uint8_t*>(p.out);
-  v2i res[2][kJ];
+  constexpr int kAhead = 4;
+  v2i res[kAhead][kJ];
   auto fetch = [&](int i, v2i (&r)[kJ]) {
     const int rb = row0 + i * 16;
     const int nrows = __builtin_amdgcn_readfirstlane(max(0, min(16, row_end<MODE>(p, tl) - rb)));
@@ -828,21 +830,26 @@ __device__ __forceinline__ void epilogue_staged_act(const GemmArgs& p, const Til
     for (int j = 0; j < kJ; ++j) load_residual_bits<false>(p, rb, nrows, nd + j * 16, ncols, lane, r[j]);
   };
 #pragma unroll
-  for (int j = 0; j < kJ; ++j) res[0][j] = res[1][j] = (v2i){0, 0};
-  if (p.res) fetch(0, res[0]);
+  for (int h = 0; h < kAhead; ++h)
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) res[h][j] = (v2i){0, 0};
+  if (p.res) {
+#pragma unroll
+    for (int h = 0; h < kAhead; ++h) fetch(h, res[h]);
+  }
 #pragma unroll
   for (int i = 0; i < kWM; ++i) {
-    if (p.res && i + 1 < kWM) fetch(i + 1, res[(i + 1) & 1]);
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
       float v[4];
-      finish<MODE, CLASS>(p, acc[i], bl, j, res[i & 1][j], v);
+      finish<MODE, CLASS>(p, acc[i], bl, j, res[i % kAhead][j], v);
       const v2i d = {(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])};
       if (j == 0) ds_write8<0>(waddr, d);
       if (j == 1) ds_write8<32>(waddr, d);
       if (j == 2) ds_write8<64>(waddr, d);
       if (j == 3) ds_write8<96>(waddr, d);
     }
+    if (p.res && i + kAhead < kWM) fetch(i + kAhead, res[i % kAhead]);
     v4i r0, r1;
     ds_read16<0>(r0, raddr);
     if constexpr (kPieces == 2) {

@@ -67,6 +67,21 @@ def test_every_kernel_form(path, act, gated, bias, residual):
         run(330, 1120, 1056, act, gated, bias, residual, path=path)
 
 
+@pytest.mark.parametrize("M", [1, 4, 9, 16, 17, 32, 33, 48, 49, 64])
+@pytest.mark.parametrize("path", [0, 7, 8])
+def test_row_tiles_of_the_small_kernels(M, path):
+    need_gpu()
+    run(M, 1088, 5152, "silu", True, True, True, path=path)
+    run(M, 1088, 2080, "silu", True, False, False, path=path)
+    run(M, 1088, 5152, "gelu", False, True, True, path=path)
+
+
+def test_gate_of_many_strips():
+    """A shape that the persistent form takes without a gate."""
+    need_gpu()
+    run(64, 12288, 4640, "silu", True, False, False, out_dtypes=(torch.bfloat16,))
+
+
 def test_without_an_epilogue_it_is_the_linear():
     need_gpu()
     for M, N, K in ((1, 1024, 1024), (3, 96, 512), (40, 224, 512), (300, 544, 512)):
