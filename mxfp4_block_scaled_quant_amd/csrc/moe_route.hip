@@ -467,6 +467,203 @@ __device__ __forceinline__ Choice choice_of(const RouteArgs& p, int lanes2, bool
   return c;
 }
 
+// Batcher's odd-even merge sort of V values in registers, descending: merges of
+// P values, in each the exchanges over a distance of D = P, P / 2, ..., 1.
+template <int V, int P = 1, int D = P>
+__device__ __forceinline__ void sort_down(int (&k)[V]) {
+#pragma unroll
+  for (int i = D % P; i + D < V; ++i)
+    if ((i - D % P) / D % 2 == 0 && i / (2 * P) == (i + D) / (2 * P)) {
+      const int a = k[i], b = k[i + D];
+      k[i] = max(a, b);
+      k[i + D] = min(a, b);
+    }
+  if constexpr (D > 1)
+    sort_down<V, P, D / 2>(k);
+  else if constexpr (2 * P < V)
+    sort_down<V, 2 * P>(k);
+}
+
+// Many tokens: 16 lanes a token, V experts each, expert 64 (r / 4) + 4 lane +
+// r % 4 in register r (so that the lanes read whole lines).  Each lane sorts its
+// keys once; a round then is the largest of the 16 heads (four DPP steps), and
+// the lane that holds it moves its list up by one.  A key is the score's order
+// with its last four bits replaced by the register; bf16 logits that decide
+// by themselves keep all their bits above the expert's number.  Where two keys
+// next to each other are too close for what they leave out, or two lanes
+// have the same key, the wave chooses that token's experts again in 64 bits.
+// Bound by its vector instructions: 16001 tokens of 256 fp32 logits in 8 groups
+// take 21.3 us, 17.4 MB at 0.8 TB/s (kManyTokens has the wave per token's).
+constexpr int kGone = (int)0x80000000u;
+template <int V, bool SIGMOID, bool F32>
+__global__ __launch_bounds__(256) void moe_route_many_kernel(RouteArgs p, int lanes2, int wave_lanes2) {
+  constexpr float kLow = -__builtin_huge_valf();
+  constexpr float kBase = SIGMOID ? kMarginSigmoid : kMarginSoftmax;
+  __shared__ float gscore[16][17];
+  __shared__ int won[16][17];
+  const int lane = threadIdx.x & 15, slot = threadIdx.x >> 4;
+  const int64_t token = (int64_t)blockIdx.x * 16 + slot;
+  const bool live = token < p.tokens;
+  const int64_t row = (live ? token : p.tokens - 1) * p.ld;
+  float x[V], b[V];
+  float lo = -kLow, hi = kLow;
+#pragma unroll
+  for (int c = 0; c < V / 4; ++c) {
+    const int e = c * 64 + lane * 4;
+    const int at = e < p.experts ? e : p.experts - 4;  // (experts % 4 == 0)
+    if constexpr (F32) {
+      const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.logits) + row + at);
+      x[c * 4] = v.x, x[c * 4 + 1] = v.y, x[c * 4 + 2] = v.z, x[c * 4 + 3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.logits) + row + at);
+      x[c * 4] = __uint_as_float(v.x << 16), x[c * 4 + 1] = __uint_as_float(v.x & 0xFFFF0000u);
+      x[c * 4 + 2] = __uint_as_float(v.y << 16), x[c * 4 + 3] = __uint_as_float(v.y & 0xFFFF0000u);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < V; ++r) b[r] = 0.f;
+  if (p.bias) {
+#pragma unroll
+    for (int r = 0; r < V; ++r) {
+      const int e = r / 4 * 64 + lane * 4;
+      b[r] = p.bias[(e < p.experts ? e : p.experts - 4) + r % 4];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < V; ++r) {
+    lo = fminf(lo, b[r]);
+    hi = fmaxf(hi, b[r]);
+    const bool open = (r / 4) * 64 + lane * 4 < p.experts && x[r] > kLow && b[r] > kLow;
+    x[r] = open ? fminf(x[r], FLT_MAX) : kLow;
+  }
+  const bool by_logit = !p.bias || !__any(lo != hi || lo != __shfl(lo, 0));
+  const bool grouped = p.groups > 1;
+  const bool exact = !F32 && by_logit;  // the key holds the whole logit
+  float score[V];
+  if (!by_logit || grouped) {
+    if constexpr (SIGMOID) {
+#pragma unroll
+      for (int r = 0; r < V; ++r) score[r] = quotient(1.f, 1.f + exp_of(-x[r]));
+    } else {
+      float m = x[0];
+#pragma unroll
+      for (int r = 1; r < V; ++r) m = fmaxf(m, x[r]);
+      m = all_max<16>(m);
+      float z = 0.f;
+#pragma unroll
+      for (int r = 0; r < V; ++r) {
+        score[r] = x[r] > kLow ? exp_of(x[r] - m) : 0.f;
+        z += score[r];
+      }
+      const float inv = quotient(1.f, all_sum<16>(z));
+#pragma unroll
+      for (int r = 0; r < V; ++r) score[r] *= inv;
+    }
+#pragma unroll
+    for (int r = 0; r < V; ++r) score[r] = x[r] > kLow ? score[r] + b[r] : kLow;
+  }
+  bool unsure = false;
+  bool in[V / 4];
+#pragma unroll
+  for (int c = 0; c < V / 4; ++c) in[c] = true;
+  if (grouped) {
+    // 2^lanes2 lanes hold a group's experts of register quad c
+    float mine[V / 4];
+    const int per = 16 >> lanes2;  // groups of a quad
+#pragma unroll
+    for (int c = 0; c < V / 4; ++c) {
+      float a = kLow, d = kLow;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        d = fmaxf(d, fminf(a, score[c * 4 + q]));
+        a = fmaxf(a, score[c * 4 + q]);
+      }
+      merge_lanes<16>(a, d, lanes2);
+      mine[c] = (p.group_top == 2 && d > kLow) ? a + d : a;
+      const int g = c * per + (lane >> lanes2);
+      if ((lane & ((1 << lanes2) - 1)) == 0 && g < p.groups) gscore[slot][g] = mine[c];
+    }
+    __syncthreads();
+    int certain[V / 4] = {}, most[V / 4] = {};
+    for (int g = 0; g < p.groups; ++g) {
+      const float other = gscore[slot][g];
+#pragma unroll
+      for (int c = 0; c < V / 4; ++c) {
+        const float margin = 2 * kBase + 2 * kMarginRel * fabsf(mine[c]);
+        certain[c] += other > mine[c] + margin ? 1 : 0;
+        most[c] += !(other < mine[c] - margin) ? 1 : 0;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < V / 4; ++c) {
+      const bool there = c * per + (lane >> lanes2) < p.groups && mine[c] > kLow;
+      in[c] = there && most[c] - 1 < p.kept;
+      unsure = unsure || (there && !in[c] && certain[c] < p.kept);
+    }
+  }
+  int key[V];
+#pragma unroll
+  for (int r = 0; r < V; ++r) {
+    float v = x[r];
+    if (!by_logit) v = score[r];
+    int k;
+    if (exact)  // (FLT_MAX stands for +inf, above every finite bf16 number)
+      k = (order_of(v == FLT_MAX ? -kLow : v) & (int)0xFFFF0000u) | (0xFFFF - ((r / 4) * 64 + lane * 4 + r % 4));
+    else
+      k = (order_of(v) & ~15) | (15 - r);
+    key[r] = v > kLow && in[r / 4] ? k : kGone;
+  }
+  sort_down<V>(key);
+  int got = kGone;
+  uint64_t twice = 0;
+  for (int j = 0; j <= p.top_k; ++j) {
+    const int best = all_max<16>(key[0]);
+    const bool hit = key[0] == best && best != kGone;
+    const uint64_t votes = __ballot(hit), any = __ballot(best != kGone);
+    // more than one vote of a token: every field of 16 that has votes, less one
+    twice |= votes & (votes - (0x0001000100010001ull & ((any >> 15) & 0x0001000100010001ull)));
+    if (hit) won[slot][j] = exact ? 0xFFFF - (key[0] & 0xFFFF) : 15 - (key[0] & 15) + lane * 16;
+    got = lane == j ? best : got;
+#pragma unroll
+    for (int r = 0; r + 1 < V; ++r) {
+      const int kept = key[r], next = key[r + 1];  // (of two elements ?: takes an address, and the list leaves its registers)
+      key[r] = hit ? next : kept;
+    }
+    key[V - 1] = hit ? kGone : key[V - 1];
+  }
+  __syncthreads();
+  int id = -1;
+  if (lane < p.top_k && got != kGone) {
+    const int w = won[slot][lane];
+    id = exact ? w : (w & 15) / 4 * 64 + (w >> 4) * 4 + (w & 3);
+  }
+  if (!exact) {
+    const int next = __builtin_amdgcn_update_dpp(kGone, got, 0x101, 0xF, 0xF, false);  // lane + 1's
+    if (lane < p.top_k && next != kGone) {
+      if (by_logit) {
+        unsure = unsure || (got >> 4) == (next >> 4);
+      } else {
+        const float v = value_of(got), n = value_of(next);
+        unsure = unsure || !(v - n > kBase + (kMarginRel + 3.9e-6f) * fmaxf(fabsf(v), fabsf(n)));  // + 2^-18: the last bits
+      }
+    }
+  }
+  const uint64_t again = __ballot(unsure) | twice;
+  for (int s = 0; s < 4; ++s) {
+    if (!(again >> (16 * s) & 0xFFFF)) continue;
+    const int64_t t0 = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 6) * 4 + s;
+    const int64_t r0 = (t0 < p.tokens ? t0 : p.tokens - 1) * p.ld;
+    const int wl = threadIdx.x & 63;
+    float xs[V / 4], bs[V / 4];
+    const bool same = load_row<64, V / 4, F32>(p, r0, wl, xs, bs);
+    bool never = false;
+    const int other = choose<64, V / 4, SIGMOID, double>(choice_of(p, wave_lanes2, same), xs, bs, wl, never);
+    const int moved = __shfl(other, lane);
+    if ((wl >> 4) == s) id = moved;
+  }
+  store_choice<16, V, SIGMOID, F32>(p, token, row, live, lane, id, x);
+}
+
 // A wave per token.
 template <int V, bool SIGMOID, bool F32>
 __global__ __launch_bounds__(256) void moe_route_wave_kernel(RouteArgs p, int lanes2) {
@@ -505,6 +702,24 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs p, int lanes2)
   store_choice<L, V, SIGMOID, F32>(p, token, row, live, lane, id, x);
 }
 
+// log2 of the lanes that a group of `size` experts fills, -1 if it does not
+// fill whole lanes, a power of two of them.
+int group_lanes(int size, int V, int L) {
+  for (int n = 0; (1 << n) <= L; ++n)
+    if (size == V << n) return n;
+  return -1;
+}
+
+// Whether a call's rows suit moe_route_many_kernel: whole aligned quads, groups
+// that fill lanes of one quad of registers, and a lane for the first expert that
+// is not chosen.
+bool many_fits(const RouteArgs& p, bool f32) {
+  const uintptr_t a = f32 ? 15 : 7;
+  if (p.experts % 4 || p.top_k > 15 || p.groups > 16) return false;
+  if (((uintptr_t)p.logits & a) || (p.tokens > 1 && p.ld % 4)) return false;
+  return p.groups == 1 || group_lanes(p.experts / p.groups, 4, 16) >= 0;
+}
+
 #define MOE_ROUTE(KERNEL, GRID, ...)                                              \
   if (sigmoid && f32)                                                               \
     KERNEL<__VA_ARGS__, true, true><<<GRID, 256, 0, stream>>>(p, lanes2);           \
@@ -514,14 +729,6 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs p, int lanes2)
     KERNEL<__VA_ARGS__, false, true><<<GRID, 256, 0, stream>>>(p, lanes2);          \
   else                                                                              \
     KERNEL<__VA_ARGS__, false, false><<<GRID, 256, 0, stream>>>(p, lanes2)
-
-// log2 of the lanes that a group of `size` experts fills, -1 if it does not
-// fill whole lanes, a power of two of them.
-int group_lanes(int size, int V, int L) {
-  for (int n = 0; (1 << n) <= L; ++n)
-    if (size == V << n) return n;
-  return -1;
-}
 
 template <int L, int V>
 hipError_t launch_parts(const RouteArgs& p, bool f32, bool sigmoid, hipStream_t stream) {
@@ -540,12 +747,43 @@ hipError_t launch_wave(const RouteArgs& p, bool f32, bool sigmoid, hipStream_t s
   return hipGetLastError();
 }
 
+// From here on moe_route_many_kernel, us against a wave a token (bf16 logits of
+// 256 experts; fp32, sigmoid, 8 groups; fp32 logits of 128 experts):
+//   4096 tokens:  6.1 |  5.9   13.7 | 12.1    7.9 |  4.7
+//   8192          7.0 |  8.6   16.1 | 16.7    6.5 |  6.6
+//   16001         9.8 | 14.6   21.3 | 24.5    8.5 | 10.8
+//   40000        20.2 | 30.9   34.2 | 45.8   13.7 | 22.8
+// Few tokens leave no second wave to hide one token's 64-bit choice behind.  Up
+// to 64 experts, where moe_route_kernel has 16 lanes a token as well, it is the
+// faster without groups (16001 tokens: 5.4 | 4.8, with them 9.5 | 11.1).
+constexpr int64_t kManyTokens = 8192;
+
+template <int V>
+hipError_t launch_many(const RouteArgs& p, bool f32, bool sigmoid, hipStream_t stream) {
+  const int size = p.experts / p.groups;
+  const int lanes2 = p.groups > 1 ? group_lanes(size, 4, 16) : 0, wave2 = group_lanes(size, V / 4, 64);
+  const dim3 grid((unsigned)((p.tokens + 15) / 16));
+  if (sigmoid && f32)
+    moe_route_many_kernel<V, true, true><<<grid, 256, 0, stream>>>(p, lanes2, wave2);
+  else if (sigmoid)
+    moe_route_many_kernel<V, true, false><<<grid, 256, 0, stream>>>(p, lanes2, wave2);
+  else if (f32)
+    moe_route_many_kernel<V, false, true><<<grid, 256, 0, stream>>>(p, lanes2, wave2);
+  else
+    moe_route_many_kernel<V, false, false><<<grid, 256, 0, stream>>>(p, lanes2, wave2);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_moe_route(const RouteArgs& p, bool f32, bool sigmoid, hipStream_t stream) {
   // Lane j keeps round j's expert and lane g group g's score, so a token has
   // at least as many lanes as either.
   const int need = p.top_k > p.groups ? p.top_k : p.groups;
+  if (p.tokens >= kManyTokens && p.experts > 64 && p.experts <= 256 && many_fits(p, f32)) {
+    if (p.experts <= 128) return launch_many<8>(p, f32, sigmoid, stream);
+    return launch_many<16>(p, f32, sigmoid, stream);
+  }
   if (need <= 16 && p.experts <= 64) return launch_parts<16, 4>(p, f32, sigmoid, stream);
   if (p.experts <= 64) return launch_wave<1>(p, f32, sigmoid, stream);
   if (p.experts <= 128) return launch_wave<2>(p, f32, sigmoid, stream);

@@ -44,6 +44,48 @@ def test_route(E, k, groups, keep, gt, scoring, biased, dtype):
         _check(x, k, b, scoring=scoring, groups=groups, top_groups=keep, group_top=gt, renormalize=renorm, scale=2.5)
 
 
+@pytest.mark.parametrize("E,k,groups,keep,gt", [(8, 2, 1, 1, 2), (60, 4, 1, 1, 2), (64, 6, 8, 3, 2), (64, 15, 4, 2, 1),
+                                                (128, 8, 1, 1, 2), (128, 5, 16, 7, 2), (160, 6, 1, 1, 2),
+                                                (256, 8, 8, 4, 2), (256, 8, 16, 4, 1), (256, 15, 1, 1, 2),
+                                                (200, 6, 25, 4, 2), (252, 3, 1, 1, 2)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_tokens(E, k, groups, keep, gt, scoring, biased, dtype):
+    """The form of many tokens, on rows whose like are checked one by one above: the same rows in small calls."""
+    need_gpu()
+    x = _logits(8203, E, 11, dtype)
+    x[5] = -np.inf
+    x[6, k // 2:] = -np.inf
+    x[7, ::3] = np.nan
+    x[8, 1] = np.inf
+    x[9] = 1.0
+    b = _logits(1, E, 12, torch.float32, 0.1)[0] if biased else None
+    kw = dict(scoring=scoring, groups=groups, top_groups=keep, group_top=gt, scale=2.5)
+    for renorm in (True, False):
+        w, ids = mx.moe_route(x, k, b, renormalize=renorm, **kw)
+        parts = [mx.moe_route(p, k, b, renormalize=renorm, **kw) for p in x.split(2000)]
+        assert torch.equal(ids, torch.cat([q[1] for q in parts]))
+        assert torch.allclose(w, torch.cat([q[0] for q in parts]), rtol=2.0 ** -20, atol=1e-37)
+    rw, rids = D.route(x[:40].double().cpu().numpy(), k, None if b is None else b.double().cpu().numpy(), **kw)
+    assert np.array_equal(mx.moe_route(x, k, b, **kw)[1][:40].cpu().numpy(), rids)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_tokens_with_ties(scoring, biased, dtype):
+    need_gpu()
+    r = np.random.default_rng(15)
+    x = torch.from_numpy(r.integers(-3, 4, (8192, 256)).astype(np.float32) / 2).to(dtype).cuda()
+    b = torch.from_numpy(r.integers(-1, 2, 256).astype(np.float32) / 8).cuda() if biased else None
+    for groups, keep in ((1, 1), (8, 3)):
+        kw = dict(scoring=scoring, groups=groups, top_groups=keep)
+        ids = mx.moe_route(x, 8, b, **kw)[1].cpu().numpy()
+        ref = D.route(x[:200].double().cpu().numpy(), 8, None if b is None else b.double().cpu().numpy(), **kw)[1]
+        assert np.array_equal(ids[:200], ref)
+
+
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("biased", [False, True])
 def test_ties_masks_and_values_that_are_not_finite(scoring, biased):
