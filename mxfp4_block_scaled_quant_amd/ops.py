@@ -26,6 +26,12 @@ queries, and works with symbolic sizes.
         block_table, lengths, scale) -> (out, lse)
     torch.ops.mxfp4.mla_prefill(q, k_nope, k_pe, v, cu_q, cu_k, scale, causal)
         -> (out [Tq, H, dv], lse [Tq, H])
+    torch.ops.mxfp4.moe_route(logits, top_k, bias, scoring, groups, top_groups, group_top,
+        renormalize, scale) -> (weights [T, top_k], ids [T, top_k])
+    torch.ops.mxfp4.moe(x, ids, weights, up_w, up_ws, down_w, down_ws, experts, inner,
+        up_bias, down_bias, activation, gated, residual) -> [T, hidden]
+    torch.ops.mxfp4.linear_act(x, w_pre, ws_pre, N, bias, activation, gated, residual,
+        out_dtype) -> [M, N] ([M, N/2] gated)
 
 mla_cache_append writes the cache and q_out it is given; no other op mutates
 its inputs, and none has an autograd formula (the path is inference only).
@@ -39,9 +45,9 @@ import torch
 from torch import Tensor
 
 from . import (MXFP4_LAYOUT_GEMM, MXFP4_LAYOUT_ROWMAJOR, a16wfp4_bmm, mxfp4_gemm_a4w4,
-               mla_cache_append, mla_decode, mla_decode_shared_prefix, mla_prefill, mxfp4_gemm_a4w4_mxfp4_out,
-               mxfp4_linear, mxfp4_linear_prequantized, mxfp4_preshuffle_weight, mxfp4_quant_1x32,
-               mxfp4_shuffle_scales)
+               MXFP4Weight, mla_cache_append, mla_decode, mla_decode_shared_prefix, mla_prefill, moe_route,
+               mxfp4_gemm_a4w4_mxfp4_out, mxfp4_linear, mxfp4_linear_act, mxfp4_linear_prequantized, mxfp4_moe,
+               mxfp4_preshuffle_weight, mxfp4_quant_1x32, mxfp4_shuffle_scales)
 
 __all__ = ["gemm_data_bytes", "gemm_scale_bytes"]
 
@@ -217,3 +223,44 @@ def prefill(q: Tensor, k_nope: Tensor, k_pe: Tensor, v: Tensor, cu_q: Tensor, cu
 def _(q, k_nope, k_pe, v, cu_q, cu_k, scale, causal=True):
     T, H = q.shape[:2]
     return (q.new_empty((T, H, v.shape[2]), dtype=torch.bfloat16), q.new_empty((T, H), dtype=torch.float32))
+
+
+@torch.library.custom_op("mxfp4::moe_route", mutates_args=())
+def route(logits: Tensor, top_k: int, bias: Optional[Tensor] = None, scoring: str = "softmax", groups: int = 1,
+          top_groups: int = 1, group_top: int = 2, renormalize: bool = True,
+          scale: float = 1.0) -> Tuple[Tensor, Tensor]:
+    return moe_route(logits, top_k, bias, scoring, groups, top_groups, group_top, renormalize, scale)
+
+
+@route.register_fake
+def _(logits, top_k, bias=None, scoring="softmax", groups=1, top_groups=1, group_top=2, renormalize=True, scale=1.0):
+    T = logits.shape[0]
+    return logits.new_empty((T, top_k), dtype=torch.float32), logits.new_empty((T, top_k), dtype=torch.int32)
+
+
+@torch.library.custom_op("mxfp4::moe", mutates_args=())
+def moe(x: Tensor, ids: Tensor, weights: Tensor, up_w: Tensor, up_ws: Tensor, down_w: Tensor, down_ws: Tensor,
+        experts: int, inner: int, up_bias: Optional[Tensor] = None, down_bias: Optional[Tensor] = None,
+        activation: str = "silu", gated: bool = True, residual: Optional[Tensor] = None) -> Tensor:
+    hidden = x.shape[1]
+    up = MXFP4Weight(up_w, up_ws, 2 * inner if gated else inner, hidden, experts)
+    return mxfp4_moe(x, ids, weights, up, MXFP4Weight(down_w, down_ws, hidden, inner, experts), up_bias, down_bias,
+                     activation, gated, residual)
+
+
+@moe.register_fake
+def _(x, ids, weights, up_w, up_ws, down_w, down_ws, experts, inner, up_bias=None, down_bias=None, activation="silu",
+      gated=True, residual=None):
+    return x.new_empty((x.shape[0], x.shape[1]))
+
+
+@torch.library.custom_op("mxfp4::linear_act", mutates_args=())
+def linear_act(x: Tensor, w_pre: Tensor, ws_pre: Tensor, N: int, bias: Optional[Tensor] = None,
+               activation: str = "none", gated: bool = False, residual: Optional[Tensor] = None,
+               out_dtype: torch.dtype = torch.bfloat16) -> Tensor:
+    return mxfp4_linear_act(x, w_pre, ws_pre, N, bias, activation, gated, residual, out_dtype)
+
+
+@linear_act.register_fake
+def _(x, w_pre, ws_pre, N, bias=None, activation="none", gated=False, residual=None, out_dtype=torch.bfloat16):
+    return x.new_empty((x.shape[0], N // 2 if gated else N), dtype=out_dtype)
