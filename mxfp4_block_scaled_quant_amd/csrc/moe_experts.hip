@@ -647,7 +647,7 @@ __global__ __launch_bounds__(768) void moe_up_few_kernel(ProductArgs p, FewArgs 
     for (int u = 0; u < 4; ++u) af[u] = (int4){0, 0, 0, 0}, sa[u] = kE8M0One;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      if (q * 4 < blk.rows) {  // (uniform)
+      if (q * 4 >= blk.rows) continue;  // (uniform)
       if (q) load_x(token[q]);
       uint32_t b;
       const int4 code = quant_block32(xv, b);
@@ -660,7 +660,6 @@ __global__ __launch_bounds__(768) void moe_up_few_kernel(ProductArgs p, FewArgs 
         const uint32_t sc = (uint32_t)__builtin_amdgcn_ds_bpermute(src, (int)b);
         af[u] = {here ? v.x : af[u].x, here ? v.y : af[u].y, here ? v.z : af[u].z, here ? v.w : af[u].w};
         sa[u] = here ? sc : sa[u];
-      }
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -692,9 +691,9 @@ struct SumArgs {
   MoeArgs m;
   const MoeHead* head;
   const MoeBlock* blocks;
-  const int32_t *pos, *src;
+  const int32_t* src;
   const uint8_t *h, *hs;
-  int Kt, G, Ns;   // of the weights
+  int Kt, G, Ns;    // of the weights
   int shares, gps;  // shares of K, groups of one
 };
 constexpr int kSumWaves = 8;
@@ -808,7 +807,6 @@ hipError_t launch_down_sum(const MoeArgs& p, const MoeLayout& l, bool few, int64
   s.m = p;
   s.head = reinterpret_cast<const MoeHead*>(p.work + l.head);
   s.blocks = reinterpret_cast<const MoeBlock*>(p.work + l.blocks);
-  s.pos = reinterpret_cast<const int32_t*>(p.work + l.pos);
   s.src = reinterpret_cast<const int32_t*>(p.work + l.src);
   s.h = p.work + l.h, s.hs = p.work + l.hs;
   s.Kt = (int)cdiv(p.inner, 128), s.G = (int)cdiv(s.Kt, 4), s.Ns = p.hidden / 16;

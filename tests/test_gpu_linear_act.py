@@ -144,3 +144,18 @@ def test_captured(M):
         again = mx.mxfp4_linear_act(x, W.w_pre, W.ws_pre, N, None, "silu", True, r)
         torch.cuda.synchronize()
         assert torch.equal(out, again)
+
+
+def test_rows_past_32_bits():
+    """Outputs and residuals whose last rows lie past 4 GiB, in place."""
+    need_gpu()
+    M, N, K = 70000, 64, 32
+    W = mx.quantize_weight(dev_bf16(inputs.weights(N, K, 3)))
+    x = dev_bf16(inputs.activations(M, K, 4))
+    r = dev_bf16(inputs.activations(M, N // 2, 5))
+    want = mx.mxfp4_linear_act(x, W.w_pre, W.ws_pre, N, None, "silu", True, r)
+    wide = torch.empty((M, 40000), dtype=torch.bfloat16, device="cuda")
+    at = wide[:, 1024:1024 + N // 2]
+    at.copy_(r)
+    mx.mxfp4_linear_act(x, W.w_pre, W.ws_pre, N, None, "silu", True, at, out=at)
+    assert torch.equal(at, want)

@@ -167,3 +167,49 @@ def test_rows_between_the_products_are_the_library_s_quantisation():
     # (sums of the same products in another order: an ulp of bf16 in a few places)
     same = (host_bf16_bits(out) == host_bf16_bits(y)).mean()
     assert same > 0.99
+
+
+# On both sides of each change of form: pairs of one launch's sum (1024) and of
+# the plan for itself (64 of 4 tokens), chunks of the plan, mean rows of one
+# and of two row tiles, of the tiled kernels.
+@pytest.mark.parametrize("T,k,E,H,I", [(4, 16, 20, 96, 64), (4, 17, 20, 96, 64), (128, 8, 128, 64, 64), (129, 8, 128, 64, 96),
+                                       (1024, 1, 100, 64, 32), (1025, 1, 1024, 32, 32), (64, 16, 93, 96, 32),
+                                       (96, 1, 4, 64, 64), (100, 1, 4, 64, 64), (2100, 1, 1, 64, 64)])
+def test_borders_of_the_forms(T, k, E, H, I):
+    need_gpu()
+    p = problem(T, k, E, H, I, seed=21, residual=True, bias=True)
+    check(p, mx.mxfp4_moe(**device(p)))
+
+
+def test_rows_past_32_bits():
+    """Rows between the products of more than 4 GiB: the last tokens as in a call of their own."""
+    need_gpu()
+    T, k, E, H, I = 33000, 8, 8, 8320, 32
+    p = problem(400, k, E, H, I, seed=22, residual=True)
+    d = device(p)
+    few = mx.mxfp4_moe(**d)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    ids = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    w = torch.rand(T, k, generator=g, device="cuda")
+    x[-400:], ids[-400:], w[-400:] = d["x"], d["ids"], d["weights"]
+    out = torch.zeros_like(x)
+    out[-400:] = d["residual"]
+    mx.mxfp4_moe(x, ids, w, d["up"], d["down"], residual=out, out=out)
+    assert torch.equal(out[-400:], few)
+
+
+def test_two_calls_at_once():
+    need_gpu()
+    a, b = (device(problem(T, 4, 16, 512, 256, seed=23, residual=True)) for T in (150, 31))
+    want = mx.mxfp4_moe(**a), mx.mxfp4_moe(**b)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for s, d in zip(streams, (a, b)):
+            with torch.cuda.stream(s):
+                got.append(mx.mxfp4_moe(**d))
+    torch.cuda.synchronize()
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % 2])

@@ -197,3 +197,14 @@ def test_captured_and_on_another_stream():
         again = mx.moe_route(x, 8, b, **kw)
         torch.cuda.synchronize()
         assert torch.equal(w, again[0]) and torch.equal(ids, again[1])
+
+
+def test_rows_past_32_bits():
+    need_gpu()
+    T, E, k = 9000, 256, 8
+    x = _logits(T, E, 31, torch.bfloat16)
+    wide = torch.empty((T, 262144), dtype=torch.bfloat16, device="cuda")
+    wide[:, 128:128 + E] = x
+    for rows in (T, 8190):  # both forms
+        a, b = mx.moe_route(x[-rows:], k), mx.moe_route(wide[-rows:, 128:128 + E], k)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
