@@ -1205,7 +1205,16 @@ __device__ __forceinline__ void epilogue_part(const GemmArgs& p, const Tile& tl,
       top = fmaxf(fmaxf(top, fabsf(v[j][0])), fabsf(v[j][1]));
       top = fmaxf(fmaxf(top, fabsf(v[j][2])), fabsf(v[j][3]));
     }
-    const uint32_t e = max(row_max(__float_as_uint(top)) >> 23, 15u);
+    uint32_t most = row_max(__float_as_uint(top));
+    if (__any(most >= 0x7F800000u)) {  // an infinity has no part in the exponent: the columns beside it keep theirs
+      top = 0.f;
+#pragma unroll
+      for (int j = 0; j < kWN; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) top = fmaxf(top, fabsf(v[j][r]) < __builtin_huge_valf() ? fabsf(v[j][r]) : 0.f);
+      most = row_max(__float_as_uint(top));
+    }
+    const uint32_t e = max(most >> 23, 15u);
     const float f = __uint_as_float((268u - e) << 23);
 #pragma unroll
     for (int j = 0; j < kWN; ++j) {

@@ -213,3 +213,21 @@ def test_two_calls_at_once():
     torch.cuda.synchronize()
     for i, y in enumerate(got):
         assert torch.equal(y, want[i % 2])
+
+
+@pytest.mark.parametrize("T", [3, 40, 150])
+def test_an_infinite_column_leaves_the_others(T):
+    """A bias of +-inf or NaN in three columns: those are so, their neighbours are as without."""
+    need_gpu()
+    p = problem(T, 2, 4, 192, 64, seed=24, bias=True)
+    d = device(p)
+    at = [5, 70, 131]
+    for n in at:
+        p["down_bias"][:, n] = 0
+    d["down_bias"][:, at] = torch.tensor([float("inf"), float("-inf"), float("nan")], dtype=torch.bfloat16, device="cuda")
+    d["weights"].clamp_(min=0.125)
+    p["weights"] = d["weights"].cpu().numpy()
+    out = mx.mxfp4_moe(**d)
+    assert (out[:, 5] == float("inf")).all() and (out[:, 70] == float("-inf")).all() and out[:, 131].isnan().all()
+    out[:, at] = mx.mxfp4_moe(**{**d, "down_bias": dev_bf16(p["down_bias"])})[:, at]
+    check(p, out)
