@@ -231,3 +231,18 @@ def test_an_infinite_column_leaves_the_others(T):
     assert (out[:, 5] == float("inf")).all() and (out[:, 70] == float("-inf")).all() and out[:, 131].isnan().all()
     out[:, at] = mx.mxfp4_moe(**{**d, "down_bias": dev_bf16(p["down_bias"])})[:, at]
     check(p, out)
+
+
+@pytest.mark.parametrize("T,k,E", [(3, 2, 4), (40, 2, 16), (70, 4, 16), (150, 4, 16)])
+def test_a_token_that_is_not_finite_and_weights_outside(T, k, E):
+    """One token's infinities and NaN stay its own; the weight of an id outside is not read into the sum."""
+    need_gpu()
+    d = device(problem(T, k, E, 192, 64, seed=25, elsewhere=True))
+    want = mx.mxfp4_moe(**d)
+    outside = (d["ids"] < 0) | (d["ids"] >= E)
+    d["weights"][outside] = float("nan")
+    assert torch.equal(mx.mxfp4_moe(**d), want)
+    d["x"][1, 3], d["x"][1, 40] = float("inf"), float("nan")
+    out = mx.mxfp4_moe(**d)
+    rest = [t for t in range(T) if t != 1]
+    assert torch.equal(out[rest], want[rest])
