@@ -1460,6 +1460,14 @@ __global__ __launch_bounds__(512, 1) void MXFP4_PREFILL_KERNEL(GemmArgs p, int t
 
   for (int k = 0;;) {
     for (int g = c.g0; g < c.g1; ++g) group_body<MODE, kStores, kBiasLds>(p, P, c, cn, rc, rn, g, wv, wm, wn, ra, lane16);
+    // The fragments and scales read in the last group are not used (they are
+    // read again below), so the compiler takes their registers as free at once:
+    // hold them until the reads have landed, or a value that the epilogue puts
+    // there is overwritten by a read still under way.
+    wait_lgkm<0>(P.af[0], P.af[1], P.af[2], P.af[3]);
+    wait_lgkm<0>(P.af[4], P.af[5], P.af[6], P.af[7]);
+    wait_weights<0>(P.b0);
+    wait_lgkm_scales<0>(P.sa, P.sb);
     bool out = true;
     if constexpr (!is_group(MODE)) out = k >= s.nsk || sk_combine<kStores>(sk, s, P, wv);
     if (out) {

@@ -246,3 +246,13 @@ def test_a_token_that_is_not_finite_and_weights_outside(T, k, E):
     out = mx.mxfp4_moe(**d)
     rest = [t for t in range(T) if t != 1]
     assert torch.equal(out[rest], want[rest])
+
+
+def test_many_tiles_repeat_to_the_bit():
+    """Thousands of tiles, each after another's epilogue: equal in every run, and the token of each row its own."""
+    need_gpu()
+    d = device(problem(400, 8, 8, 1024, 512, seed=26, residual=True))
+    few = mx.mxfp4_moe(**d)
+    wide = {n: d[n].repeat(20, 1) for n in ("x", "ids", "weights", "residual")}
+    for _ in range(20):
+        assert torch.equal(mx.mxfp4_moe(**{**d, **wide}), few.repeat(20, 1))
