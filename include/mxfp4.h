@@ -504,9 +504,6 @@ int moe_route(const void* logits, int64_t ld, int logits_dtype, const void* bias
  * with Q the quantisation of mxfp4_quant_1x32, products and sums in fp32, the
  * sum in the order of j.  A choice whose id is outside [0, experts) (an
  * expert of another GPU, a token of padding) adds nothing.
- * Where an expert has more than 24 pairs on average, y waits for its sum in
- * fp16 beside one exponent per 64 columns: half a step is 2^-11 of a value,
- * and 2^-39 of the columns' largest for the smallest ones.
  *
  *   x         bf16 [tokens, hidden], row stride ldx (% 8), 16-byte aligned
  *   ids       int32, weights fp32 [tokens, top_k], row strides ldi and ldw

@@ -174,8 +174,7 @@ __device__ __forceinline__ v4f mfma_fp4v(v4i a, v4i b, uint32_t sa, uint32_t sb,
 //  kModeGroup  row tiles come from the plan's list, with their experts' weights
 //  kModeRows   (kModeGroup) rows gathered from tokens that are quantised row
 //              by row, MXFP4 output in the GEMM layouts
-//  kModePart   (kModeGroup) a pair's rows of the second product, as fp16 with
-//              one exponent per 64 columns
+//  kModePart   (kModeGroup) a pair's rows of the second product, in fp32
 constexpr int kModeAct = 8, kModeGated = 16, kModeGroup = 32, kModeRows = 64, kModePart = 128;
 constexpr bool is_act(int mode) { return (mode & kModeAct) != 0; }
 constexpr bool is_gated(int mode) { return (mode & kModeGated) != 0; }
@@ -460,6 +459,10 @@ template <int OFF>
 __device__ __forceinline__ void ds_write8(uint32_t addr, v2i v) {
   asm volatile("ds_write_b64 %0, %1 offset:%2" ::"v"(addr), "v"(v), "i"(OFF));
 }
+template <int OFF>
+__device__ __forceinline__ void ds_write16(uint32_t addr, v4i v) {
+  asm volatile("ds_write_b128 %0, %1 offset:%2" ::"v"(addr), "v"(v), "i"(OFF));
+}
 __device__ __forceinline__ void ds_write4(uint32_t addr, uint32_t v) {
   asm volatile("ds_write_b32 %0, %1" ::"v"(addr), "v"(v));
 }
@@ -700,10 +703,10 @@ struct OutMode {
   static constexpr bool kFp4 = kOut == 4;
   static constexpr bool kStaged = kOut == 0 || kOut == 4;
   static constexpr bool kVec = kOut == 2;
-  // per 16-row block: kWN / 2 row-piece stores (bf16), or as many code and
-  // as many scale stores (MXFP4)
+  // per 16-row block: kWN / 2 row-piece stores (bf16), twice as many of a
+  // pair's fp32 rows, or as many code and as many scale stores (MXFP4)
   static constexpr int kPieces = is_gated(MODE) ? 1 : kWN / 2;
-  static constexpr int kStores = is_part(MODE) ? (kPieces + 1) * kWM
+  static constexpr int kStores = is_part(MODE) ? 2 * kPieces * kWM
                                  : kOut == 0 ? kPieces * kWM
                                  : kFp4    ? 2 * kPieces * kWM
                                  : kVec    ? kWM * kOutWN<MODE>
@@ -1158,89 +1161,52 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Tile& tl, v4f 
   if (OM::kDrain) wait_vm<0>();
 }
 
-// The larger of a value and those of the lanes 16, 32 and 48 on (the lanes of
-// one row): swaps of neighbouring rows of 16 lanes, then of the halves.
-__device__ __forceinline__ uint32_t row_max(uint32_t v) {
-  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  v = max(a[0], a[1]);
-  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  return max(b[0], b[1]);
-}
-
-// A pair's row of the second product (kModePart), to be weighted and added up
-// by moe_combine_kernel: fp16 with one exponent per row and wave (64 columns),
-// the biased exponent E of the columns' largest magnitude, and v 2^(141 - E)
-// (below 2^15) rounded to fp16.  Half the bytes of fp32, which bound these
-// kernels, for an error of 2^-11 relative down to 2^-28 of the largest: an
-// eighth of the output's own bf16 rounding (bf16 here would add as much as that
-// rounding again).  (E >= 15, so that 2^(E - 141) is a normal number.)
+// A pair's row of the second product (kModePart), in fp32, to be weighted and
+// added up by moe_combine_kernel.  A wave's 64 columns of a 16-row block go
+// through its staging rows in two halves of 32, so that each store takes
+// whole 128-byte lines of eight rows, past the caches (kStagedStoreAux: the
+// rows of a long prompt outgrow every one of them).
 template <int MODE>
 __device__ __forceinline__ void epilogue_part(const GemmArgs& p, const Tile& tl, v4f (&acc)[kWM][kWN], int wv, int wm,
                                               int wn) {
   static_assert(kWN == 4, "64 columns a wave");
   const int lane = (int)lane_here();
   const int row0 = tl.ms * 16 + wm * 128;
-  const int n0 = (tl.s0 + wn * kWN) * 16;
-  const int n = n0 + (lane & 7) * 8;
+  const int n = (tl.s0 + wn * kWN) * 16 + (lane & 7) * 4;  // this lane's 4 stored columns of the first half
   v2i bl[kWN];
   read_bias(bl, wv, lane);
   const uint32_t wst = kEpiLds + (uint32_t)wv * 16 * kEpiRowB;
-  const uint32_t waddr = wst + (uint32_t)(lane & 15) * kEpiRowB + (uint32_t)(lane >> 4) * 8;
+  const uint32_t waddr = wst + (uint32_t)(lane & 15) * kEpiRowB + (uint32_t)(lane >> 4) * 16;
   const uint32_t raddr = wst + (uint32_t)(lane >> 3) * kEpiRowB + (uint32_t)(lane & 7) * 16;
-  const uint32_t voff = n < p.N ? (uint32_t)((lane >> 3) * p.N + n) * 2u : kOOB;
-  const uint32_t ldx = (uint32_t)((p.N + 63) >> 6);
-  const uint32_t xoff = lane < 16 && n0 < p.N ? (uint32_t)lane * ldx + (uint32_t)(n0 >> 6) : kOOB;
+  const uint32_t voff = (uint32_t)((lane >> 3) * p.N + n) * 4u;
   uint8_t* const out = reinterpret_cast<uint8_t*>(p.out);
 #pragma unroll
   for (int i = 0; i < kWM; ++i) {
-    float v[kWN][4];
-    float top = 0.f;
-#pragma unroll
-    for (int j = 0; j < kWN; ++j) {
-      float b[4];
-      bias_floats(bl[j], b);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) v[j][r] = acc[i][j][r] + b[r];
-      // (one three-way maximum of magnitudes per pair)
-      top = fmaxf(fmaxf(top, fabsf(v[j][0])), fabsf(v[j][1]));
-      top = fmaxf(fmaxf(top, fabsf(v[j][2])), fabsf(v[j][3]));
-    }
-    uint32_t most = row_max(__float_as_uint(top));
-    if (__any(most >= 0x7F800000u)) {  // an infinity has no part in the exponent: the columns beside it keep theirs
-      top = 0.f;
-#pragma unroll
-      for (int j = 0; j < kWN; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) top = fmaxf(top, fabsf(v[j][r]) < __builtin_huge_valf() ? fabsf(v[j][r]) : 0.f);
-      most = row_max(__float_as_uint(top));
-    }
-    const uint32_t e = max(most >> 23, 15u);
-    const float f = __uint_as_float((268u - e) << 23);
-#pragma unroll
-    for (int j = 0; j < kWN; ++j) {
-      typedef _Float16 v2h __attribute__((ext_vector_type(2)));
-      const v2h lo = {(_Float16)(v[j][0] * f), (_Float16)(v[j][1] * f)};
-      const v2h hi = {(_Float16)(v[j][2] * f), (_Float16)(v[j][3] * f)};
-      const v2i d = {__builtin_bit_cast(int, lo), __builtin_bit_cast(int, hi)};
-      if (j == 0) ds_write8<0>(waddr, d);
-      if (j == 1) ds_write8<32>(waddr, d);
-      if (j == 2) ds_write8<64>(waddr, d);
-      if (j == 3) ds_write8<96>(waddr, d);
-    }
-    v4i r0, r1;
-    ds_read16<0>(r0, raddr);
-    ds_read16<8 * kEpiRowB>(r1, raddr);
-    asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(r0), "+v"(r1));
     const int rb = row0 + i * 16;
     // (uniform: see epilogue_staged)
     const int nrows = __builtin_amdgcn_readfirstlane(max(0, min(16, row_end<MODE>(p, tl) - rb)));
-    const __amdgpu_buffer_rsrc_t ro = make_rsrc(out + (int64_t)rb * p.N * 2, (uint32_t)(nrows * p.N * 2));
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.out_scales + (int64_t)rb * ldx, (uint32_t)nrows * ldx);
-    // (whole lines, non-temporal: the rows of a long prompt outgrow every cache)
-    __builtin_amdgcn_raw_buffer_store_b128(r0, ro, voff, 0, kStagedStoreAux);
-    __builtin_amdgcn_raw_buffer_store_b128(r1, ro, n < p.N ? voff + (uint32_t)(8 * p.N) * 2u : kOOB, 0,
-                                           kStagedStoreAux);
-    __builtin_amdgcn_raw_buffer_store_b8((uint8_t)e, rx, xoff, 0, 0);
+    const __amdgpu_buffer_rsrc_t ro = make_rsrc(out + (int64_t)rb * p.N * 4, (uint32_t)(nrows * p.N * 4));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float b[4];
+        bias_floats(bl[2 * h + q], b);
+        v4i d;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) d[r] = (int)__float_as_uint(acc[i][2 * h + q][r] + b[r]);
+        if (q == 0) ds_write16<0>(waddr, d);
+        if (q == 1) ds_write16<64>(waddr, d);
+      }
+      v4i r0, r1;
+      ds_read16<0>(r0, raddr);
+      ds_read16<8 * kEpiRowB>(r1, raddr);
+      asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(r0), "+v"(r1));
+      const bool in = n + h * 32 < p.N;  // (N is a multiple of 32: a half is whole or absent)
+      __builtin_amdgcn_raw_buffer_store_b128(r0, ro, in ? voff + h * 128u : kOOB, 0, kStagedStoreAux);
+      __builtin_amdgcn_raw_buffer_store_b128(r1, ro, in ? voff + (uint32_t)(8 * p.N) * 4u + h * 128u : kOOB, 0,
+                                             kStagedStoreAux);
+    }
   }
 }
 
@@ -1509,7 +1475,7 @@ __global__ __launch_bounds__(512, 1) void MXFP4_PREFILL_KERNEL(GemmArgs p, int t
 
 #if MXFP4_PREFILL_FORM == 2
 // The experts' products on `grid` workgroups: rows for the second product
-// (rows_out), or a pair's rows (out, their exponents in out_scales).
+// (rows_out), or a pair's fp32 rows (out).
 hipError_t MXFP4_PREFILL_TILES(const GemmArgs& p, int grid, hipStream_t stream) {
   const SkArgs none = {0, 1, nullptr, nullptr, nullptr, nullptr};
   const int out_strips = p.gated ? p.Ns / 2 : p.Ns;

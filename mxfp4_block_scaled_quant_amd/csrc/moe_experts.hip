@@ -46,7 +46,7 @@ inline bool moe_tiles(int64_t pairs, int64_t experts) { return pairs / experts >
 // most as many strips as pairs, and 15 rows of padding per expert met.
 struct MoeLayout {
   int64_t strips, max_blocks;
-  size_t head, blocks, counts, pos, src, tok, a, as, h, hs, part, exps, total;
+  size_t head, blocks, counts, pos, src, tok, a, as, h, hs, part, total;
 };
 
 MoeLayout moe_layout(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, int64_t inner) {
@@ -72,8 +72,7 @@ MoeLayout moe_layout(int64_t tokens, int64_t top_k, int64_t experts, int64_t hid
   l.as = take(tokens * cdiv(kt1, 4) * 16);
   l.h = take(l.strips * kt2 * 1024);
   l.hs = take(l.strips * cdiv(kt2, 4) * 256);
-  l.part = take(l.strips * 16 * hidden * (moe_tiles(pairs, experts) ? 2 : 4));
-  l.exps = take(moe_tiles(pairs, experts) ? l.strips * 16 * cdiv(hidden, 64) : 0);
+  l.part = take(l.strips * 16 * hidden * 4);
   l.total = at;
   return l;
 }
@@ -838,34 +837,24 @@ hipError_t launch_tiles(const GemmArgs& p, int64_t max_blocks, hipStream_t strea
 
 // --------------------------------------------------------------- the combine
 
-// A token's rows, weighted and added in the order of its choices: 16 bytes of
-// each a thread (four fp32 columns, or eight of fp16 with an exponent per 64,
-// epilogue_part's), the rows of up to eight choices under way together.
-template <bool HALF>
-__global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs p, const int32_t* pos, const void* part,
-                                                          const uint8_t* exps) {
-  constexpr int kCols = HALF ? 8 : 4;
-  const int64_t pieces = p.hidden / kCols;
+// A token's rows, weighted and added in the order of its choices: four columns
+// a thread, the rows of up to eight choices under way together.
+__global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs p, const int32_t* pos, const float* part) {
+  const int64_t quads = p.hidden / 4;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= p.tokens * pieces) return;
-  const int64_t t = i / pieces;
-  const int n = (int)(i % pieces) * kCols;
-  float v[kCols];
+  if (i >= p.tokens * quads) return;
+  const int64_t t = i / quads;
+  const int n = (int)(i % quads) * 4;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
   if (p.residual) {
-    uint32_t r[kCols / 2];
-    __builtin_memcpy(r, __builtin_assume_aligned(p.residual + t * p.ldr + n, 8), kCols * 2);
-#pragma unroll
-    for (int q = 0; q < kCols / 2; ++q)
-      v[2 * q] = __uint_as_float(r[q] << 16), v[2 * q + 1] = __uint_as_float(r[q] & 0xFFFF0000u);
-  } else {
-#pragma unroll
-    for (int q = 0; q < kCols; ++q) v[q] = 0.f;
+    const uint2 r = *reinterpret_cast<const uint2*>(p.residual + t * p.ldr + n);
+    v[0] = __uint_as_float(r.x << 16), v[1] = __uint_as_float(r.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(r.y << 16), v[3] = __uint_as_float(r.y & 0xFFFF0000u);
   }
-  const int ldx = (p.hidden + 63) >> 6;
   for (int j0 = 0; j0 < p.top_k; j0 += 8) {
     int row[8];
     float w[8];
-    int4 y[8];
+    v4f y[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const bool in = j0 + j < p.top_k;
@@ -873,34 +862,19 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs p, const int32
       w[j] = in ? p.weights[t * p.ldw + j0 + j] : 0.f;
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (row[j] >= 0) {
-        y[j] = *reinterpret_cast<const int4*>(static_cast<const uint8_t*>(part) +
-                                              ((int64_t)row[j] * p.hidden + n) * (HALF ? 2 : 4));
-        if constexpr (HALF) w[j] *= __uint_as_float(((uint32_t)exps[(int64_t)row[j] * ldx + (n >> 6)] - 14u) << 23);
-      }
-    }
+    for (int j = 0; j < 8; ++j)
+      if (row[j] >= 0) y[j] = *reinterpret_cast<const v4f*>(part + (int64_t)row[j] * p.hidden + n);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (row[j] < 0) continue;
-      const int word[4] = {y[j].x, y[j].y, y[j].z, y[j].w};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if constexpr (HALF) {
-          typedef _Float16 v2h __attribute__((ext_vector_type(2)));
-          const v2h h = __builtin_bit_cast(v2h, word[q]);
-          v[2 * q] = fmaf(w[j], (float)h[0], v[2 * q]);
-          v[2 * q + 1] = fmaf(w[j], (float)h[1], v[2 * q + 1]);
-        } else {
-          v[q] = fmaf(w[j], __uint_as_float((uint32_t)word[q]), v[q]);
-        }
-      }
+      for (int q = 0; q < 4; ++q) v[q] = fmaf(w[j], y[j][q], v[q]);
     }
   }
-  uint32_t o[kCols / 2];
-#pragma unroll
-  for (int q = 0; q < kCols / 2; ++q) o[q] = pack_bf16x2(v[2 * q], v[2 * q + 1]);
-  __builtin_memcpy(__builtin_assume_aligned(p.out + t * p.ldo + n, 8), o, kCols * 2);
+  uint2 o;
+  o.x = pack_bf16x2(v[0], v[1]);
+  o.y = pack_bf16x2(v[2], v[3]);
+  *reinterpret_cast<uint2*>(p.out + t * p.ldo + n) = o;
 }
 
 }  // namespace
@@ -979,7 +953,7 @@ hipError_t launch_moe(const MoeArgs& p, hipStream_t stream) {
     d.a = p.work + l.h, d.as = p.work + l.hs, d.w = p.down, d.ws = p.down_scales, d.bias = p.down_bias;
     d.N = p.hidden, d.K = p.inner, d.Kt = kt2, d.G = g2, d.Ns = p.hidden / 16;
     d.w_expert = (int64_t)d.Ns * kt2 * 1024, d.ws_expert = (int64_t)d.Ns * g2 * 256;
-    d.out = part, d.out_scales = p.work + l.exps;
+    d.out = part;
     e = launch_tiles(d, max_blocks, stream);
     if (e != hipSuccess) return e;
   } else {
@@ -993,12 +967,7 @@ hipError_t launch_moe(const MoeArgs& p, hipStream_t stream) {
     e = mt == 1 ? launch_stream<1, 2, false>(d, max_blocks, stream) : launch_stream<2, 2, false>(d, max_blocks, stream);
     if (e != hipSuccess) return e;
   }
-  if (tiles)
-    moe_combine_kernel<true><<<dim3((unsigned)cdiv(p.tokens * (p.hidden / 8), 256)), 256, 0, stream>>>(
-        p, plan.pos, part, p.work + l.exps);
-  else
-    moe_combine_kernel<false><<<dim3((unsigned)cdiv(p.tokens * (p.hidden / 4), 256)), 256, 0, stream>>>(
-        p, plan.pos, part, nullptr);
+  moe_combine_kernel<<<dim3((unsigned)cdiv(p.tokens * (p.hidden / 4), 256)), 256, 0, stream>>>(p, plan.pos, part);
   return hipGetLastError();
 }
 
