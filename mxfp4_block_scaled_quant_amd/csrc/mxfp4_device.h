@@ -141,7 +141,8 @@ __device__ __forceinline__ int4 quant_block32(const int4 (&v)[4], uint32_t& b) {
 //  0  v, or max(v, 0)
 //  1  v times the sigmoid of a v (1 + b v^2): silu (1, 0) and gelu's tanh form
 //     (2 sqrt(2 / pi), 0.044715), through the power and reciprocal
-//     instructions (an ulp each)
+//     instructions (an ulp each).  The square stays finite: silu's b is 0,
+//     and 0 times the infinite square of a value past 2^64 would be NaN
 //  2  gelu: v/2 erfc(-v / sqrt 2), with erfc(z) = t exp(-z^2 + P(t)),
 //     t = 1 / (1 + z/2), z >= 0.  P, of degree 9, is a least-maximum fit of
 //     ln(exp(z^2) erfc(z) / t) over 0 <= z <= 23 in 64 bits (off by 7.2e-8),
@@ -154,12 +155,13 @@ __host__ __device__ __forceinline__ constexpr int act_class(int act) {
 template <int CLASS>
 __device__ __forceinline__ float activate_as(float v, int act) {
   constexpr float kLog2e = 1.44269504088896340736f;
+  constexpr float kLargest = 0x1.fffffep127f;
   if constexpr (CLASS == 0) {
     return !(v <= 0.f) || act == kActNone ? v : 0.f;
   } else if constexpr (CLASS == 1) {
     const float a = act == kActSilu ? -kLog2e : -1.59576912160573071176f * kLog2e;
     const float ab = act == kActSilu ? 0.f : -0.044715f * 1.59576912160573071176f * kLog2e;
-    return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * fmaf(ab, v * v, a)));
+    return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * fmaf(ab, fminf(v * v, kLargest), a)));
   } else {
     const float z = fabsf(v) * 0.70710678118654752440f;
     const float t = __builtin_amdgcn_rcpf(fmaf(0.5f, z, 1.f));
