@@ -176,7 +176,8 @@ __device__ __forceinline__ float activate_as(float v, int act) {
     q = fmaf(q, t, 1.44264585f);
     q = fmaf(q, t, -1.8257446f);
     const float h = 0.5f * t * __builtin_amdgcn_exp2f(fmaf(-kLog2e * z, z, q));
-    return v < 0.f ? v * h : fmaf(-v, h, v);
+    // (v bounded in the product: h is 0 for v = inf)
+    return v < 0.f ? v * h : fmaf(-fminf(v, kLargest), h, v);
   }
 }
 __device__ __forceinline__ float activate(float v, int act) {

@@ -17,7 +17,6 @@ from tests.test_gpu_moe import device, problem
 pytestmark = pytest.mark.gpu
 
 ACTS = ["none", "silu", "gelu", "gelu_tanh", "relu"]
-INFINITE = ["none", "silu", "gelu_tanh", "relu"]
 VALUES = [s * v for v in (0.0, 1.0, 2.0 ** 20, 2.0 ** 63, 1.8e19, 2.0 ** 65, 1e20, 2.0 ** 100, 3e38) for s in (1, -1)]
 
 
@@ -72,7 +71,7 @@ def test_large_values_of_the_linear(M, N, gates, path, act, dtype):
 
 
 @pytest.mark.parametrize("M,N,gates,path", FORMS)
-@pytest.mark.parametrize("act", INFINITE)
+@pytest.mark.parametrize("act", ACTS)
 def test_infinite_values_of_the_linear(M, N, gates, path, act):
     """+inf stays so; of -inf the formulas leave -inf, 0, or NaN (infinity over infinity, or times 0)."""
     need_gpu()
