@@ -40,6 +40,11 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // A softmax term is off by (|x - max| 2 + 2) 2^-23 relative, its sum by the
 // terms' error and one rounding per addition (at most 16 + 6): < 2.1e-6 of
 // s <= 1 each.
+// A group's score a + c of two terms is off by as much in all where each counts
+// with its own magnitude: base covers the two s, kMarginRel (|a| + |c|) both
+// terms' rounding, the sum's and that of the bounds below, 2^-24 each.  (|a + c|
+// in place of |a| + |c| would not do: the roundings stay where terms of large
+// biases of both signs cancel.)
 constexpr float kMarginSigmoid = 1.0e-6f;
 constexpr float kMarginSoftmax = 5.0e-6f;
 constexpr float kMarginRel = 2.5e-7f;
@@ -136,6 +141,25 @@ struct Lowest<double> {
   static constexpr double v = -__builtin_huge_val();
 };
 
+// A group's score in fp32 (-inf for a group without an available expert), and
+// what the exact one lies between.  a, c: its largest two (c = -inf: one term).
+// A sum past fp32 leaves the bound on its far side infinite.
+struct GroupScore {
+  float mine, low, high;
+};
+__device__ __forceinline__ GroupScore group_score(float a, float c, int group_top, float base) {
+  constexpr float kLow = -__builtin_huge_valf();
+  const bool two = group_top == 2 && c > kLow;
+  const float sum = two ? a + c : a;
+  const float off = base + kMarginRel * fabsf(a) + (two ? kMarginRel * fabsf(c) : 0.f);
+  GroupScore g;
+  const bool open = sum > kLow;
+  g.mine = open ? sum : kLow;
+  g.low = open ? fminf(sum, FLT_MAX) - off : kLow;
+  g.high = open ? sum + off : kLow;
+  return g;
+}
+
 // What the choice needs of the call, the same in every lane.
 struct Choice {
   int experts, top_k, groups, kept, group_top;
@@ -186,14 +210,26 @@ __device__ __forceinline__ int choose(const Choice& p, const float (&x)[V], cons
   if (p.groups > 1) {
     // every lane g < groups gets group g's score
     F mine = kLow;
+    float low = -__builtin_huge_valf(), high = low;
+    const auto score_of = [&](F a, F c) {
+      if constexpr (kFast) {
+        const GroupScore g = group_score(a, c, p.group_top, kBase);
+        mine = g.mine, low = g.low, high = g.high;
+      } else {
+        mine = (p.group_top == 2 && c > kLow) ? a + c : a;
+      }
+    };
     if (p.lanes2 >= 0) {
       F a = kLow, c = kLow;
 #pragma unroll
       for (int r = 0; r < V; ++r) merge2(a, c, key[r], kLow);
       merge_lanes<L>(a, c, p.lanes2);
-      const F score = (p.group_top == 2 && c > kLow) ? a + c : a;
-      mine = __shfl(score, (lane << p.lanes2) & (L - 1), L);
+      score_of(a, c);
+      const int from = (lane << p.lanes2) & (L - 1);
+      mine = __shfl(mine, from, L);
+      if constexpr (kFast) low = __shfl(low, from, L), high = __shfl(high, from, L);
     } else {
+      F a1 = kLow, c1 = kLow;
       for (int g = 0; g < p.groups; ++g) {
         F a = kLow, c = kLow;
 #pragma unroll
@@ -202,9 +238,9 @@ __device__ __forceinline__ int choose(const Choice& p, const float (&x)[V], cons
           merge2(a, c, (e >= g * p.size && e < (g + 1) * p.size) ? key[r] : kLow, kLow);
         }
         merge_lanes<L>(a, c, log2of(L));
-        const F score = (p.group_top == 2 && c > kLow) ? a + c : a;
-        if (lane == g) mine = score;
+        if (lane == g) a1 = a, c1 = c;
       }
+      score_of(a1, c1);
     }
     if (lane >= p.groups) mine = kLow;
     int ahead = 0;
@@ -214,10 +250,9 @@ __device__ __forceinline__ int choose(const Choice& p, const float (&x)[V], cons
     }
     const bool stays = lane < p.groups && ahead < p.kept && mine > kLow;
     if constexpr (kFast) {
-      const float lo = all_min<L>(stays ? mine : __builtin_huge_valf());
-      const float hi = all_max<L>(stays ? kLow : mine);
-      // (written so that inf - inf counts as too close)
-      if (hi > kLow && !(lo - hi > 2 * kBase + 2 * kMarginRel * fabsf(hi))) unsure = true;
+      const float lo = all_min<L>(stays ? low : __builtin_huge_valf());
+      const float hi = all_max<L>(!stays && mine > kLow ? high : kLow);
+      if (hi > kLow && !(lo > hi)) unsure = true;
     }
     const uint64_t votes = __ballot(stays);
     const uint64_t here = votes >> ((threadIdx.x & 63) & ~(L - 1));
@@ -334,18 +369,18 @@ __device__ __forceinline__ int choose_wave(const Choice& p, const float (&x)[V],
       a = fmaxf(a, key[r]);
     }
     merge_lanes<64>(a, c, p.lanes2);
-    const float mine = (p.group_top == 2 && c > kLow) ? a + c : a;
+    const GroupScore mine = group_score(a, c, p.group_top, kBase);
     // groups ahead of this lane's: for certain, and at most (its own among
     // them); between the two fp32 cannot tell
-    const float margin = 2 * kBase + 2 * kMarginRel * fabsf(mine);
     int certain = 0, most = 0;
     for (int g = 0; g < p.groups; ++g) {
-      const float other =
-          __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine), g << p.lanes2));
-      certain += other > mine + margin ? 1 : 0;
-      most += !(other < mine - margin) ? 1 : 0;  // (true for inf - inf)
+      const auto of = [&](float v) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), g << p.lanes2));
+      };
+      certain += of(mine.low) > mine.high ? 1 : 0;
+      most += !(of(mine.high) < mine.low) ? 1 : 0;
     }
-    const bool in = (lane >> p.lanes2) < p.groups && mine > kLow;
+    const bool in = (lane >> p.lanes2) < p.groups && mine.mine > kLow;
     const bool stays = in && most - 1 < p.kept;
     unsure = unsure || (in && !stays && certain < p.kept);
 #pragma unroll
@@ -499,7 +534,7 @@ template <int V, bool SIGMOID, bool F32>
 __global__ __launch_bounds__(256) void moe_route_many_kernel(RouteArgs p, int lanes2, int wave_lanes2) {
   constexpr float kLow = -__builtin_huge_valf();
   constexpr float kBase = SIGMOID ? kMarginSigmoid : kMarginSoftmax;
-  __shared__ float gscore[16][17];
+  __shared__ float glow[16][17], ghigh[16][17];
   __shared__ int won[16][17];
   const int lane = threadIdx.x & 15, slot = threadIdx.x >> 4;
   const int64_t token = (int64_t)blockIdx.x * 16 + slot;
@@ -568,7 +603,7 @@ __global__ __launch_bounds__(256) void moe_route_many_kernel(RouteArgs p, int la
   for (int c = 0; c < V / 4; ++c) in[c] = true;
   if (grouped) {
     // 2^lanes2 lanes hold a group's experts of register quad c
-    float mine[V / 4];
+    GroupScore mine[V / 4];
     const int per = 16 >> lanes2;  // groups of a quad
 #pragma unroll
     for (int c = 0; c < V / 4; ++c) {
@@ -579,24 +614,23 @@ __global__ __launch_bounds__(256) void moe_route_many_kernel(RouteArgs p, int la
         a = fmaxf(a, score[c * 4 + q]);
       }
       merge_lanes<16>(a, d, lanes2);
-      mine[c] = (p.group_top == 2 && d > kLow) ? a + d : a;
+      mine[c] = group_score(a, d, p.group_top, kBase);
       const int g = c * per + (lane >> lanes2);
-      if ((lane & ((1 << lanes2) - 1)) == 0 && g < p.groups) gscore[slot][g] = mine[c];
+      if ((lane & ((1 << lanes2) - 1)) == 0 && g < p.groups) glow[slot][g] = mine[c].low, ghigh[slot][g] = mine[c].high;
     }
     __syncthreads();
     int certain[V / 4] = {}, most[V / 4] = {};
     for (int g = 0; g < p.groups; ++g) {
-      const float other = gscore[slot][g];
+      const float low = glow[slot][g], high = ghigh[slot][g];
 #pragma unroll
       for (int c = 0; c < V / 4; ++c) {
-        const float margin = 2 * kBase + 2 * kMarginRel * fabsf(mine[c]);
-        certain[c] += other > mine[c] + margin ? 1 : 0;
-        most[c] += !(other < mine[c] - margin) ? 1 : 0;
+        certain[c] += low > mine[c].high ? 1 : 0;
+        most[c] += !(high < mine[c].low) ? 1 : 0;
       }
     }
 #pragma unroll
     for (int c = 0; c < V / 4; ++c) {
-      const bool there = c * per + (lane >> lanes2) < p.groups && mine[c] > kLow;
+      const bool there = c * per + (lane >> lanes2) < p.groups && mine[c].mine > kLow;
       in[c] = there && most[c] - 1 < p.kept;
       unsure = unsure || (there && !in[c] && certain[c] < p.kept);
     }
