@@ -143,7 +143,8 @@ struct Lowest<double> {
 
 // A group's score in fp32 (-inf for a group without an available expert), and
 // what the exact one lies between.  a, c: its largest two (c = -inf: one term).
-// A sum past fp32 leaves the bound on its far side infinite.
+// Sums past fp32 count as its largest number of that sign in `mine`, and leave
+// the bound on their far side infinite.
 struct GroupScore {
   float mine, low, high;
 };
@@ -153,10 +154,10 @@ __device__ __forceinline__ GroupScore group_score(float a, float c, int group_to
   const float sum = two ? a + c : a;
   const float off = base + kMarginRel * fabsf(a) + (two ? kMarginRel * fabsf(c) : 0.f);
   GroupScore g;
-  const bool open = sum > kLow;
-  g.mine = open ? sum : kLow;
+  const bool open = a > kLow;
+  g.mine = open ? fmaxf(sum, -FLT_MAX) : kLow;
   g.low = open ? fminf(sum, FLT_MAX) - off : kLow;
-  g.high = open ? sum + off : kLow;
+  g.high = open ? fmaxf(sum, -FLT_MAX) + off : kLow;
   return g;
 }
 

@@ -1,4 +1,4 @@
-"""The choice of groups where fp32 scores cannot tell them apart: cancelling biases, near ties."""
+"""The choice of groups where fp32 scores cannot tell them apart: cancelling biases, near ties, masks of the lowest value."""
 
 import numpy as np
 import pytest
@@ -9,6 +9,8 @@ from oracle import feedforward as D
 from tests.helpers import need_gpu
 
 pytestmark = pytest.mark.gpu
+
+LOWEST = float(np.finfo(np.float32).min)
 
 
 def _scores64(x, b, scoring):
@@ -79,3 +81,22 @@ def test_groups_whose_scores_are_less_than_an_ulp_apart(T, scoring, group_top):
     for b in ((r.integers(-2, 3, 128) * 2.0 ** -26).astype(np.float32), np.full(128, 0.25, np.float32)):
         for groups, keep in ((8, 2), (16, 5)):
             _same_choice(x, b, 8, scoring, groups, keep, group_top)
+
+
+@pytest.mark.parametrize("T,E,groups", [(40, 64, 8), (40, 60, 6), (40, 128, 16), (40, 256, 16), (8200, 128, 16)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_masks_of_the_lowest_value(T, E, groups, scoring, group_top):
+    """A bias of the type's lowest value is not -inf: its expert comes last, and two of them, whose sum is past fp32,
+    leave their group in the choice."""
+    need_gpu()
+    r = np.random.default_rng([9, E])
+    size = E // groups
+    x = r.standard_normal((T, E)).astype(np.float32)
+    b = np.full((groups, size), LOWEST, np.float32)
+    b[1], b[4] = 0, -np.inf                     # one group is open, one closed
+    assert (_same_choice(x, b.reshape(E), size + 1, scoring, groups, 2, group_top) >= 0).all()
+    b[3, 2] = 0.5                               # and one of a single expert
+    assert (_same_choice(x, b.reshape(E), size + 1, scoring, groups, 3, group_top) >= 0).all()
+    x[:, :size * 2] = LOWEST                    # and logits of it
+    _same_choice(x, b.reshape(E), size + 1, scoring, groups, 3, group_top)
