@@ -809,9 +809,10 @@ hipError_t launch_many(const RouteArgs& p, bool f32, bool sigmoid, hipStream_t s
   return hipGetLastError();
 }
 
-}  // namespace
+// The tokens of one launch: 64 lanes each stay below the 2^32 work items of a grid.
+constexpr int64_t kLaunchTokens = 1 << 25;
 
-hipError_t launch_moe_route(const RouteArgs& p, bool f32, bool sigmoid, hipStream_t stream) {
+hipError_t launch_tokens(const RouteArgs& p, bool f32, bool sigmoid, hipStream_t stream) {
   // Lane j keeps round j's expert and lane g group g's score, so a token has
   // at least as many lanes as either.
   const int need = p.top_k > p.groups ? p.top_k : p.groups;
@@ -825,6 +826,21 @@ hipError_t launch_moe_route(const RouteArgs& p, bool f32, bool sigmoid, hipStrea
   if (p.experts <= 256) return launch_wave<4>(p, f32, sigmoid, stream);
   if (p.experts <= 512) return launch_wave<8>(p, f32, sigmoid, stream);
   return launch_wave<16>(p, f32, sigmoid, stream);
+}
+
+}  // namespace
+
+hipError_t launch_moe_route(const RouteArgs& p, bool f32, bool sigmoid, hipStream_t stream) {
+  for (int64_t t = 0; t < p.tokens; t += kLaunchTokens) {
+    RouteArgs q = p;
+    q.tokens = p.tokens - t < kLaunchTokens ? p.tokens - t : kLaunchTokens;
+    q.logits = static_cast<const uint8_t*>(p.logits) + t * p.ld * (f32 ? 4 : 2);
+    q.weights = p.weights + t * p.ldw;
+    q.ids = p.ids + t * p.ldi;
+    const hipError_t e = launch_tokens(q, f32, sigmoid, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace mxfp4
