@@ -443,7 +443,7 @@ constexpr int stream_waves(int mt) { return mt == 1 ? 12 : 8; }
 template <int MT, int NS, bool UP>
 __global__ __launch_bounds__(64 * stream_waves(MT)) void moe_stream_kernel(ProductArgs p) {
   extern __shared__ float red[];
-  const int bi = (int)(blockIdx.x / (unsigned)p.cols), c = (int)(blockIdx.x % (unsigned)p.cols);
+  const int bi = blockIdx.y, c = blockIdx.x;
   if (bi >= p.head->blocks) return;
   const MoeBlock blk = p.blocks[bi];
   const int expert = __builtin_amdgcn_readfirstlane(blk.expert);
@@ -550,7 +550,10 @@ template <int MT, int NS, bool UP>
 hipError_t launch_stream(const ProductArgs& p, int64_t max_blocks, hipStream_t stream) {
   const int kw = p.G < stream_waves(MT) ? p.G : stream_waves(MT);
   const size_t lds = (size_t)MT * NS * 4 * kw * 64 * 4 + (UP ? MT * 16 * 32 * 2 : 0);
-  moe_stream_kernel<MT, NS, UP><<<dim3((unsigned)(max_blocks * p.cols)), 64 * kw, lds, stream>>>(p);
+  // (columns and blocks in two dimensions of the grid: a launch does no more
+  // than 2^32 work items of one; blocks are fewer than 2^12, kStreamRows rows of
+  // kMaxExperts experts at most)
+  moe_stream_kernel<MT, NS, UP><<<dim3((unsigned)p.cols, (unsigned)max_blocks), 64 * kw, lds, stream>>>(p);
   return hipGetLastError();
 }
 
