@@ -140,10 +140,16 @@ hipError_t launch_quant_1x32(const void* x, int64_t M, int64_t K, int64_t ldx, v
     // Four segments per wave where there are many: measured on MI355X,
     // M = 8192 x K = 5120 / 14336 21.9 / 53.4 -> 18.5 / 49.0 us; decode sizes
     // keep one per wave (M = 16: 2.0 us against 3.0).
-    if (waves >= 8192)
-      quant_1x32_rowmajor_kernel<4><<<dim3((unsigned)((waves + 15) / 16)), 256, 0, stream>>>(
-          (const uint16_t*)x, ldx, (int)M, (int)K, (uint8_t*)q, ldq, (uint8_t*)scales, segs);
-    else
+    if (waves >= 8192) {
+      // (rows of up to 2^26 segments a launch: one does no more than 2^32 work items)
+      const int64_t rows = (1 << 26) / segs;
+      for (int64_t r = 0; r < M; r += rows) {
+        const int64_t n = M - r < rows ? M - r : rows;
+        quant_1x32_rowmajor_kernel<4><<<dim3((unsigned)((n * segs + 15) / 16)), 256, 0, stream>>>(
+            (const uint16_t*)x + r * ldx, ldx, (int)n, (int)K, (uint8_t*)q + r * ldq, ldq,
+            (uint8_t*)scales + r * (K / 32), segs);
+      }
+    } else
       quant_1x32_rowmajor_kernel<1><<<dim3((unsigned)((waves + 3) / 4)), 256, 0, stream>>>(
           (const uint16_t*)x, ldx, (int)M, (int)K, (uint8_t*)q, ldq, (uint8_t*)scales, segs);
   } else {
