@@ -85,15 +85,21 @@ hipError_t launch_preshuffle_strided(const void* w_fp4, int64_t ldw, const void*
   const int Ns = (int)((N + 15) / 16);
   const int Kt = (int)((K + 127) / 128);
   const int G = (Kt + 3) / 4;
-  const int64_t slots = batch * Ns * (int64_t)Kt * 64;
-  const int64_t dwords = batch * Ns * (int64_t)G * 64;
+  const int64_t slots1 = Ns * (int64_t)Kt * 64, dwords1 = Ns * (int64_t)G * 64;  // of one batch entry
   if (w_fp4) {
-    const int64_t total = slots + dwords;
-    preshuffle_kernel<<<dim3((unsigned)((total + 255) / 256)), 256, 0, stream>>>(
-        (const uint8_t*)w_fp4, ldw, (const uint8_t*)w_scales, lds, (int)N, (int)K, (uint8_t*)w_out,
-        (uint8_t*)ws_out, Ns, Kt, G, slots, dwords);
+    // (entries of up to 2^30 threads a launch: one does no more than 2^32 work
+    // items; an entry has at most 2^28)
+    const int64_t most = (1 << 30) / (slots1 + dwords1);
+    for (int64_t b = 0; b < batch; b += most) {
+      const int64_t n = batch - b < most ? batch - b : most;
+      const int64_t slots = n * slots1, dwords = n * dwords1;
+      preshuffle_kernel<<<dim3((unsigned)((slots + dwords + 255) / 256)), 256, 0, stream>>>(
+          (const uint8_t*)w_fp4 + b * N * ldw, ldw, (const uint8_t*)w_scales + b * N * lds, lds, (int)N, (int)K,
+          (uint8_t*)w_out + b * slots1 * 16, (uint8_t*)ws_out + b * dwords1 * 4, Ns, Kt, G, slots, dwords);
+    }
     return hipGetLastError();
   }
+  const int64_t dwords = batch * dwords1;
   preshuffle_scale_kernel<<<dim3((unsigned)((dwords + 255) / 256)), 256, 0, stream>>>(
       (const uint8_t*)w_scales, lds, (int)N, (int)K, (uint8_t*)ws_out, Ns, G, dwords);
   return hipGetLastError();
