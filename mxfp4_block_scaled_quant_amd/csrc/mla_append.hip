@@ -111,9 +111,19 @@ __global__ __launch_bounds__(64 * kWaves) void mla_append_kernel(AppendArgs p) {
 }  // namespace
 
 hipError_t launch_mla_append(const AppendArgs& p, hipStream_t stream) {
-  const dim3 grid((unsigned)((p.T + kWaves - 1) / kWaves));
-  if (p.interleaved) mla_append_kernel<true><<<grid, 64 * kWaves, 0, stream>>>(p);
-  else mla_append_kernel<false><<<grid, 64 * kWaves, 0, stream>>>(p);
+  // (2^25 tokens a launch, a wave each: one does no more than 2^32 work items)
+  constexpr int64_t kTokens = 1 << 25;
+  for (int64_t t = 0; t < p.T; t += kTokens) {
+    AppendArgs a = p;
+    a.T = p.T - t < kTokens ? p.T - t : kTokens;
+    a.kv += t * p.ldkv;
+    a.positions += t;
+    a.slots += t;
+    if (p.q) a.q += t * p.sqt, a.q_out += t * p.sot;
+    const dim3 grid((unsigned)((a.T + kWaves - 1) / kWaves));
+    if (a.interleaved) mla_append_kernel<true><<<grid, 64 * kWaves, 0, stream>>>(a);
+    else mla_append_kernel<false><<<grid, 64 * kWaves, 0, stream>>>(a);
+  }
   return hipGetLastError();
 }
 

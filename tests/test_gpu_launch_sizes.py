@@ -38,3 +38,25 @@ def test_preshuffled_stacks():
     for got, ref in ((pw, rw), (ps, rs)):
         for part in got.view(batch, -1).split(4096):
             assert (part == ref.view(-1)).all()
+
+
+def test_appended_rows():
+    """A wave per token: all but the last few tokens' rows are padding."""
+    _room(110)
+    T, n = 2 ** 26 + 64, 96
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kv = torch.empty((T, 576), dtype=torch.bfloat16, device="cuda")
+    kv[-n:] = torch.randn((n, 576), generator=g, device="cuda").bfloat16()
+    q = torch.empty((T, 1, 64), dtype=torch.bfloat16, device="cuda")
+    q[-n:] = torch.randn((n, 1, 64), generator=g, device="cuda").bfloat16()
+    slots = torch.full((T,), -1, dtype=torch.int64, device="cuda")
+    slots[-n:] = torch.arange(n, device="cuda")
+    positions = torch.full((T,), 1 << 20, dtype=torch.int64, device="cuda")     # outside the table: nothing is written
+    positions[-n:] = torch.arange(n, device="cuda")
+    angles = torch.randn((n, 64), generator=g, device="cuda")
+    norm = torch.ones(512, dtype=torch.bfloat16, device="cuda")
+    cache, want = (torch.zeros((2, 64, 576), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    want_q = mx.mla_cache_append(kv[-n:], norm, want, slots[-n:], positions[-n:], angles, q[-n:])
+    got_q = mx.mla_cache_append(kv, norm, cache, slots, positions, angles, q)
+    assert torch.equal(cache, want) and torch.equal(got_q[-n:], want_q)
+    assert want.any()
