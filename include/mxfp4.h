@@ -445,7 +445,8 @@ int mla_decode_shared_prefix(const void* q, int64_t q_batch, int64_t q_token, in
  *   (dn, dv)  (128, 128) or (192, 256)
  *   cu_q, cu_k  int32 [B + 1], ascending, from 0 to Tq and Tk
  *   lse       fp32 [Tq, H] contiguous, or NULL
- *   Tq >= 0 and B >= 0 (0 enqueues nothing), H >= 1.
+ *   Tq >= 0 and B >= 0 (0 enqueues nothing), H >= 1,
+ *   (Tq / 128 + min(Tq, B)) * H < 2^24.
  */
 int mla_prefill(const void* q, int64_t q_token, int64_t q_head, const void* k_nope,
                 int64_t k_token, int64_t k_head, const void* k_pe, int64_t pe_token,

@@ -246,6 +246,8 @@ int mla_prefill(const void* q, int64_t q_token, int64_t q_head, const void* k_no
   if (B < 0 || B > (1 << 24) || H < 1 || H > (1 << 16) || Tq < 0 || Tk < 0 || Tq > kMaxTokens || Tk > kMaxTokens ||
       (Tq / 64 + (Tq < B ? Tq : B)) * H > kMaxInt)
     return MXFP4_ERR_SHAPE;
+  // 256 threads a block of 128 query rows and head: a launch does no more than 2^32 work items
+  if ((Tq / 128 + (Tq < B ? Tq : B)) * H >= (1 << 24)) return MXFP4_ERR_SHAPE;
   q_token = used(q_token, Tq), out_token = used(out_token, Tq);
   k_token = used(k_token, Tk), pe_token = used(pe_token, Tk), v_token = used(v_token, Tk);
   q_head = used(q_head, H), k_head = used(k_head, H), v_head = used(v_head, H), out_head = used(out_head, H);
