@@ -324,6 +324,8 @@ int mxfp4_linear_prequantized(const void* x_fp4, int64_t ldq, const void* x_scal
  *          and som >= (B-1)*sob + N (a stride of a size-1 dimension is
  *          free); otherwise MXFP4_ERR_SHAPE.
  *   B >= 1, M >= 0 (M == 0 enqueues nothing), N >= 1, K > 0, K % 32 == 0.
+ *   Sizes that one launch cannot do (2^30 rows, or about 2^28 columns of the
+ *   B matrices together) return MXFP4_ERR_LAUNCH and write nothing.
  */
 int a16wfp4_bmm(const void* x, int64_t sxb, int64_t sxm,
                 const void* w_pre, const void* ws_pre,

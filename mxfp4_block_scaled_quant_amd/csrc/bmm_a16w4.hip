@@ -604,6 +604,8 @@ hipError_t launch_bmm_a16w4(const void* x, int64_t sxb, int64_t sxm, const void*
     // vector mode: whole 16-byte pieces of output rows
     const int per = 16 / esz;
     const bool vec = N % per == 0 && som % per == 0 && sob % per == 0 && ((uintptr_t)out & 15) == 0;
+    // (a launch does no more than 2^32 work items; of more it would leave a part out)
+    if (B * S * NB > 0xFFFFFFFFll / (64 * kWavesS)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)(B * S * NB)), block(64 * kWavesS);
 #define MXFP4_BMM_LAUNCH_NS(KF_, NT_, NS_)                                                                      \
   do {                                                                                                          \
@@ -632,6 +634,7 @@ hipError_t launch_bmm_a16w4(const void* x, int64_t sxb, int64_t sxm, const void*
   }
 
   constexpr int MTW = 4, NTW = 2;
+  if ((M + MTW * 16 - 1) / (MTW * 16) > 0xFFFFFFFFll / 256) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)((M + MTW * 16 - 1) / (MTW * 16)),
                   (unsigned)((N + 4 * NTW * 16 - 1) / (4 * NTW * 16)), (unsigned)B);
   bmm_a16w4_kernel<MTW, NTW><<<grid, 256, 0, stream>>>(p);

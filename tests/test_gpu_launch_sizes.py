@@ -60,3 +60,13 @@ def test_appended_rows():
     got_q = mx.mla_cache_append(kv, norm, cache, slots, positions, angles, q)
     assert torch.equal(cache, want) and torch.equal(got_q[-n:], want_q)
     assert want.any()
+
+
+def test_a_batched_product_of_too_many_columns_is_refused():
+    _room(70)
+    B, M, N, K = 16, 64, 2 ** 24 + 4096, 32
+    w = torch.empty((mx.weight_bytes(B, N, K),), dtype=torch.uint8, device="cuda")
+    s = torch.empty((mx.weight_scale_bytes(B, N, K),), dtype=torch.uint8, device="cuda")
+    x = torch.zeros((B, M, K), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(Exception, match="a16wfp4_bmm"):
+        mx.a16wfp4_bmm(x, w, s, N)
