@@ -462,7 +462,9 @@ int mla_prefill(const void* q, int64_t q_token, int64_t q_head, const void* k_no
  * there is one row. ---- */
 
 /* Activations of an epilogue: v; v / (1 + exp(-v)); v/2 (1 + erf(v / sqrt 2));
- * v/2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))); max(v, 0). */
+ * v/2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))); max(v, 0).  Right over the
+ * whole range of fp32, +inf included; -inf gives 0 in the last, and in the
+ * three before it the formulas' infinity times 0, NaN. */
 enum {
   MXFP4_ACT_NONE = 0,
   MXFP4_ACT_SILU = 1,

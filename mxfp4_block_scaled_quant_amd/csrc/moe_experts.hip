@@ -36,9 +36,11 @@ constexpr int kChunk = 1024;  // pairs that one workgroup counts
 // Mean rows of an expert up to which its weights are streamed into registers,
 // once per block of one or two 16-row tiles; with more the products run on
 // tiles of 256 rows.  Measured (us, streamed / tiles; experts, choices, hidden,
-// inner): 64, 8, 5120, 1024 with mean 12.5 133 / 153, 20 159 / 161, 25 (four
-// row tiles) 195 / 164; 128, 8, 2048, 768 with mean 16 89 / 117, 24 99 / 121,
-// 32 193 / 123; 32, 4, 5120, 1504 with mean 20 121 / 135, 25 154 / 137.
+// inner): 64, 8, 5120, 1024 with mean 12.5 124 / 140, 20 148 / 148, 25
+// 158 / 150; 128, 8, 2048, 768 with mean 16 85 / 115, 24 96 / 118, 32
+// 110 / 122; 32, 4, 5120, 1504 with mean 20 111 / 128, 25 119 / 129.  (The
+// first, with the most weights, decides; the mean counts pairs whose expert is
+// elsewhere too, since the host sees no ids.)
 constexpr int64_t kStreamRows = 24;
 inline bool moe_tiles(int64_t pairs, int64_t experts) { return pairs / experts > kStreamRows; }
 

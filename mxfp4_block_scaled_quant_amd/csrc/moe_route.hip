@@ -528,8 +528,11 @@ __device__ __forceinline__ void sort_down(int (&k)[V]) {
 // by themselves keep all their bits above the expert's number.  Where two keys
 // next to each other are too close for what they leave out, or two lanes
 // have the same key, the wave chooses that token's experts again in 64 bits.
-// Bound by its vector instructions: 16001 tokens of 256 fp32 logits in 8 groups
-// take 21.3 us, 17.4 MB at 0.8 TB/s (kManyTokens has the wave per token's).
+// 16001 tokens of 256 fp32 logits in 8 groups take 22 us, 17.4 MB at 0.8 TB/s
+// (kManyTokens has the wave per token's): about half of it is vector
+// instructions (1490 a wave, 4 cycles each, four waves a SIMD), the rest waits:
+// the waves, all resident in one round, meet at two barriers, and the fourth
+// of a wave whose token is chosen again holds up the others.
 constexpr int kGone = (int)0x80000000u;
 template <int V, bool SIGMOID, bool F32>
 __global__ __launch_bounds__(256) void moe_route_many_kernel(RouteArgs p, int lanes2, int wave_lanes2) {
@@ -784,10 +787,10 @@ hipError_t launch_wave(const RouteArgs& p, bool f32, bool sigmoid, hipStream_t s
 
 // From here on moe_route_many_kernel, us against a wave a token (bf16 logits of
 // 256 experts; fp32, sigmoid, 8 groups; fp32 logits of 128 experts):
-//   4096 tokens:  6.1 |  5.9   13.7 | 12.1    7.9 |  4.7
-//   8192          7.0 |  8.6   16.1 | 16.7    6.5 |  6.6
-//   16001         9.8 | 14.6   21.3 | 24.5    8.5 | 10.8
-//   40000        20.2 | 30.9   34.2 | 45.8   13.7 | 22.8
+//   4096 tokens:  6.2 |  6.0   15.9 | 13.6    6.8 |  4.8
+//   8192          7.0 |  8.6   17.1 | 16.4    7.0 |  6.7
+//   16001         9.5 | 14.1   21.9 | 24.6    8.2 | 10.6
+//   40000        21.0 | 31.1   35.7 | 47.8   15.3 | 22.9
 // Few tokens leave no second wave to hide one token's 64-bit choice behind.  Up
 // to 64 experts, where moe_route_kernel has 16 lanes a token as well, it is the
 // faster without groups (16001 tokens: 5.4 | 4.8, with them 9.5 | 11.1).

@@ -144,7 +144,8 @@ __device__ __forceinline__ int4 quant_block32(const int4 (&v)[4], uint32_t& b) {
 //     instructions (an ulp each).  The square stays finite: silu's b is 0,
 //     and 0 times the infinite square of a value past 2^64 would be NaN
 //  2  gelu: v/2 erfc(-v / sqrt 2), with erfc(z) = t exp(-z^2 + P(t)),
-//     t = 1 / (1 + z/2), z >= 0.  P, of degree 9, is a least-maximum fit of
+//     t = 1 / (1 + z/2), z >= 0: the form of Press et al., Numerical Recipes,
+//     section 6.2.  P, of degree 9, is a least-maximum fit made for this of
 //     ln(exp(z^2) erfc(z) / t) over 0 <= z <= 23 in 64 bits (off by 7.2e-8),
 //     its coefficients here times log2(e).  The exponent's own rounding
 //     leaves 2.5e-6 relative at |v| = 5 and 7e-6 at 8.

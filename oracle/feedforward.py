@@ -148,9 +148,10 @@ def moe(x_bf16, ids, weights, up, down, up_bias=None, down_bias=None, act="silu"
     """up, down: (qw [E, N, K/2], sw [E, N, K/32]); weights fp64.  (out fp64, bound before the cast).
 
     half: a looser bound, which the library's fp32 rows do not need: a choice's
-    row may be held in fp16 with one exponent per 64 columns before it is weighted, its largest magnitude scaled into [2^14, 2^15):
-    fp16 keeps 11 bits, so a value is half a step off, 2^-11 of itself, down to
-    fp16's smallest normal number 2^-14, which is 2^-28 of the largest at
+    row may be held in fp16 with one exponent per 64 columns before it is
+    weighted, its largest magnitude scaled into [2^14, 2^15): fp16 keeps 11
+    bits, so a value is half a step off, 2^-11 of itself, down to fp16's
+    smallest normal number 2^-14, which is 2^-28 of the largest at
     least; below that half a step is 2^-25, 2^-39 of the largest."""
     x = dequantised(x_bf16)
     T, k = ids.shape
